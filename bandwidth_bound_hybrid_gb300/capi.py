@@ -97,6 +97,9 @@ SIGNATURES = {
     "hy_op_attention_workspace": (sz, [i32, i32, i32, i32]),
     "hy_op_attention": (ctypes.c_int, [vp, vp, vp, i32, i32, i32, i32, vp, vp, i32, vp, vp, vp]),
     "hy_op_attention_noalloc": (ctypes.c_int, [vp, vp, vp, i32, i32, i32, i32, vp, vp, i32, vp, vp]),
+    "hy_op_attention_q4_workspace": (sz, [i32, i32, i32, i32]),
+    "hy_op_attention_q4": (ctypes.c_int, [vp, i32, i32, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, i32, vp, vp, vp]),
+    "hy_op_kv_append_q4": (ctypes.c_int, [vp, i32, i32, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp]),
     "hy_op_attention_i8": (ctypes.c_int, [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, i32, vp, vp, vp]),
 }
 

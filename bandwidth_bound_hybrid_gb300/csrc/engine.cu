@@ -59,6 +59,7 @@ int ensure_init(int dev) {
   HY_CK(bgemv::init());
   HY_CK(gemm::init());
   HY_CK(prefill::init());
+  HY_CK(kv4::init());
   g_inited[dev] = true;
   return HY_OK;
 }
@@ -220,7 +221,10 @@ float* conv_state(hy_cache* c, int seq, int gi) {
   const hy_model* m = c->m;
   return reinterpret_cast<float*>(c->mem[seq] + c->off_conv) + (size_t)gi * m->cfg.conv_k * m->CC;
 }
-// Scale row stride of an int8 cache (a multiple of 4, so that every kv
+// Score factor of the 4-bit attention: its softmax works in powers of two.
+float kv4_scale(int hd) { return (float)(1.4426950408889634 / sqrt((double)hd)); }
+
+// Scale row stride of an int8 or 4-bit cache (a multiple of 4, so that every kv
 // head's scales start 16-byte aligned).
 int cap_scales(int cap) { return (cap + 3) & ~3; }
 
@@ -2146,6 +2150,95 @@ int hy_op_attention_i8(const float* y_dev, void* Kq_dev, float* Ks_dev, void* Vq
   a.guard = guard;
   cudaError_t e = attn::launch(a, (cudaStream_t)stream, false);
   if (e != cudaSuccess) return fail(HY_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
+  return HY_OK;
+}
+
+// Checks that hy_op_attention_q4 and hy_op_kv_append_q4 share.
+static int check_q4_cache(const void* K, const void* Ks, const void* V, const void* Vs, int32_t cap, int32_t nq,
+                          int32_t nkv, int32_t hd) {
+  if (!aligned16(K) || !aligned16(Ks) || !aligned16(V) || !aligned16(Vs) || cap <= 0 || nkv <= 0 || nq <= 0 || nq % nkv)
+    return fail(HY_ERR_ARG, "bad 4-bit cache arguments");
+  if ((hd != 64 && hd != 128 && hd != 256) || nq / nkv > 8 || ((nq / nkv) & (nq / nkv - 1)) || nkv > 1024)
+    return fail(HY_ERR_UNSUPPORTED, "4-bit cache: head_dim 64/128/256, nq/nkv in {1,2,4,8}, nkv <= 1024");
+  return HY_OK;
+}
+
+size_t hy_op_attention_q4_workspace(int32_t batch, int32_t nq, int32_t nkv, int32_t hd) {
+  if (batch < 1 || batch > kv4::kMaxB || nkv <= 0 || nq <= 0 || nq % nkv || hd <= 0) return 0;
+  return ((size_t)batch * nkv * 4 + 255) / 256 * 256 + kv4::part_floats(nq, nkv, hd, op_nsm()) * 4;
+}
+
+int hy_op_attention_q4(const float* y_dev, int32_t ldy, int32_t batch, void* Kq_dev, void* Ks_dev, void* Vq_dev,
+                       void* Vs_dev, int32_t cap, int32_t nq, int32_t nkv, int32_t hd, const int32_t* len_dev,
+                       const float* rope_table_dev, float* o_dev, int32_t ldo, float* kv_new_dev, void* workspace_dev,
+                       void* stream) {
+  int rc = check_q4_cache(Kq_dev, Ks_dev, Vq_dev, Vs_dev, cap, nq, nkv, hd);
+  if (rc != HY_OK) return rc;
+  if (!y_dev || !len_dev || !rope_table_dev || !o_dev || !aligned16(workspace_dev) || batch < 1 ||
+      batch > kv4::kMaxB || (long long)ldy < ((long long)nq + 2 * nkv) * hd || (long long)ldo < (long long)nq * hd)
+    return fail(HY_ERR_ARG, "bad 4-bit attention arguments (batch 1..%d, ldy >= (nq + 2 nkv) hd, ldo >= nq hd)",
+                kv4::kMaxB);
+  unsigned* guard = nullptr;
+  if ((rc = op_guard(&guard)) != HY_OK) return rc;
+  kv4::Params a;
+  memset(&a, 0, sizeof(a));
+  a.y = y_dev;
+  a.ld_y = ldy;
+  a.o = o_dev;
+  a.ld_o = ldo;
+  a.kv_new = kv_new_dev;
+  a.rope = (const float2*)rope_table_dev;
+  a.nq = nq;
+  a.nkv = nkv;
+  a.nb = batch;
+  a.scale_log2e = kv4_scale(hd);
+  a.counter = (unsigned*)workspace_dev;
+  a.part = (float*)((uint8_t*)workspace_dev + ((size_t)batch * nkv * 4 + 255) / 256 * 256);
+  a.guard = guard;
+  for (int b = 0; b < batch; ++b) {
+    const size_t row = (size_t)b * nkv * cap, row_s = (size_t)b * nkv * cap_scales(cap);
+    a.K[b] = (uint8_t*)Kq_dev + row * (hd / 2);
+    a.V[b] = (uint8_t*)Vq_dev + row * (hd / 2);
+    a.Ks[b] = (uint16_t*)Ks_dev + row_s * (hd / 32);
+    a.Vs[b] = (uint16_t*)Vs_dev + row_s * (hd / 32);
+    a.len[b] = len_dev + b;
+    a.cap[b] = cap;
+  }
+  cudaError_t e = kv4::launch(a, hd, op_nsm(), (cudaStream_t)stream, false);
+  if (e != cudaSuccess) return fail(HY_ERR_CUDA, "4-bit attention launch: %s", cudaGetErrorString(e));
+  return HY_OK;
+}
+
+int hy_op_kv_append_q4(const float* y_dev, int32_t ldy, int32_t n, void* Kq_dev, void* Ks_dev, void* Vq_dev,
+                       void* Vs_dev, int32_t cap, int32_t nq, int32_t nkv, int32_t hd, const int32_t* len_dev,
+                       const float* rope_table_dev, float* kv_new_dev, void* stream) {
+  int rc = check_q4_cache(Kq_dev, Ks_dev, Vq_dev, Vs_dev, cap, nq, nkv, hd);
+  if (rc != HY_OK) return rc;
+  if ((n > 0 && !y_dev) || !len_dev || !rope_table_dev || n < 0 ||
+      (long long)ldy < ((long long)nq + 2 * nkv) * hd)
+    return fail(HY_ERR_ARG, "bad 4-bit append arguments (ldy >= (nq + 2 nkv) hd)");
+  if (n > cap) return fail(HY_ERR_CAPACITY, "%d rows exceed the capacity %d", n, cap);
+  if (n == 0) return HY_OK;
+  unsigned* guard = nullptr;
+  if ((rc = op_guard(&guard)) != HY_OK) return rc;
+  kv4::AppendParams a;
+  memset(&a, 0, sizeof(a));
+  a.y = y_dev;
+  a.ld_y = ldy;
+  a.n = n;
+  a.K = (uint8_t*)Kq_dev;
+  a.V = (uint8_t*)Vq_dev;
+  a.Ks = (uint16_t*)Ks_dev;
+  a.Vs = (uint16_t*)Vs_dev;
+  a.cap = cap;
+  a.nq = nq;
+  a.nkv = nkv;
+  a.len = len_dev;
+  a.rope = (const float2*)rope_table_dev;
+  a.kv_new = kv_new_dev;
+  a.guard = guard;
+  cudaError_t e = kv4::append(a, hd, (cudaStream_t)stream);
+  if (e != cudaSuccess) return fail(HY_ERR_CUDA, "4-bit append launch: %s", cudaGetErrorString(e));
   return HY_OK;
 }
 

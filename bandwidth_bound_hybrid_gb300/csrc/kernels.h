@@ -193,6 +193,53 @@ cudaError_t launch(const Params& p, cudaStream_t st, bool pdl);
 cudaError_t rope_table(float2* tab, int cap, int hd, double theta, cudaStream_t st);
 }  // namespace attn
 
+// ---------------------------------------------------------------- 4-bit KV cache
+// Decode attention over a cache of 4-bit codes with an fp16 scale per block
+// of 32, one token for each of up to kMaxB sequences, and the quantising
+// append of prompt rows (kv4.cu).
+namespace kv4 {
+constexpr int kMaxB = 8;
+struct Params {
+  const float* y;          // projection outputs q|k|v of the batch [nb][ld_y]
+  int ld_y;
+  float* o;                // [nb][ld_o]
+  int ld_o;
+  float* kv_new;           // values of the appended rows [nb][2][nkv][hd] (nullable)
+  const float2* rope;      // (cos, sin) [>= every cap][hd/2]
+  int nq, nkv, nb;
+  float scale_log2e;       // log2(e) / sqrt(hd)
+  float* part;             // part_floats() floats
+  unsigned* counter;       // [nb * nkv], zero between launches
+  unsigned* guard;
+  int min_tiles;           // set by launch(): fewest tiles of a CTA
+  // per sequence: codes [nkv][cap][hd/2], scales [nkv][cap rounded up to 4][hd/32], position of the new row
+  uint8_t* K[kMaxB];
+  uint8_t* V[kMaxB];
+  uint16_t* Ks[kMaxB];
+  uint16_t* Vs[kMaxB];
+  const int* len[kMaxB];
+  int cap[kMaxB];
+};
+struct AppendParams {
+  const float* y;          // projection rows q|k|v [n][ld_y]
+  long long ld_y;
+  int n;
+  uint8_t* K;
+  uint8_t* V;
+  uint16_t* Ks;
+  uint16_t* Vs;
+  int cap, nq, nkv;
+  const int* len;          // position of the first row
+  const float2* rope;
+  float* kv_new;           // [n][2][nkv][hd] (nullable)
+  unsigned* guard;
+};
+size_t part_floats(int nq, int nkv, int hd, int nsm);
+cudaError_t init();
+cudaError_t launch(const Params& p, int hd, int nsm, cudaStream_t st, bool pdl);
+cudaError_t append(const AppendParams& p, int hd, cudaStream_t st);
+}  // namespace kv4
+
 // ---------------------------------------------------------------- batched GEMV
 // Up to kMaxB token vectors through one weight stream (tensor-core MMA), bf16
 // or 4-bit block weights.

@@ -406,6 +406,45 @@ int hy_op_attention_i8(const float* y_dev, void* Kq_dev, float* Ks_dev, void* Vq
                        int32_t nq, int32_t nkv, int32_t hd, const int32_t* len_dev, const float* rope_table_dev,
                        int32_t nsplit, float* o_dev, void* workspace_dev, void* stream);
 
+/* Decode attention over a 4-bit cache, one token for each of `batch` (1..8)
+ * sequences.  A cached vector of hd values is hd / 32 blocks of 32, each with
+ * codes c in [-7, 7] and one fp16 scale s: value = s * c.  Kq_dev, Vq_dev:
+ * packed codes [batch][nkv][cap][hd/2] (byte i of a block's 16 holds c + 8 of
+ * element i in its low nibble and of element i + 16 in its high nibble, the
+ * layout of the 4-bit weights); Ks_dev, Vs_dev: scales
+ * [batch][nkv][cap4][hd/32], cap4 = cap rounded up to a multiple of 4 (all
+ * four 16-byte aligned).  y_dev [batch][ldy] are the projection outputs q|k|v
+ * before RoPE, o_dev [batch][ldo] the outputs [nq*hd] of each sequence.
+ * Sequence b: rotates q and the new k at position T = len_dev[b], quantises
+ * the new k and v, appends them at row T, and attends over rows [0, T] as
+ * stored.  The rule, in FP32 with each operation rounded on its own: k from
+ * RoPE (x0 cos - x1 sin, x1 cos + x0 sin); per block s = fp16(min(max |x| * r,
+ * 65504)) with r = 1/7 rounded to FP32, c = round-half-even(x * (1 / s))
+ * clamped to [-7, 7] (s = 0: c = 0). An infinity or NaN makes its block's
+ * scale NaN, so that it is not lost.  kv_new_dev (nullable) receives the
+ * values that the appended rows stand for, FP32 [batch][2][nkv][hd] (k, then
+ * v).  A sequence whose T is negative or at or past cap is left as it was, its
+ * o and kv_new unwritten (HY_GUARD_BAD_POSITION); the others run.
+ * rope_table_dev has at least cap rows.  The work is shared over the GPU by
+ * cached rows whatever the mix of lengths.  workspace_dev:
+ * hy_op_attention_q4_workspace() bytes, zeroed before its first use and then
+ * passed unmodified to later calls; calls that can overlap on the GPU need a
+ * workspace each. */
+size_t hy_op_attention_q4_workspace(int32_t batch, int32_t nq, int32_t nkv, int32_t hd);
+int hy_op_attention_q4(const float* y_dev, int32_t ldy, int32_t batch, void* Kq_dev, void* Ks_dev, void* Vq_dev,
+                       void* Vs_dev, int32_t cap, int32_t nq, int32_t nkv, int32_t hd, const int32_t* len_dev,
+                       const float* rope_table_dev, float* o_dev, int32_t ldo, float* kv_new_dev, void* workspace_dev,
+                       void* stream);
+/* The k and v of n tokens of one sequence (projection rows y_dev [n][ldy],
+ * q|k|v before RoPE; a prompt) rotated, quantised by the same rule and
+ * written at rows [T, T + n), T = *len_dev, of its 4-bit cache ([nkv][cap]...
+ * as above).  kv_new_dev: nullable, [n][2][nkv][hd].  HY_ERR_CAPACITY if n
+ * exceeds cap; with T negative or T + n past cap nothing is written
+ * (HY_GUARD_BAD_POSITION).  n = 0 does nothing. */
+int hy_op_kv_append_q4(const float* y_dev, int32_t ldy, int32_t n, void* Kq_dev, void* Ks_dev, void* Vq_dev,
+                       void* Vs_dev, int32_t cap, int32_t nq, int32_t nkv, int32_t hd, const int32_t* len_dev,
+                       const float* rope_table_dev, float* kv_new_dev, void* stream);
+
 /* hy_op_attention without a caller-provided workspace, for callers that
  * cannot allocate device memory: a host framework that owns the whole memory
  * budget through its own pool, a latency path where an allocation and the
