@@ -2165,7 +2165,8 @@ static int check_q4_cache(const void* K, const void* Ks, const void* V, const vo
 
 size_t hy_op_attention_q4_workspace(int32_t batch, int32_t nq, int32_t nkv, int32_t hd) {
   if (batch < 1 || batch > kv4::kMaxB || nkv <= 0 || nq <= 0 || nq % nkv || hd <= 0) return 0;
-  return ((size_t)batch * nkv * 4 + 255) / 256 * 256 + kv4::part_floats(nq, nkv, hd, op_nsm()) * 4;
+  if ((hd != 64 && hd != 128 && hd != 256) || nq / nkv > 8 || ((nq / nkv) & (nq / nkv - 1))) return 0;
+  return (kv4::counters(batch, nkv) * 4 + 255) / 256 * 256 + kv4::part_floats(nq, nkv, hd, op_nsm()) * 4;
 }
 
 int hy_op_attention_q4(const float* y_dev, int32_t ldy, int32_t batch, void* Kq_dev, void* Ks_dev, void* Vq_dev,
@@ -2193,7 +2194,7 @@ int hy_op_attention_q4(const float* y_dev, int32_t ldy, int32_t batch, void* Kq_
   a.nb = batch;
   a.scale_log2e = kv4_scale(hd);
   a.counter = (unsigned*)workspace_dev;
-  a.part = (float*)((uint8_t*)workspace_dev + ((size_t)batch * nkv * 4 + 255) / 256 * 256);
+  a.part = (float*)((uint8_t*)workspace_dev + (kv4::counters(batch, nkv) * 4 + 255) / 256 * 256);
   a.guard = guard;
   for (int b = 0; b < batch; ++b) {
     const size_t row = (size_t)b * nkv * cap, row_s = (size_t)b * nkv * cap_scales(cap);

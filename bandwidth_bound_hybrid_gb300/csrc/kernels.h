@@ -209,9 +209,8 @@ struct Params {
   int nq, nkv, nb;
   float scale_log2e;       // log2(e) / sqrt(hd)
   float* part;             // part_floats() floats
-  unsigned* counter;       // [nb * nkv], zero between launches
+  unsigned* counter;       // counters(nb, nkv), zero between launches
   unsigned* guard;
-  int min_tiles;           // set by launch(): fewest tiles of a CTA
   // per sequence: codes [nkv][cap][hd/2], scales [nkv][cap rounded up to 4][hd/32], position of the new row
   uint8_t* K[kMaxB];
   uint8_t* V[kMaxB];
@@ -235,6 +234,7 @@ struct AppendParams {
   unsigned* guard;
 };
 size_t part_floats(int nq, int nkv, int hd, int nsm);
+size_t counters(int nb, int nkv);
 cudaError_t init();
 cudaError_t launch(const Params& p, int hd, int nsm, cudaStream_t st, bool pdl);
 cudaError_t append(const AppendParams& p, int hd, cudaStream_t st);

@@ -20,14 +20,18 @@
 // shared memory, so this uses mma.sync, whose operands are widened in
 // registers.
 //
-// Work split: the cached rows of every (sequence, kv head) are cut into tiles
-// of 32 rows, all tiles form one list, and every CTA takes an equal
-// contiguous span of it, whatever the mix of lengths.  In a CTA each warp
-// takes every 8th tile of the span through its own cp.async ring and keeps
-// its own running maximum, sum and outputs (no block barrier inside a span).
+// Work split: the cached rows of every (sequence, kv head) are cut into tiles,
+// and in a CTA each warp takes every W-th tile of the CTA's range through its
+// own cp.async ring and keeps its own running maximum, sum and outputs (no
+// block barrier inside a range).  A CTA gets one range of at most m tiles of
+// one (sequence, head), m the least for which the CTAs suffice; where that
+// leaves much more than an equal share (more heads than CTAs, a few long
+// contexts each), all tiles form one list instead and every CTA takes an
+// equal span of it, its ends moved to a nearby border between heads.
 // An (sequence, head) that several CTAs share is joined from their partials
 //   R = max_i r_i,  o = sum_i 2^(r_i - R) o_i / sum_i 2^(r_i - R) l_i
-// by the last of them to arrive.
+// without any CTA waiting: the last of each 16 sharers to arrive joins the 16,
+// and the last of those joins the rest.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -37,36 +41,57 @@ namespace hy {
 namespace kv4 {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 32;  // rows of a warp's tile
-
+// Per head dim: warps of a CTA and CTAs per SM, rows of a warp's tile, and the
+// stages of its ring.  At hd 256 the 64 output accumulators of a lane leave no
+// room for more than 12 warps an SM, and tiles of 16 rows keep the rest small.
 template <int HD>
 struct Shape {
+  static constexpr int W = HD == 256 ? 12 : 8;
+  static constexpr int kThreads = W * 32;
+  static constexpr int kCtas = HD == 256 ? 1 : 2;    // per SM
+  static constexpr int TR = HD == 256 ? 16 : 32;     // rows of a tile
+  static constexpr int S = HD == 64 ? 4 : HD == 128 ? 2 : 3;
   static constexpr int NB = HD / 32;                 // blocks of a row
-  static constexpr int kCodes = kTile * HD / 2;      // bytes of a tile's K or V codes
-  static constexpr int kScales = kTile * NB * 2;     // and of their scales
-  static constexpr int kStage = 2 * (kCodes + kScales);
-  static constexpr int S = HD == 64 ? 4 : 2;         // ring stages of a warp
-  static constexpr int kMinCtas = HD == 256 ? 1 : 2; // CTAs per SM
-  static constexpr int kRing = kWarps * S * kStage;
-  static constexpr int kQ = NB * 32 * 8 * 4;         // query operand fragments
+  static constexpr int kCodes = TR * HD / 2;         // bytes of a tile's K or V codes
+  static constexpr int kScales = TR * NB * 2;        // and of their scales
+  static constexpr int kKV = kCodes + kScales;
+  static constexpr int kStage = 2 * kKV;
+  static constexpr int kWarpRing = S * kStage;
+  static constexpr int kRing = W * kWarpRing;
+  static constexpr int kQ = NB * 2 * 32 * 4 * 4;     // query operand fragments (two of them for 8 heads)
 };
 
 struct alignas(16) Small {
   float nk[256], nv[256];          // the new row before quantisation
   uint8_t codes[2][128];           // and its codes and scales
   uint16_t scales[2][8];
+  uint32_t amax[8][4];             // per head and pair of blocks: largest |q| (bits)
   float qf[8];                     // per head: 2^-e of the query normalisation
-  float qb[8][8];                  // per block and head: start value of the score accumulator
-  float r[kWarps][8], l[kWarps][8];
+  float2 qb[8][4];                 // per block and column pair: -8 sum q of the block
+  float r[12][8], l[12][8];
   int last;
+  // the work (set by warp 0, so that no warp holds it over its tiles)
+  int T[kMaxB];                    // positions of the new rows (-1: refused)
+  int at[kMaxB + 1];               // first unit of each sequence: tiles (spans) or ranges
+  int m;                           // most tiles of a range; 0: spans
+  int q, rem, near;
+  int unit, unit_end;              // this CTA's units
+  int b, g, first, end, tile0, ntile, next;  // the item and this CTA's range of it
+  int c_lo, np, slot0;             // the CTAs that share the item
+  const uint8_t *Kc, *Vc, *Ksc, *Vsc;        // its cache rows
 };
 
 template <int HD>
 constexpr size_t smem_bytes() {
   return (size_t)Shape<HD>::kRing + Shape<HD>::kQ + sizeof(Small);
 }
+
+constexpr int kJoin = 16;       // partials joined at a time
+constexpr int kCounters = 32;   // of a (sequence, kv head): the last join's, then one per 16 sharers
+// floats of a partial: outputs [G][HD], references [G], sums [G], in 16-byte pieces
+__host__ __device__ constexpr int part_size(int G, int HD) { return (G * (HD + 2) + 3) / 4 * 4; }
+// floats of a head's outputs in shared memory: padded, so that a quad's heads fall in different banks
+__host__ __device__ constexpr int out_pitch(int HD) { return HD + 8; }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -83,10 +108,39 @@ __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t b
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
   return r;
 }
+// The nibbles n of two 16-bit halves as fp16 pairs, without arithmetic: a
+// nibble in the low bits of a half is the subnormal n 2^-24 (h[0], h[1]: of the
+// low and the high byte), one above it n 2^-20 (h[2], h[3]).
+__device__ __forceinline__ void nibbles(uint32_t w, uint32_t* h) {
+  const uint32_t w8 = w >> 8;
+  h[0] = w & 0x000f000fu;
+  h[1] = w8 & 0x000f000fu;
+  h[2] = w & 0x00f000f0u;
+  h[3] = w8 & 0x00f000f0u;
+}
+// The codes n - 8 themselves, in the same order: 1024 + n - 1032 and (1024 + 16 n) / 16 - 72.
+__device__ __forceinline__ void codes(uint32_t w, uint32_t* v) {
+  const __half2 k1032 = u2h(0x64086408u), k16th = u2h(0x2c002c00u), k72 = u2h(0xd480d480u);
+  const uint32_t w8 = w >> 8;
+  v[0] = h2u(__hsub2(u2h(and_or(w, 0x000f000fu, 0x64006400u)), k1032));
+  v[1] = h2u(__hsub2(u2h(and_or(w8, 0x000f000fu, 0x64006400u)), k1032));
+  v[2] = h2u(__hfma2(u2h(and_or(w, 0x00f000f0u, 0x64006400u)), k16th, k72));
+  v[3] = h2u(__hfma2(u2h(and_or(w8, 0x00f000f0u, 0x64006400u)), k16th, k72));
+}
+// v truncated to fp16's 11 significant bits: v - trunc11(v) is exact
+__device__ __forceinline__ float trunc11(float v) { return __uint_as_float(__float_as_uint(v) & 0xffffe000u); }
 
+// d = a b + c
+__device__ __forceinline__ void mma_c(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
 __device__ __forceinline__ void mma(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -102,6 +156,12 @@ __device__ __forceinline__ void ldsm4t(uint32_t* w, uint32_t addr) {
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                : "r"(addr)
                : "memory");
+}
+// transpose of an 8 x 8 matrix of halves held as mma fragments
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
@@ -160,212 +220,471 @@ __device__ __forceinline__ void store_block(uint16_t s, int code, uint8_t* codes
 // (x0, x1) of a rotate-half pair, each product and sum rounded on its own, so
 // that a code never depends on how the compiler contracts them.
 __device__ __forceinline__ void rotate(float x0, float x1, float2 cs, float* r0, float* r1) {
-  *r0 = __fsub_rn(__fmul_rn(x0, cs.x), __fmul_rn(x1, cs.y));
+  *r0 = __fsub_rn(__fmul_rn(x0, cs.x), __fmul_rn(x1, cs.y));  // (x0, x1 are copies: r0, r1 may be their origin)
   *r1 = __fadd_rn(__fmul_rn(x1, cs.x), __fmul_rn(x0, cs.y));
 }
 
 // ------------------------------------------------------------ attention
+// The work is a list of units: per sequence b (n_b = T_b / TR + 1 tiles, none
+// when its position is refused), head by head, ceil(n_b / m) ranges of
+// about equal length a head, a CTA each; or (m = 0) the tiles themselves, in
+// spans: CTA c begins at tile c q + min(c, rem) (q = total / CTAs, rem = total %
+// CTAs), moved to the border of an item that is within `near` tiles (near <=
+// q / 4, so that the order of the CTAs stays).  The launch refuses caches of
+// more than 2^30 tiles.  These run in warp 0, all lanes alike unless said.
 struct Item {
-  int b, g, T;           // sequence, kv head, position of the new row
-  long long first, end;  // its tiles in the list
+  int b, g, first, end;  // sequence, kv head, its units in the list
 };
+__device__ __forceinline__ Item item_at(const Params& p, const Small& sm, int t) {
+  const int lane = threadIdx.x & 31;
+  const int b = __ffs(__ballot_sync(0xffffffffu, lane < p.nb && t < sm.at[lane < p.nb ? lane + 1 : 0])) - 1;
+  const int n = (sm.at[b + 1] - sm.at[b]) / p.nkv;
+  const int g = (int)((unsigned)(t - sm.at[b]) / (unsigned)n);
+  return {b, g, sm.at[b] + g * n, sm.at[b] + g * n + n};
+}
+__device__ __forceinline__ int span_first(const Params& p, const Small& sm, unsigned c) {
+  if (c == 0) return 0;
+  if (c >= gridDim.x) return sm.at[p.nb];
+  const int t = (int)(c * sm.q + min(c, (unsigned)sm.rem));
+  const Item it = item_at(p, sm, t);
+  return it.end - t <= sm.near ? it.end : t - it.first <= sm.near ? it.first : t;
+}
+// The CTA whose span, before its ends are moved, holds tile t (0 for t < 0).
+__device__ __forceinline__ int span_of(const Small& sm, int t) {
+  if (t < 0) return 0;
+  const unsigned q = sm.q, rem = sm.rem, big = rem * (q + 1);
+  return (int)((unsigned)t < big ? t / (q + 1) : rem + (t - big) / q);
+}
 
-// The tile list: sequence b has nkv * n_b tiles, n_b = T_b / 32 + 1 (0 when its
-// position is refused), head by head.
-struct List {
-  int T[kMaxB];
-  long long total;
-};
-
-__device__ __forceinline__ List tile_list(const Params& p) {
-  List L;
-  L.total = 0;
+// Lengths, the list and this CTA's units.
+template <int TR, int W>
+__device__ __forceinline__ void plan_work(const Params& p, Small& sm) {
+  const int lane = threadIdx.x & 31;
+  int T = -1;
+  if (lane < p.nb) {  // lengths: written only by the previous step's last kernel
+    T = *p.len[lane];
+    if (T < 0 || T >= p.cap[lane]) {
+      if (blockIdx.x == 0) set_guard(p.guard, kGuardBadPosition);
+      T = -1;
+    }
+    sm.T[lane] = T;
+  }
+  const int n = T < 0 ? 0 : T / TR + 1;  // tiles of a head of sequence `lane`
+  const int total = p.nkv * (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
+  const int items = p.nkv * __popc(__ballot_sync(0xffffffffu, n > 0));
+  const int grid = gridDim.x;
+  // least m: 32 candidates from an equal share (at least a tile per warp) up
+  // to total / (grid - items), which always suffices, a candidate a lane
+  int m = 0;
+  if (items <= grid) {
+    const int lo = max(W, (total + grid - 1) / grid);
+    const int hi = max(lo, items < grid ? (total + grid - items - 1) / (grid - items) : total);
+    const int mine = lane < 31 ? lo + (int)((long long)(hi - lo) * lane / 31) : hi;
+    int ranges = 0;
+    for (int b = 0; b < p.nb; ++b) {
+      const int nb = __shfl_sync(0xffffffffu, n, b);
+      ranges += (int)((unsigned)(nb + mine - 1) / (unsigned)mine);
+    }
+    const unsigned fits = __ballot_sync(0xffffffffu, p.nkv * ranges <= grid);
+    m = fits ? __shfl_sync(0xffffffffu, mine, __ffs(fits) - 1) : 0;
+    // a second range costs a CTA about what three tiles of every warp do
+    if (m > lo + 3 * W) m = 0;
+  }
+  int units = p.nkv * (m ? (n + m - 1) / m : n), incl = units;
 #pragma unroll
-  for (int b = 0; b < kMaxB; ++b) {
-    int T = -1;
-    if (b < p.nb) {
-      T = *p.len[b];
-      if (T < 0 || T >= p.cap[b]) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) set_guard(p.guard, kGuardBadPosition);
-        T = -1;
+  for (int o = 1; o < kMaxB; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 0) {
+    sm.at[0] = 0;
+    sm.m = m;
+    sm.q = total / grid;
+    sm.rem = total % grid;
+    sm.near = min(sm.q / 4, 2 * W);
+  }
+  if (lane < kMaxB) sm.at[lane + 1] = incl;
+  __syncwarp();
+  const int c = blockIdx.x, all = sm.at[p.nb];
+  const int u0 = all == 0 ? 0 : m ? min(c, all) : span_first(p, sm, c);
+  const int u1 = all == 0 ? 0 : m ? min(c + 1, all) : span_first(p, sm, c + 1);
+  if (lane == 0) {
+    sm.unit = u0;
+    sm.unit_end = u1;
+  }
+}
+
+// The range of this CTA that begins at unit t < unit_end, and where its rows are.
+template <int HD, int TR>
+__device__ __forceinline__ void set_range(const Params& p, Small& sm, int t) {
+  const Item it = item_at(p, sm, t);
+  const int n = sm.T[it.b] / TR + 1, parts = it.end - it.first, k = t - it.first;
+  const int end = min(it.end, sm.unit_end);
+  if ((threadIdx.x & 31) == 0) {
+    sm.b = it.b;
+    sm.g = it.g;
+    sm.first = it.first;
+    sm.end = it.end;
+    if (sm.m) {
+      const int t0 = (int)((long long)k * n / parts), t1 = (int)((long long)(k + 1) * n / parts);
+      sm.tile0 = t0;
+      sm.ntile = t1 - t0;
+    } else {
+      sm.tile0 = k;
+      sm.ntile = end - t;
+    }
+    sm.next = end;
+    const long long cap = p.cap[it.b], cap_s = (cap + 3) & ~3ll;
+    sm.Kc = p.K[it.b] + it.g * cap * (HD / 2);
+    sm.Vc = p.V[it.b] + it.g * cap * (HD / 2);
+    sm.Ksc = reinterpret_cast<const uint8_t*>(p.Ks[it.b] + it.g * cap_s * (HD / 32));
+    sm.Vsc = reinterpret_cast<const uint8_t*>(p.Vs[it.b] + it.g * cap_s * (HD / 32));
+  }
+}
+
+// The CTAs that share the item: those of the first and last tile that begin in it after moving.
+__device__ __forceinline__ void set_sharers(const Params& p, Small& sm) {
+  int c_lo = sm.first, np = sm.end - sm.first, slot0 = 0;
+  if (!sm.m) {
+    // of the unmoved begins, those past `in` go to the item's end, those up to `lo` to or before its first tile
+    const int in = sm.end - sm.near - 1 >= sm.first ? sm.end - sm.near - 1 : sm.first - 1;
+    const int lo = min(sm.first + sm.near, in);
+    c_lo = span_of(sm, lo);
+    np = span_of(sm, in) - c_lo + 1;
+    slot0 = span_first(p, sm, c_lo) != sm.first;  // the first sharer's span began before the item
+  }
+  if ((threadIdx.x & 31) == 0) {
+    sm.c_lo = c_lo;
+    sm.np = np;
+    sm.slot0 = slot0;
+  }
+}
+
+// The queries of the item as MMA operands, and the new row if the range ends with it.
+template <int HD, int G>
+__device__ __forceinline__ void prepare(const Params& p, Small& sm, uint32_t* qfrag) {
+  using Sh = Shape<HD>;
+  constexpr int NB = Sh::NB, TR = Sh::TR, W = Sh::W, NH = G == 8 ? 2 : 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = sm.b, g = sm.g, T = sm.T[b], tile0 = sm.tile0, ntile = sm.ntile;
+  const float* y = p.y + (long long)b * p.ld_y;
+  const float2* rope = p.rope + (long long)T * (HD / 2);
+  const bool has_new = tile0 + ntile == T / TR + 1;
+  // queries: a warp takes blocks c and c + NB / 2 of a head (the halves of its rotate-half pairs)
+  constexpr int NU = G * NB / 2, UW = (NU + W - 1) / W;
+  float x[UW][2];
+  float2 cs[UW];
+#pragma unroll
+  for (int k = 0; k < UW; ++k) {  // (a warp without a unit reads unit 0)
+    const int u = warp + k * W < NU ? warp + k * W : 0, j = u / (NB / 2), c = u % (NB / 2);
+    const float* qh = y + (long long)(g * G + j) * HD + c * 32 + lane;
+    x[k][0] = qh[0];
+    x[k][1] = qh[HD / 2];
+    cs[k] = rope[c * 32 + lane];
+  }
+  if (has_new && warp >= W - 4) {  // the new k and v
+    const float* kh = y + (long long)(p.nq + g) * HD;
+    const float* vh = y + (long long)(p.nq + p.nkv + g) * HD;
+    for (int i = tid - (W - 4) * 32; i < HD / 2; i += 128) {
+      const float k0 = kh[i], k1 = kh[i + HD / 2], v0 = vh[i], v1 = vh[i + HD / 2];
+      rotate(k0, k1, rope[i], &sm.nk[i], &sm.nk[i + HD / 2]);
+      sm.nv[i] = v0;
+      sm.nv[i + HD / 2] = v1;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < UW; ++k) {
+    const int u = warp + k * W;
+    rotate(x[k][0], x[k][1], cs[k], &x[k][0], &x[k][1]);
+    x[k][0] *= p.scale_log2e;
+    x[k][1] *= p.scale_log2e;
+    const uint32_t a = __reduce_max_sync(
+        0xffffffffu, max(__float_as_uint(x[k][0]) & 0x7fffffffu, __float_as_uint(x[k][1]) & 0x7fffffffu));
+    if (u < NU && lane == 0) sm.amax[u / (NB / 2)][u % (NB / 2)] = a;
+  }
+  if (warp == 0) set_sharers(p, sm);
+  __syncthreads();
+  // normalised by 2^e with 2^e max |q| in [2^9, 2^10): as two fp16 parts q
+  // keeps 22 bits of the head's largest value.  Exponent field arithmetic: a
+  // subnormal maximum counts as 2^-127; one past 2^112 (infinite, NaN) overflows.
+#pragma unroll
+  for (int k = 0; k < UW; ++k) {
+    const int u = warp + k * W, j = u / (NB / 2), c0 = u % (NB / 2);
+    if (u < NU) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int i = 0; i < NB / 2; ++i) a = max(a, sm.amax[j][i]);
+      int e = 9 + 127 - (int)(a >> 23);
+      e = min(max(e, -103), 100);
+      // codes reach the MMA as n 2^-24 (low nibbles) or n 2^-20 (high), so q is divided by 16 against the latter
+      const int k16 = lane >> 4;
+      const float up = __uint_as_float((uint32_t)(127 + e - 4 * k16) << 23);
+      if (lane == 0) sm.qf[j] = __uint_as_float((uint32_t)(127 + 24 - e) << 23);
+#pragma unroll
+      for (int hb = 0; hb < 2; ++hb) {
+        const int c = c0 + hb * (NB / 2);
+        const float v = x[k][hb] * up;
+        const __half h = __float2half_rn(v);
+        const float hf = __half2float(h);
+        const __half l = __float2half_rn(v - hf);
+        // element `lane` of a block: code byte i of word w, low (k16 = 0) or high nibble; it meets
+        // half i >> 1 of B register i & 1 of k-step k16, in the lane of quad w and column row8
+        const int w = (lane & 15) >> 2, i = lane & 3;
+        __half* f = reinterpret_cast<__half*>(qfrag);
+        auto put = [&](int col, int part, __half val) {  // part: second fragment (low parts of 8 heads)
+          f[((((c * NH + part) * 32 + col * 4 + w) * 4) + k16 * 2 + (i & 1)) * 2 + (i >> 1)] = val;
+        };
+        // n = code + 8: -8 sum q goes on top
+        const float t = warp_sum((k16 ? -0x1p-17f : -0x1p-21f) * (hf + __half2float(l)));
+        if (G == 8) {
+          const int col = (j & 3) * 2 + (j >> 2);
+          put(col, 0, h);
+          put(col, 1, l);
+          if (lane == 0) (j < 4 ? sm.qb[c][j & 3].x : sm.qb[c][j & 3].y) = t;
+        } else {
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            if (m % G == j) {
+              put(2 * m, 0, h);
+              put(2 * m + 1, 0, l);
+              if (lane == 0) sm.qb[c][m] = make_float2(t, 0.f);
+            }
+        }
       }
     }
-    L.T[b] = T;
-    L.total += T < 0 ? 0 : (long long)p.nkv * (T / kTile + 1);
   }
-  return L;
-}
-
-__device__ __forceinline__ Item item_at(const Params& p, const List& L, long long t) {
-  Item it;
-  it.b = 0;
-  it.g = 0;
-  it.T = 0;
-  it.first = it.end = 0;
-  long long at = 0;
-#pragma unroll
-  for (int b = 0; b < kMaxB; ++b) {
-    const long long n = L.T[b] < 0 ? 0 : L.T[b] / kTile + 1;
-    const long long next = at + n * p.nkv;
-    if (t >= at && t < next) {
-      const int g = (int)((t - at) / n);
-      it.b = b;
-      it.g = g;
-      it.T = L.T[b];
-      it.first = at + g * n;
-      it.end = it.first + n;
+  if (has_new) {
+    for (int u = W - 1 - warp; u < 2 * NB; u += W) {  // block u % NB of K (u < NB) or V
+      const int kv = u / NB, c = u % NB;
+      int code;
+      const uint16_t s = quant_block((kv ? sm.nv : sm.nk)[c * 32 + lane], &code);
+      store_block(s, code, sm.codes[kv] + c * 16, &sm.scales[kv][c],
+                  p.kv_new ? p.kv_new + (((long long)b * 2 + kv) * p.nkv + g) * HD + c * 32 : nullptr, lane);
+      __syncwarp();
+      uint8_t* gc = const_cast<uint8_t*>(kv ? sm.Vc : sm.Kc) + (long long)T * (HD / 2) + c * 16;
+      if (lane < 4)
+        reinterpret_cast<uint32_t*>(gc)[lane] = reinterpret_cast<const uint32_t*>(sm.codes[kv] + c * 16)[lane];
+      uint16_t* gs = reinterpret_cast<uint16_t*>(const_cast<uint8_t*>(kv ? sm.Vsc : sm.Ksc));
+      if (lane == 4) gs[(long long)T * NB + c] = s;
     }
-    at = next;
   }
-  return it;
 }
 
+// The warps' outputs joined, and those of the CTAs that share the item.
 template <int HD, int G>
-__global__ void __launch_bounds__(kThreads, Shape<HD>::kMinCtas) k_attn(const Params p) {
+__device__ __forceinline__ void join_warps(const Params& p, Small& sm, uint8_t* smem, bool first_range) {
   using Sh = Shape<HD>;
-  constexpr int NB = Sh::NB, S = Sh::S;
+  constexpr int W = Sh::W, OP = out_pitch(HD);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+  const int b = sm.b, g = sm.g, c_lo = sm.c_lo, np = sm.np;
+  float* o = p.o + (long long)b * p.ld_o + (long long)g * G * HD;
+  constexpr int NV = G * HD / 4;  // 4-vectors of the outputs
+  float* part = p.part + (2ll * cta + (first_range ? 0 : 1)) * part_size(G, HD);
+  auto put_out = [&](int v, float4 a, float f) {  // o has no alignment of its own
+    o[v * 4] = a.x * f;
+    o[v * 4 + 1] = a.y * f;
+    o[v * 4 + 2] = a.z * f;
+    o[v * 4 + 3] = a.w * f;
+  };
+  auto add = [](float4& a, float f, const float4& x) {
+    a.x = fmaf(f, x.x, a.x);
+    a.y = fmaf(f, x.y, a.y);
+    a.z = fmaf(f, x.z, a.z);
+    a.w = fmaf(f, x.w, a.w);
+  };
+  for (int v = tid; v < NV; v += Sh::kThreads) {
+    const int j = v * 4 / HD;
+    float R = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < W; ++w) R = fmaxf(R, sm.r[w][j]);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    float den = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = ex2(sm.r[w][j] - R);
+      add(a, f, *reinterpret_cast<const float4*>(smem + w * Sh::kWarpRing + (j * OP + v * 4 % HD) * 4));
+      den = fmaf(f, sm.l[w][j], den);
+    }
+    if (np == 1) {
+      put_out(v, a, 1.0f / den);
+    } else {
+      reinterpret_cast<float4*>(part)[v] = a;
+      if (v * 4 % HD == 0) {
+        part[G * HD + j] = R;
+        part[G * HD + G + j] = den;
+      }
+    }
+  }
+  __syncthreads();
+  // ---------------------------------------------------- join the CTAs
+  if (np > 1) {
+    const int slot0 = sm.slot0;
+    auto part_of = [&](int i) {
+      return p.part + (2ll * (c_lo + i) + (i == 0 ? slot0 : 0)) * part_size(G, HD);
+    };
+    // Whether this CTA is the last of n to arrive at the counter, which is left at zero.
+    auto last_of = [&](unsigned* ctr, int n) {
+      if (tid == 0) {
+        __threadfence();
+        const int last = atomicAdd(ctr, 1u) == (unsigned)(n - 1);
+        if (last) *ctr = 0;
+        __threadfence();
+        sm.last = last;
+      }
+      __syncthreads();
+      return sm.last != 0;
+    };
+    // Join partials first, first + step, ... (n <= 32 of them): the first loads are on their way
+    // while one warp per head turns the references into weights.
+    float* wt = reinterpret_cast<float*>(smem);  // [32][G] weights, joined reference and sum per head
+    auto join = [&](int first, int step, int n, bool final) {
+      constexpr int NX = 2;
+      float4 x[NX];
+#pragma unroll
+      for (int i = 0; i < NX; ++i)
+        if (i < n && tid < NV) x[i] = __ldcg(reinterpret_cast<const float4*>(part_of(first + i * step)) + tid);
+      if (warp < G) {
+        const int j = warp;
+        float r = -INFINITY, l = 0.f;
+        if (lane < n) {
+          const float* q = part_of(first + lane * step) + G * HD;
+          r = __ldcg(q + j);
+          l = __ldcg(q + G + j);
+        }
+        const float R = warp_max(r);
+        const float f = lane < n ? ex2(r - R) : 0.f;
+        const float den = warp_sum(f * l);
+        wt[lane * G + j] = f;
+        if (lane == 0) {
+          wt[32 * G + j] = R;
+          wt[33 * G + j] = den;
+        }
+      }
+      __syncthreads();
+      float* dst = part_of(first);
+      for (int v = tid; v < NV; v += Sh::kThreads) {
+        const int j = v * 4 / HD;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = 0; i0 < n; i0 += NX) {
+          if (i0 > 0 || v != tid) {
+#pragma unroll
+            for (int i = 0; i < NX; ++i)
+              if (i0 + i < n) x[i] = __ldcg(reinterpret_cast<const float4*>(part_of(first + (i0 + i) * step)) + v);
+          }
+#pragma unroll
+          for (int i = 0; i < NX; ++i)
+            if (i0 + i < n) add(a, wt[(i0 + i) * G + j], x[i]);
+        }
+        if (final) {
+          put_out(v, a, 1.0f / wt[33 * G + j]);
+        } else {
+          reinterpret_cast<float4*>(dst)[v] = a;
+          if (v * 4 % HD == 0) {
+            dst[G * HD + j] = wt[32 * G + j];
+            dst[G * HD + G + j] = wt[33 * G + j];
+          }
+        }
+      }
+      __syncthreads();
+    };
+    const int me = cta - c_lo, grp = me / kJoin, ng = (np + kJoin - 1) / kJoin;
+    unsigned* ctr = p.counter + (b * p.nkv + g) * kCounters;
+    const int n1 = np - grp * kJoin < kJoin ? np - grp * kJoin : kJoin;
+    if (last_of(ctr + 1 + grp, n1)) {
+      join(grp * kJoin, 1, n1, ng == 1);
+      if (ng > 1 && last_of(ctr, ng)) join(0, kJoin, ng, true);
+    }
+  }
+}
+
+// One token of each sequence.  MMA layouts (lane = 4 * row8 + quad): the codes
+// of 16 cached rows are the A operand of the scores (rows row8 and row8 + 8)
+// and, read transposed, of the outputs (elements row8); the heads are the
+// columns of B, two adjacent columns to a quad lane: for up to 4 heads the
+// fp16 high and low part of head `quad`, for 8 heads two heads, `quad` and
+// quad + 4, whose low parts are a second product into the same accumulator.
+// So a lane's scores, probabilities, maximum, sum and outputs all belong to
+// its own head(s), and only the probabilities change sides (movmatrix).
+template <int HD, int G>
+__global__ void __launch_bounds__(Shape<HD>::kThreads, Shape<HD>::kCtas) k_attn(const __grid_constant__ Params p) {
+  using Sh = Shape<HD>;
+  constexpr int NB = Sh::NB, S = Sh::S, TR = Sh::TR, W = Sh::W, NR = TR / 8;
+  constexpr int NH = G == 8 ? 2 : 1;  // heads of a lane
   extern __shared__ __align__(128) uint8_t smem[];
   uint32_t* qfrag = reinterpret_cast<uint32_t*>(smem + Sh::kRing);
   Small& sm = *reinterpret_cast<Small*>(smem + Sh::kRing + Sh::kQ);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int quad = lane & 3, row8 = lane >> 2;
-  const int head = (G == 8 ? row8 : (row8 & 3)) % G;  // the query head of this lane's scores
-  uint8_t* ring = smem + warp * (S * Sh::kStage);
+  uint8_t* ring = smem + warp * Sh::kWarpRing;
   const uint32_t ring_a = smem_addr(ring);
 
-  const List L = tile_list(p);  // lengths: written only by the previous step's last kernel
-  if (L.total == 0) {
-    pdl_wait();  // the next kernel counts on this one for all before it
-    return;
-  }
-  const long long want = (L.total + p.min_tiles - 1) / p.min_tiles;
-  const int C = want < (long long)gridDim.x ? (int)want : (int)gridDim.x;
   const int cta = blockIdx.x;
-  if (cta >= C) return;
-  const long long t0 = cta * L.total / C, t1 = (cta + 1) * L.total / C;
+  if (warp == 0) {
+    plan_work<TR, W>(p, sm);
+    __syncwarp();
+    if (sm.unit < sm.unit_end) set_range<HD, TR>(p, sm, sm.unit);
+  }
+  __syncthreads();
+  if (sm.at[p.nb] == 0) pdl_wait();  // the next kernel counts on this one for all before it
+  if (sm.unit >= sm.unit_end) return;
 
-  bool waited = false;
-  for (long long seg = t0; seg < t1;) {
-    const Item it = item_at(p, L, seg);
-    const long long seg_end = it.end < t1 ? it.end : t1;
-    const int T = it.T, b = it.b, g = it.g;
-    const int tile0 = (int)(seg - it.first), ntile = (int)(seg_end - seg);
-    const int mine = ntile > warp ? (ntile - warp + kWarps - 1) / kWarps : 0;  // tiles of this warp
-    const long long cap = p.cap[b], cap_s = (cap + 3) & ~3ll;
-    const uint8_t* Kc = p.K[b] + (long long)g * cap * (HD / 2);
-    const uint8_t* Vc = p.V[b] + (long long)g * cap * (HD / 2);
-    const uint8_t* Ksc = reinterpret_cast<const uint8_t*>(p.Ks[b] + (long long)g * cap_s * NB);
-    const uint8_t* Vsc = reinterpret_cast<const uint8_t*>(p.Vs[b] + (long long)g * cap_s * NB);
-
-    // rows [32 k, min(32 k + 32, T)) of tile k = tile0 + warp + 8 i into ring stage i % S
-    auto fetch = [&](int i) {
-      if (i < mine) {
-        const int r0 = (tile0 + warp + kWarps * i) * kTile;
-        const int rows = T - r0 < kTile ? T - r0 : kTile;  // cached rows of the tile (0: only the new row)
-        const uint32_t st = ring_a + (i % S) * Sh::kStage;
+  for (bool more = true, first_range = true; more; first_range = false) {
+    const int T = sm.T[sm.b], tile0 = sm.tile0, ntile = sm.ntile;
+    const int mine = ntile > warp ? (ntile - warp + W - 1) / W : 0;  // tiles of this warp
+    // the cached rows of the warp's next tile into the next ring stage: each lane its 16-byte pieces
+    constexpr int NS = Sh::kScales / 16;  // 16-byte pieces of a tile's K or V scales
+    static_assert(2 * NS <= 32, "at most one scale piece per lane");
+    const int sc_k = lane % NS;
+    int left = T - (tile0 + warp) * TR;   // cached rows from the next tile on (0: only the new row)
+    int unfetched = mine;
+    const uint8_t *kp, *vp, *sp;
+    {
+      const long long r0 = (long long)(tile0 + warp) * TR;
+      kp = sm.Kc + r0 * (HD / 2) + lane * 16;
+      vp = sm.Vc + r0 * (HD / 2) + lane * 16;
+      sp = (lane < NS ? sm.Ksc : sm.Vsc) + r0 * NB * 2 + sc_k * 16;
+    }
+    uint32_t dst = ring_a;                // stage to fetch into
+    const uint32_t sd = (lane < NS ? 0 : Sh::kKV) + Sh::kCodes + sc_k * 16;
+    auto fetch = [&]() {
+      if (unfetched > 0) {
+        if (left >= TR) {
 #pragma unroll
-        for (int u = 0; u < kTile * NB / 32; ++u) {
-          const int id = u * 32 + lane, r = id / NB, c = id % NB;
-          const bool in = r < rows;
-          const long long off = in ? (long long)r0 * (HD / 2) + id * 16 : 0;
-          cp16(st + place<NB>(r, c), Kc + off, in ? 16 : 0);
-          cp16(st + Sh::kCodes + Sh::kScales + place<NB>(r, c), Vc + off, in ? 16 : 0);
-        }
-        constexpr int NS = Sh::kScales / 16;
-        const int valid = rows * NB * 2;  // bytes
-#pragma unroll
-        for (int u = 0; u < (2 * NS + 31) / 32; ++u) {
-          const int id = u * 32 + lane;
-          if (id < 2 * NS) {
-            const int kv = id / NS, c = id % NS;
-            const int left = valid - c * 16;
-            const int bytes = left <= 0 ? 0 : (left < 16 ? left : 16);
-            const uint8_t* src = (kv ? Vsc : Ksc) + (bytes ? (long long)r0 * NB * 2 + c * 16 : 0);
-            cp16(st + kv * (Sh::kCodes + Sh::kScales) + Sh::kCodes + c * 16, src, bytes);
+          for (int u = 0; u < TR * NB / 32; ++u) {
+            const int id = u * 32 + lane;
+            cp16(dst + place<NB>(id / NB, id % NB), kp + u * 512, 16);
+            cp16(dst + Sh::kKV + place<NB>(id / NB, id % NB), vp + u * 512, 16);
           }
+          if (lane < 2 * NS) cp16(dst + sd, sp, 16);
+        } else {  // past the last cached row: zeros (codes -8 under scales 0), nothing read
+#pragma unroll
+          for (int u = 0; u < TR * NB / 32; ++u) {
+            const int id = u * 32 + lane;
+            const bool in = id / NB < left;
+            cp16(dst + place<NB>(id / NB, id % NB), in ? kp + u * 512 : sm.Kc, in ? 16 : 0);
+            cp16(dst + Sh::kKV + place<NB>(id / NB, id % NB), in ? vp + u * 512 : sm.Vc, in ? 16 : 0);
+          }
+          const int b16 = left * NB * 2 - sc_k * 16;
+          const int bytes = b16 <= 0 ? 0 : (b16 < 16 ? b16 : 16);
+          if (lane < 2 * NS) cp16(dst + sd, bytes ? sp : sm.Ksc, bytes);
         }
+        kp += W * Sh::kCodes;
+        vp += W * Sh::kCodes;
+        sp += W * Sh::kScales;
+        left -= W * TR;
+        --unfetched;
+        dst = dst == ring_a + (S - 1) * Sh::kStage ? ring_a : dst + Sh::kStage;
       }
       cp_commit();
     };
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) fetch(i);
+    for (int i = 0; i < S - 1; ++i) fetch();
 
-    if (!waited) {
+    if (first_range) {
       pdl_wait();
       pdl_launch_dependents();
-      waited = true;
     }
-    // ---------------------------------------------------- queries and the new row
-    const float* y = p.y + (long long)b * p.ld_y;
-    const float2* rope = p.rope + (long long)T * (HD / 2);
-    const bool has_new = seg_end == it.end;
-    if (warp < G) {  // one warp per head: rotated, normalised to a power of two, split
-      const float* qh = y + (long long)(g * G + warp) * HD;
-      constexpr int PL = HD / 64;  // pairs per lane
-      float x0[PL], x1[PL], amax = 0.f;
-#pragma unroll
-      for (int u = 0; u < PL; ++u) {
-        const int i = u * 32 + lane;
-        rotate(qh[i], qh[i + HD / 2], rope[i], &x0[u], &x1[u]);
-        x0[u] *= p.scale_log2e;
-        x1[u] *= p.scale_log2e;
-        amax = fmaxf(amax, fmaxf(fabsf(x0[u]), fabsf(x1[u])));
-      }
-      amax = warp_max(amax);
-      // 2^e amax in [2^9, 2^10): q as two fp16 parts keeps 22 bits of the head's largest value
-      int e = 0;
-      if (amax > 0.f && amax < INFINITY) e = 9 - ilogbf(amax);
-      e = e > 100 ? 100 : e;
-      float sum[2 * PL];
-#pragma unroll
-      for (int u = 0; u < 2 * PL; ++u) {
-        const int el = (u < PL ? u : u - PL) * 32 + lane + (u < PL ? 0 : HD / 2);  // element of the head
-        const float v = scalbnf(u < PL ? x0[u] : x1[u - PL], e);
-        const __half h = __float2half_rn(v);
-        const float hf = __half2float(h);
-        const __half l = __float2half_rn(v - hf);
-        // operand place of element el: block c, word w (4 codes of each half of a block), byte j, half k
-        const int c = el >> 5, i = el & 31, k16 = i >> 4, w = (i & 15) >> 2, j = i & 3;
-        // code j of a word meets half (j >> 1) of register (j & 1 ? a2 : a0) of k-step k16
-        __half* f = reinterpret_cast<__half*>(qfrag);
-#pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          const int hm = (G == 8 ? m : (m & 3)) % G;
-          if (hm != warp) continue;
-          const int base = (((c * 2 + k16) * 32 + m * 4 + w) * 4 + (j & 1) * 2) * 2 + (j >> 1);
-          f[base] = h;
-          f[base + 2] = l;
-        }
-        // stored codes reach the MMA as code + 24 or (high nibble of an even byte) code + 72
-        const float bias = (k16 == 1 && (j & 1) == 0) ? 72.f : 24.f;
-        sum[u] = bias * (hf + __half2float(l));
-      }
-#pragma unroll
-      for (int u = 0; u < 2 * PL; ++u) {  // a block is one u: 32 lanes
-        const float t = warp_sum(sum[u]);
-        const int c = u < PL ? u : u - PL + NB / 2;
-        if (lane == 0) sm.qb[c][warp] = -t;
-      }
-      if (lane == 0) sm.qf[warp] = scalbnf(1.0f, -e);
-    }
-    if (has_new) {
-      const float* kh = y + (long long)(p.nq + g) * HD;
-      const float* vh = y + (long long)(p.nq + p.nkv + g) * HD;
-      if (tid < HD / 2) rotate(kh[tid], kh[tid + HD / 2], rope[tid], &sm.nk[tid], &sm.nk[tid + HD / 2]);
-      if (tid < HD) sm.nv[tid] = vh[tid];
-      __syncthreads();
-      for (int u = warp; u < 2 * NB; u += kWarps) {  // block u % NB of K (u < NB) or V
-        const int kv = u / NB, c = u % NB;
-        int code;
-        const uint16_t s = quant_block((kv ? sm.nv : sm.nk)[c * 32 + lane], &code);
-        store_block(s, code, sm.codes[kv] + c * 16, &sm.scales[kv][c],
-                    p.kv_new ? p.kv_new + (((long long)b * 2 + kv) * p.nkv + g) * HD + c * 32 : nullptr, lane);
-        __syncwarp();
-        uint8_t* gc = (kv ? p.V[b] : p.K[b]) + ((long long)g * cap + T) * (HD / 2) + c * 16;
-        if (lane < 4) reinterpret_cast<uint32_t*>(gc)[lane] = reinterpret_cast<const uint32_t*>(sm.codes[kv] + c * 16)[lane];
-        if (lane == 4) (kv ? p.Vs[b] : p.Ks[b])[((long long)g * cap_s + T) * NB + c] = s;
-      }
-    }
+    prepare<HD, G>(p, sm, qfrag);
     __syncthreads();
 
     // ---------------------------------------------------- the warp's tiles
@@ -376,253 +695,232 @@ __global__ void __launch_bounds__(kThreads, Shape<HD>::kMinCtas) k_attn(const Pa
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[c][t][k] = 0.f;
-    float mx = -INFINITY, ref = -INFINITY, lsum = 0.f;
-    int sh = 29;  // probabilities are held as 2^sh p: p sV then fills fp16's range from above
-    const float qf = sm.qf[head];
-    float qb[NB];
+    float mx[NH], ref[NH], lsum[NH], qf[NH];
 #pragma unroll
-    for (int c = 0; c < NB; ++c) qb[c] = sm.qb[c][head];
+    for (int h = 0; h < NH; ++h) {
+      mx[h] = ref[h] = -INFINITY;
+      lsum[h] = 0.f;
+      qf[h] = sm.qf[G == 8 ? quad + 4 * h : quad % G];
+    }
+    int sh = 29;  // probabilities are held as 2^sh p: p sV then fills fp16's range from above
+    // ldmatrix row of this lane: 8-row groups of one block, or (16-row tiles) of two
+    auto frag = [&](int cp, int half) {
+      return NR == 4 ? place<NB>(lane, cp * 2 + half) : place<NB>(lane & 15, cp * 2 + (lane >> 4));
+    };
 
+    uint32_t st = ring_a;                     // stage to read
+    int valid = T + 1 - (tile0 + warp) * TR;  // rows of the tile that exist
     for (int i = 0; i < mine; ++i) {
-      fetch(i + S - 1);
+      fetch();
       cp_wait<S - 1>();
       __syncwarp();
-      const int r0 = (tile0 + warp + kWarps * i) * kTile;
-      uint8_t* stp = ring + (i % S) * Sh::kStage;
-      const uint32_t st = ring_a + (i % S) * Sh::kStage;
-      const uint32_t vst = st + Sh::kCodes + Sh::kScales;
-      const int valid = T + 1 - r0;  // rows of the tile that exist
-      if (valid <= kTile) {          // the last tile: the new row's codes and scales are its last row
+      const uint32_t vst = st + Sh::kKV;
+      if (valid <= TR) {  // the last tile: the new row's codes and scales are its last row
         const int r = valid - 1;
         if (lane < 2 * NB) {
           const int kv = lane / NB, c = lane % NB;
-          uint8_t* d = stp + kv * (Sh::kCodes + Sh::kScales);
+          uint8_t* d = ring + (st - ring_a) + kv * Sh::kKV;
           *reinterpret_cast<uint4*>(d + place<NB>(r, c)) = *reinterpret_cast<const uint4*>(sm.codes[kv] + c * 16);
           *reinterpret_cast<uint16_t*>(d + Sh::kCodes + (r * NB + c) * 2) = sm.scales[kv][c];
         }
         __syncwarp();
       }
-      // largest V scale of the tile (as fp16 bits: scales are not negative, a sign is masked)
-      uint32_t vmax = 0;
+      // largest V scale of the tile (as fp16 bits, a sign masked)
+      __half2 vm = u2h(lds32(vst + Sh::kCodes + lane * 4) & 0x7fff7fffu);
 #pragma unroll
-      for (int u = 0; u < NB / 2; ++u) {
-        const uint32_t w = lds32(vst + Sh::kCodes + (u * 32 + lane) * 4);
-        vmax = max(vmax, max(w & 0x7fffu, (w >> 16) & 0x7fffu));
-      }
+      for (int u = 1; u < Sh::kScales / 128; ++u)
+        vm = __hmax2(vm, u2h(lds32(vst + Sh::kCodes + (u * 32 + lane) * 4) & 0x7fff7fffu));
+      uint32_t vmax = max(h2u(vm) & 0xffffu, h2u(vm) >> 16);
       vmax = __reduce_max_sync(0xffffffffu, vmax);
 
-      // scores: heads x 8 rows per MMA, two blocks' scales at a time
-      float s[4][2];
+      // scores of rows row8 + 8 n, two blocks at a time
+      float s[NR][NH];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) s[n][0] = s[n][1] = 0.f;
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int h = 0; h < NH; ++h) s[n][h] = 0.f;
 #pragma unroll
       for (int cp = 0; cp < NB / 2; ++cp) {
-        uint32_t sc[4][2];
+        uint32_t sc[NR], w[2][NR];
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) sc[n][k] = lds32(st + Sh::kCodes + ((n * 8 + quad * 2 + k) * NB + cp * 2) * 2);
+        for (int n = 0; n < NR; ++n) sc[n] = lds32(st + Sh::kCodes + ((n * 8 + row8) * NB + cp * 2) * 2);
+        ldsm4(&w[0][0], st + frag(cp, 0));
+        if (NR == 4) ldsm4(&w[1][0], st + frag(cp, 1));
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int c = cp * 2 + half;
-          uint32_t w[4];
-          ldsm4(w, st + place<NB>(lane, c));
-          const uint4 a0 = *reinterpret_cast<const uint4*>(qfrag + ((c * 2 + 0) * 32 + lane) * 4);
-          const uint4 a1 = *reinterpret_cast<const uint4*>(qfrag + ((c * 2 + 1) * 32 + lane) * 4);
+          const uint4 q0 = *reinterpret_cast<const uint4*>(qfrag + (c * NH * 32 + lane) * 4);
+          uint4 q1;
+          if (G == 8) q1 = *reinterpret_cast<const uint4*>(qfrag + ((c * NH + 1) * 32 + lane) * 4);
+          const float2 qb = sm.qb[c][quad];
+          uint32_t h[NR][4];
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            // 16 + n or 64 + n in fp16 from each nibble n = code + 8
-            const uint32_t h0 = and_or(w[n] << 6, 0x03c003c0u, 0x4c004c00u);
-            const uint32_t h1 = and_or(w[n], 0x00f000f0u, 0x54005400u);
-            const uint32_t h2 = and_or(w[n] >> 2, 0x03c003c0u, 0x4c004c00u);
-            const uint32_t h3 = and_or(w[n] >> 6, 0x03c003c0u, 0x4c004c00u);
-            float d[4] = {qb[c], qb[c], 0.f, 0.f};
-            mma(d, a0.x, a0.y, a0.z, a0.w, h0, h2);
-            mma(d, a1.x, a1.y, a1.z, a1.w, h1, h3);
-            s[n][0] = fmaf(half ? hi_f(sc[n][0]) : lo_f(sc[n][0]), d[0] + d[2], s[n][0]);
-            s[n][1] = fmaf(half ? hi_f(sc[n][1]) : lo_f(sc[n][1]), d[1] + d[3], s[n][1]);
+          for (int n = 0; n < NR; ++n) nibbles(w[half][n], h[n]);
+          // 16 rows a product; the products into one accumulator are apart
+          float d[NR / 2][4];
+#pragma unroll
+          for (int m = 0; m < NR / 2; ++m) {
+            const uint32_t *x = h[m * 2], *z = h[m * 2 + 1];
+            mma_c(d[m], x[0], z[0], x[1], z[1], q0.x, q0.y, 0.f, 0.f, 0.f, 0.f);
+          }
+#pragma unroll
+          for (int m = 0; m < NR / 2; ++m) {
+            const uint32_t *x = h[m * 2], *z = h[m * 2 + 1];
+            mma(d[m], x[2], z[2], x[3], z[3], q0.z, q0.w);
+          }
+          if (G == 8) {
+#pragma unroll
+            for (int m = 0; m < NR / 2; ++m) {
+              const uint32_t *x = h[m * 2], *z = h[m * 2 + 1];
+              mma(d[m], x[0], z[0], x[1], z[1], q1.x, q1.y);
+            }
+#pragma unroll
+            for (int m = 0; m < NR / 2; ++m) {
+              const uint32_t *x = h[m * 2], *z = h[m * 2 + 1];
+              mma(d[m], x[2], z[2], x[3], z[3], q1.z, q1.w);
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            const float f = half ? hi_f(sc[n]) : lo_f(sc[n]);
+            const float *dn = d[n / 2] + (n & 1) * 2;
+            if (G == 8) {
+              s[n][0] = fmaf(f, dn[0] + qb.x, s[n][0]);
+              s[n][NH - 1] = fmaf(f, dn[1] + qb.y, s[n][NH - 1]);
+            } else {
+              s[n][0] = fmaf(f, (dn[0] + qb.x) + dn[1], s[n][0]);
+            }
           }
         }
       }
-      float tm = -INFINITY;
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          s[n][k] *= qf;
-          if (n * 8 + quad * 2 + k >= valid) s[n][k] = -INFINITY;
-          tm = fmaxf(tm, s[n][k]);
-        }
-      tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
-      tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 2));
-      mx = fmaxf(mx, tm);
       // sV < 2^(E - 14) with E the exponent field of the largest, so 2^sh p sV <= 2^15
       const int fit = 29 - (int)(vmax >> 10);
       sh = fit < sh ? fit : sh;
-      const float nref = mx - (float)sh;
-      if (__any_sync(0xffffffffu, nref != ref)) {
-        const float corr = ex2(ref - nref);
-        lsum *= corr;
-        const float c0 = __shfl_sync(0xffffffffu, corr, quad * 8), c1 = __shfl_sync(0xffffffffu, corr, quad * 8 + 4);
+      float nref[NH];
+      bool moved = false;
+      if (valid < TR) {
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int h = 0; h < NH; ++h)
+            if (n * 8 + row8 >= valid) s[n][h] = -INFINITY;
+      }
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        float tm = s[0][h];
+#pragma unroll
+        for (int n = 1; n < NR; ++n) tm = fmaxf(tm, s[n][h]);
+        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 4));
+        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 8));
+        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
+        mx[h] = fmaxf(mx[h], tm * qf[h]);
+        nref[h] = mx[h] - (float)sh;
+        moved |= nref[h] != ref[h];
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+        float corr[NH];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          corr[h] = ex2(ref[h] - nref[h]);
+          lsum[h] *= corr[h];
+          ref[h] = nref[h];
+        }
 #pragma unroll
         for (int c = 0; c < NB; ++c)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            acc[c][t][0] *= c0;
-            acc[c][t][1] *= c1;
-            acc[c][t][2] *= c0;
-            acc[c][t][3] *= c1;
-          }
-        ref = nref;
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[c][t][k] *= corr[G == 8 ? (k & 1) * (NH - 1) : 0];
       }
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          s[n][k] = ex2(s[n][k] - ref);
-          lsum += s[n][k];
+        for (int h = 0; h < NH; ++h) {
+          s[n][h] = ex2(fmaf(s[n][h], qf[h], -ref[h]));
+          lsum[h] += s[n][h];
         }
-      // outputs
+      // outputs, two blocks at a time
 #pragma unroll
       for (int cp = 0; cp < NB / 2; ++cp) {
-        uint32_t sc[4][2];
+        uint32_t sc[NR], w[2][NR];
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) sc[n][k] = lds32(vst + Sh::kCodes + ((n * 8 + quad * 2 + k) * NB + cp * 2) * 2);
+        for (int n = 0; n < NR; ++n) sc[n] = lds32(vst + Sh::kCodes + ((n * 8 + row8) * NB + cp * 2) * 2);
+        ldsm4t(&w[0][0], vst + frag(cp, 0));
+        if (NR == 4) ldsm4t(&w[1][0], vst + frag(cp, 1));
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int c = cp * 2 + half;
-          uint32_t w[4];
-          ldsm4t(w, vst + place<NB>(lane, c));
-          uint32_t ph[4], pl[4];
+          uint32_t ph[NR], pl[NR];
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const float v0 = s[n][0] * (half ? hi_f(sc[n][0]) : lo_f(sc[n][0]));
-            const float v1 = s[n][1] * (half ? hi_f(sc[n][1]) : lo_f(sc[n][1]));
-            ph[n] = h2u(__floats2half2_rn(v0, v1));
-            pl[n] = h2u(__floats2half2_rn(v0 - lo_f(ph[n]), v1 - hi_f(ph[n])));
-            if (G <= 4 && row8 >= 4) ph[n] = pl[n];  // columns 4..7 carry the low parts
+          for (int n = 0; n < NR; ++n) {
+            const float sv = half ? hi_f(sc[n]) : lo_f(sc[n]);
+            if (G == 8) {
+              const float v0 = s[n][0] * sv, v1 = s[n][NH - 1] * sv, h0 = trunc11(v0), h1 = trunc11(v1);
+              ph[n] = movmatrix(h2u(__floats2half2_rn(h0, h1)));
+              pl[n] = movmatrix(h2u(__floats2half2_rn(v0 - h0, v1 - h1)));
+            } else {
+              const float v = s[n][0] * sv, h0 = trunc11(v);
+              ph[n] = movmatrix(h2u(__floats2half2_rn(h0, v - h0)));
+              pl[n] = 0;
+            }
           }
-          uint32_t v[4][4];  // codes of 8 rows: elements 2 c', 2 c' + 16, 2 c' + 1, 2 c' + 17 of the block
-          const __half2 k1032 = u2h(0x64086408u), k16th = u2h(0x2c002c00u), k72 = u2h(0xd480d480u);
+          // codes of 8 rows: elements 2 r, 2 r + 1 (v[0], v[1]) and 2 r + 16, 2 r + 17 of the block, r = row8
+          uint32_t v[NR][4];
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const uint32_t w8 = w[n] >> 8;
-            v[n][0] = h2u(__hsub2(u2h(and_or(w[n], 0x000f000fu, 0x64006400u)), k1032));
-            v[n][1] = h2u(__hfma2(u2h(and_or(w[n], 0x00f000f0u, 0x64006400u)), k16th, k72));
-            v[n][2] = h2u(__hsub2(u2h(and_or(w8, 0x000f000fu, 0x64006400u)), k1032));
-            v[n][3] = h2u(__hfma2(u2h(and_or(w8, 0x00f000f0u, 0x64006400u)), k16th, k72));
-          }
+          for (int n = 0; n < NR; ++n) codes(w[half][n], v[n]);
 #pragma unroll
-          for (int kt = 0; kt < 2; ++kt) {
-            const int n = kt * 2;
+          for (int part = 0; part < (G == 8 ? 2 : 1); ++part) {
+            const uint32_t* pp = part ? pl : ph;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              mma(acc[c][t], v[n][t], v[n][t + 2], v[n + 1][t], v[n + 1][t + 2], ph[n], ph[n + 1]);
-              if (G == 8) mma(acc[c][t], v[n][t], v[n][t + 2], v[n + 1][t], v[n + 1][t + 2], pl[n], pl[n + 1]);
+            for (int m = 0; m < NR / 2; ++m) {
+              const int n = m * 2;
+#pragma unroll
+              for (int t = 0; t < 2; ++t)
+                mma(acc[c][t], v[n][2 * t], v[n][2 * t + 1], v[n + 1][2 * t], v[n + 1][2 * t + 1], pp[n], pp[n + 1]);
             }
           }
         }
       }
       __syncwarp();  // every lane has read the stage before it is fetched into again
+      st = st == ring_a + (S - 1) * Sh::kStage ? ring_a : st + Sh::kStage;
+      valid -= W * TR;
     }
     cp_wait<0>();
     __syncwarp();
 
     // ---------------------------------------------------- join the warps
-    lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
-    lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
-    if (quad == 0 && row8 < G) {
-      sm.r[warp][row8] = ref;
-      sm.l[warp][row8] = lsum;
-    }
-    float* ow = reinterpret_cast<float*>(ring);  // [G][HD] of this warp, in its own ring
+    constexpr int OP = out_pitch(HD);
+    float* ow = reinterpret_cast<float*>(ring);  // [G][OP] of this warp, in its own ring
+    static_assert(G * OP * 4 <= Sh::kWarpRing, "a warp's outputs fit its ring");
 #pragma unroll
-    for (int c = 0; c < NB; ++c)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        float a[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          a[k] = acc[c][t][k];
-          if (G <= 4) a[k] += __shfl_xor_sync(0xffffffffu, a[k], 2);  // low parts: columns 4..7
+    for (int h = 0; h < NH; ++h) {
+      const int j = quad + 4 * h;
+      lsum[h] += __shfl_xor_sync(0xffffffffu, lsum[h], 4);
+      lsum[h] += __shfl_xor_sync(0xffffffffu, lsum[h], 8);
+      lsum[h] += __shfl_xor_sync(0xffffffffu, lsum[h], 16);
+      if (j < G) {
+        if (row8 == 0) {
+          sm.r[warp][j] = ref[h];
+          sm.l[warp][j] = lsum[h];
         }
-        const int e = c * 32 + t * 16 + row8 * 2, j = quad * 2;
-        if (j < G) *reinterpret_cast<float2*>(ow + j * HD + e) = make_float2(a[0], a[2]);
-        if (j + 1 < G) *reinterpret_cast<float2*>(ow + (j + 1) * HD + e) = make_float2(a[1], a[3]);
-      }
-    __syncthreads();
-    const int c_lo = (int)(((it.first + 1) * C - 1) / L.total), c_hi = (int)((it.end * C - 1) / L.total);
-    const int np = c_hi - c_lo + 1;  // CTAs that share the item
-    float* o = p.o + (long long)b * p.ld_o + (long long)g * G * HD;
-    constexpr int PF = G * (HD + 2);
-    float* part = p.part + (2ll * cta + (seg == t0 ? 0 : 1)) * PF;
-    for (int e = tid; e < G * HD; e += kThreads) {
-      const int j = e / HD;
-      float R = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) R = fmaxf(R, sm.r[w][j]);
-      float num = 0.f, den = 0.f;
+        for (int c = 0; c < NB; ++c)
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2(sm.r[w][j] - R);
-        num = fmaf(f, reinterpret_cast<const float*>(smem + w * (S * Sh::kStage))[e], num);
-        den = fmaf(f, sm.l[w][j], den);
-      }
-      if (np == 1) {
-        o[e] = num / den;
-      } else {
-        part[e] = num;
-        if (e % HD == 0) {
-          part[G * HD + j] = R;
-          part[G * HD + G + j] = den;
-        }
-      }
-    }
-    __syncthreads();
-    // ---------------------------------------------------- join the CTAs
-    if (np > 1) {
-      if (tid == 0) {
-        __threadfence();
-        unsigned* ctr = p.counter + b * p.nkv + g;
-        const unsigned old = atomicAdd(ctr, 1u);
-        const int last = old == (unsigned)(np - 1);
-        if (last) *ctr = 0;  // zero between launches
-        __threadfence();
-        sm.last = last;
-      }
-      __syncthreads();
-      if (sm.last) {
-        float* wt = reinterpret_cast<float*>(smem);  // [np][G] weights, then the joined 1 / l per head
-        const int slot0 = (c_lo * L.total / C != it.first) ? 1 : 0;  // the first sharer's span began before the item
-        auto part_of = [&](int i) { return p.part + (2ll * (c_lo + i) + (i == 0 ? slot0 : 0)) * PF; };
-        if (warp < G) {
-          const int j = warp;
-          float R = -INFINITY, den = 0.f;
-          for (int i = lane; i < np; i += 32) R = fmaxf(R, __ldcg(part_of(i) + G * HD + j));
-          R = warp_max(R);
-          for (int i = lane; i < np; i += 32) {
-            const float* q = part_of(i) + G * HD;
-            const float f = ex2(__ldcg(q + j) - R);
-            wt[i * G + j] = f;
-            den = fmaf(f, __ldcg(q + G + j), den);
+          for (int t = 0; t < 2; ++t) {
+            const float* a = acc[c][t];
+            *reinterpret_cast<float2*>(ow + j * OP + c * 32 + t * 16 + row8 * 2) =
+                G == 8 ? make_float2(a[h], a[2 + h]) : make_float2(a[0] + a[1], a[2] + a[3]);
           }
-          den = warp_sum(den);
-          if (lane == 0) wt[np * G + j] = 1.0f / den;
-        }
-        __syncthreads();
-        for (int e = tid; e < G * HD; e += kThreads) {
-          const int j = e / HD;
-          float num = 0.f;
-#pragma unroll 8
-          for (int i = 0; i < np; ++i) num = fmaf(wt[i * G + j], __ldcg(part_of(i) + e), num);
-          o[e] = num * wt[np * G + j];
-        }
       }
+    }
+    __syncthreads();
+    join_warps<HD, G>(p, sm, smem, first_range);
+    more = sm.next < sm.unit_end;
+    __syncthreads();
+    if (more) {
+      if (warp == 0) set_range<HD, TR>(p, sm, sm.next);
       __syncthreads();
     }
-    seg = seg_end;
   }
 }
 
@@ -670,30 +968,35 @@ __global__ void __launch_bounds__(256) k_append(const AppendParams p) {
 }
 
 using Kern = void (*)(Params);
-
+struct Pick {
+  Kern k;
+  size_t smem;
+  int threads, per_sm, tile, warps;
+};
 template <int HD>
-Kern pick_g(int G) {
-  return G == 1 ? k_attn<HD, 1> : G == 2 ? k_attn<HD, 2> : G == 4 ? k_attn<HD, 4> : G == 8 ? k_attn<HD, 8> : nullptr;
+Pick pick_g(int G) {
+  using Sh = Shape<HD>;
+  Kern k = G == 1 ? k_attn<HD, 1> : G == 2 ? k_attn<HD, 2> : G == 4 ? k_attn<HD, 4> : G == 8 ? k_attn<HD, 8> : nullptr;
+  return {k, smem_bytes<HD>(), Sh::kThreads, Sh::kCtas, Sh::TR, Sh::W};
 }
-Kern pick(int hd, int G, size_t* smem, int* per_sm) {
-  *smem = hd == 64 ? smem_bytes<64>() : hd == 128 ? smem_bytes<128>() : smem_bytes<256>();
-  *per_sm = hd == 64 ? Shape<64>::kMinCtas : hd == 128 ? Shape<128>::kMinCtas : Shape<256>::kMinCtas;
-  return hd == 64 ? pick_g<64>(G) : hd == 128 ? pick_g<128>(G) : hd == 256 ? pick_g<256>(G) : nullptr;
+Pick pick(int hd, int G) {
+  return hd == 64 ? pick_g<64>(G) : hd == 128 ? pick_g<128>(G) : hd == 256 ? pick_g<256>(G) : Pick{};
 }
 
 }  // namespace
 
-int max_ctas(int hd, int nsm) { return nsm * (hd == 256 ? Shape<256>::kMinCtas : Shape<64>::kMinCtas); }
-
-size_t part_floats(int nq, int nkv, int hd, int nsm) { return (size_t)2 * max_ctas(hd, nsm) * (nq / nkv) * (hd + 2); }
+size_t part_floats(int nq, int nkv, int hd, int nsm) {
+  const Pick k = pick(hd, nq / nkv);
+  return (size_t)2 * nsm * k.per_sm * part_size(nq / nkv, hd);
+}
+size_t counters(int nb, int nkv) { return (size_t)nb * nkv * kCounters; }
 
 cudaError_t init() {
   for (int hd : {64, 128, 256})
     for (int G : {1, 2, 4, 8}) {
-      size_t smem = 0;
-      int per_sm = 0;
-      Kern k = pick(hd, G, &smem, &per_sm);
-      const cudaError_t e = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      const Pick k = pick(hd, G);
+      const cudaError_t e =
+          cudaFuncSetAttribute((const void*)k.k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
       if (e != cudaSuccess) return e;
     }
   return cudaSuccess;
@@ -701,17 +1004,19 @@ cudaError_t init() {
 
 cudaError_t launch(const Params& p, int hd, int nsm, cudaStream_t st, bool pdl) {
   if (p.nb < 1 || p.nb > kMaxB || p.nkv <= 0 || p.nq % p.nkv) return cudaErrorInvalidValue;
-  size_t smem = 0;
-  int per_sm = 0;
-  Kern k = pick(hd, p.nq / p.nkv, &smem, &per_sm);
-  if (!k) return cudaErrorInvalidValue;
-  Params q = p;
-  q.min_tiles = kWarps;
-  long long tiles = 0;  // the most the list can hold
-  for (int b = 0; b < p.nb; ++b) tiles += (long long)p.nkv * ((p.cap[b] - 1) / kTile + 1);
-  long long grid = (tiles + q.min_tiles - 1) / q.min_tiles;
-  if (grid > max_ctas(hd, nsm)) grid = max_ctas(hd, nsm);
-  return launch_k(k, dim3((unsigned)grid), dim3(kThreads), smem, st, pdl, q);
+  const Pick k = pick(hd, p.nq / p.nkv);
+  if (!k.k) return cudaErrorInvalidValue;
+  long long tiles = 0, chunks = 0;  // the most the caches can hold
+  for (int b = 0; b < p.nb; ++b) {
+    const long long n = (p.cap[b] - 1) / k.tile + 1;
+    tiles += p.nkv * n;
+    chunks += p.nkv * ((n + k.warps - 1) / k.warps);
+  }
+  if (tiles > (1 << 30)) return cudaErrorInvalidValue;
+  long long grid = (long long)nsm * k.per_sm;
+  if (grid > (kCounters - 1) * kJoin) grid = (kCounters - 1) * kJoin;  // what the joins can count
+  if (grid > chunks) grid = chunks;
+  return launch_k(k.k, dim3((unsigned)grid), dim3(k.threads), k.smem, st, pdl, p);
 }
 
 cudaError_t append(const AppendParams& p, int hd, cudaStream_t st) {
