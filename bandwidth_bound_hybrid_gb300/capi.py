@@ -31,7 +31,7 @@ HY_FLAG_TOKEN_PREFILL = 16
 
 HY_NOALLOC_SCRATCH_BYTES = 1 << 20
 
-i32, u32, u64, f32, vp, sz = ctypes.c_int32, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+i32, i64, u32, u64, f32, vp, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
 P = ctypes.POINTER
 
 
@@ -100,6 +100,9 @@ SIGNATURES = {
     "hy_op_attention_q4_workspace": (sz, [i32, i32, i32, i32]),
     "hy_op_attention_q4": (ctypes.c_int, [vp, i32, i32, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, i32, vp, vp, vp]),
     "hy_op_kv_append_q4": (ctypes.c_int, [vp, i32, i32, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp]),
+    "hy_op_beam_select_workspace": (sz, [i32, i32, i32]),
+    "hy_op_beam_select": (ctypes.c_int, [vp, i32, i32, i32, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp]),
+    "hy_op_beam_reorder": (ctypes.c_int, [vp, i64, i32, i64, i64, i32, i32, vp, vp]),
     "hy_op_attention_i8": (ctypes.c_int, [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, i32, vp, vp, vp]),
 }
 

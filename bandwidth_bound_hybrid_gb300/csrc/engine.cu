@@ -2154,12 +2154,14 @@ int hy_op_attention_i8(const float* y_dev, void* Kq_dev, float* Ks_dev, void* Vq
 }
 
 // Checks that hy_op_attention_q4 and hy_op_kv_append_q4 share.
-static int check_q4_cache(const void* K, const void* Ks, const void* V, const void* Vs, int32_t cap, int32_t nq,
-                          int32_t nkv, int32_t hd) {
+static int check_q4_cache(const void* K, const void* Ks, const void* V, const void* Vs, int32_t batch, int32_t cap,
+                          int32_t nq, int32_t nkv, int32_t hd) {
   if (!aligned16(K) || !aligned16(Ks) || !aligned16(V) || !aligned16(Vs) || cap <= 0 || nkv <= 0 || nq <= 0 || nq % nkv)
     return fail(HY_ERR_ARG, "bad 4-bit cache arguments");
   if ((hd != 64 && hd != 128 && hd != 256) || nq / nkv > 8 || ((nq / nkv) & (nq / nkv - 1)) || nkv > 1024)
     return fail(HY_ERR_UNSUPPORTED, "4-bit cache: head_dim 64/128/256, nq/nkv in {1,2,4,8}, nkv <= 1024");
+  if ((long long)batch * nkv * ((cap - 1) / 16 + 1) > (1 << 30))  // the attention's list of tiles
+    return fail(HY_ERR_UNSUPPORTED, "4-bit cache: batch x nkv x cap above 2^34 rows");
   return HY_OK;
 }
 
@@ -2173,7 +2175,7 @@ int hy_op_attention_q4(const float* y_dev, int32_t ldy, int32_t batch, void* Kq_
                        void* Vs_dev, int32_t cap, int32_t nq, int32_t nkv, int32_t hd, const int32_t* len_dev,
                        const float* rope_table_dev, float* o_dev, int32_t ldo, float* kv_new_dev, void* workspace_dev,
                        void* stream) {
-  int rc = check_q4_cache(Kq_dev, Ks_dev, Vq_dev, Vs_dev, cap, nq, nkv, hd);
+  int rc = check_q4_cache(Kq_dev, Ks_dev, Vq_dev, Vs_dev, batch, cap, nq, nkv, hd);
   if (rc != HY_OK) return rc;
   if (!y_dev || !len_dev || !rope_table_dev || !o_dev || !aligned16(workspace_dev) || batch < 1 ||
       batch > kv4::kMaxB || (long long)ldy < ((long long)nq + 2 * nkv) * hd || (long long)ldo < (long long)nq * hd)
@@ -2213,7 +2215,7 @@ int hy_op_attention_q4(const float* y_dev, int32_t ldy, int32_t batch, void* Kq_
 int hy_op_kv_append_q4(const float* y_dev, int32_t ldy, int32_t n, void* Kq_dev, void* Ks_dev, void* Vq_dev,
                        void* Vs_dev, int32_t cap, int32_t nq, int32_t nkv, int32_t hd, const int32_t* len_dev,
                        const float* rope_table_dev, float* kv_new_dev, void* stream) {
-  int rc = check_q4_cache(Kq_dev, Ks_dev, Vq_dev, Vs_dev, cap, nq, nkv, hd);
+  int rc = check_q4_cache(Kq_dev, Ks_dev, Vq_dev, Vs_dev, 1, cap, nq, nkv, hd);
   if (rc != HY_OK) return rc;
   if ((n > 0 && !y_dev) || !len_dev || !rope_table_dev || n < 0 ||
       (long long)ldy < ((long long)nq + 2 * nkv) * hd)
@@ -2240,6 +2242,88 @@ int hy_op_kv_append_q4(const float* y_dev, int32_t ldy, int32_t n, void* Kq_dev,
   a.guard = guard;
   cudaError_t e = kv4::append(a, hd, (cudaStream_t)stream);
   if (e != cudaSuccess) return fail(HY_ERR_CUDA, "4-bit append launch: %s", cudaGetErrorString(e));
+  return HY_OK;
+}
+
+static size_t beam_counters(int32_t groups) { return ((size_t)groups * 4 + 255) / 256 * 256; }
+static size_t beam_stats(int32_t groups, int32_t beams, int32_t vocab) {
+  return ((size_t)groups * beams * beam::chunks(vocab) * 8 + 255) / 256 * 256;
+}
+
+size_t hy_op_beam_select_workspace(int32_t groups, int32_t beams, int32_t vocab) {
+  if (groups <= 0 || beams <= 0 || beams > beam::kMaxBeams || vocab <= 0) return 0;
+  return beam_counters(groups) + beam_stats(groups, beams, vocab) +
+         (size_t)groups * beams * beam::chunks(vocab) * beam::kMaxPicks * 8;
+}
+
+int hy_op_beam_select(const float* logits_dev, int32_t ldl, int32_t groups, int32_t beams, int32_t vocab,
+                      int32_t picks, const float* score_dev, const int32_t* done_dev, int32_t eos,
+                      float* score_out_dev, int32_t* parent_out_dev, int32_t* token_out_dev, int32_t* done_out_dev,
+                      void* workspace_dev, void* stream) {
+  if (!logits_dev || !score_dev || !score_out_dev || !parent_out_dev || !token_out_dev || !aligned16(workspace_dev) ||
+      groups <= 0 || beams <= 0 || vocab <= 0 || picks <= 0 || ldl < vocab)
+    return fail(HY_ERR_ARG, "bad beam selection arguments");
+  if ((long long)picks > (long long)beams * vocab)
+    return fail(HY_ERR_ARG, "%d picks of %d beams x %d tokens", picks, beams, vocab);
+  if (done_dev && (eos < 0 || eos >= vocab)) return fail(HY_ERR_ARG, "ended beams need an end token in [0, vocab)");
+  const long long lists = (long long)beams * beam::chunks(vocab);
+  if (beams > beam::kMaxBeams || picks > beam::kMaxPicks || lists > beam::kMaxLists ||
+      (long long)groups * lists > 0x7fffffffll || (long long)beams * vocab > 0xffffffffll)
+    return fail(HY_ERR_UNSUPPORTED, "beam selection: at most %d beams, %d picks, %d beams x chunks of %d tokens",
+                beam::kMaxBeams, beam::kMaxPicks, beam::kMaxLists, beam::kChunk);
+  uint8_t* ws = (uint8_t*)workspace_dev;
+  beam::SelectParams p;
+  memset(&p, 0, sizeof(p));
+  p.logits = logits_dev;
+  p.ld = ldl;
+  p.vocab = vocab;
+  p.beams = beams;
+  p.picks = picks;
+  p.chunks = beam::chunks(vocab);
+  p.score = score_dev;
+  p.done = done_dev;
+  p.eos = eos;
+  p.score_out = score_out_dev;
+  p.parent = parent_out_dev;
+  p.token = token_out_dev;
+  p.done_out = done_out_dev;
+  p.counter = (unsigned*)ws;
+  p.stats = (float2*)(ws + beam_counters(groups));
+  p.lists = (uint64_t*)(ws + beam_counters(groups) + beam_stats(groups, beams, vocab));
+  cudaError_t e = beam::select(p, groups, (cudaStream_t)stream);
+  if (e != cudaSuccess) return fail(HY_ERR_CUDA, "beam selection launch: %s", cudaGetErrorString(e));
+  return HY_OK;
+}
+
+int hy_op_beam_reorder(void* state_dev, int64_t beam_stride, int32_t n_seg, int64_t seg_stride, int64_t seg_bytes,
+                       int32_t groups, int32_t beams, const int32_t* parent_dev, void* stream) {
+  if (!aligned16(state_dev) || !parent_dev || groups <= 0 || beams <= 0 || n_seg <= 0 || seg_bytes < 0 ||
+      beam_stride % 16 || seg_stride % 16 || seg_bytes % 16)
+    return fail(HY_ERR_ARG, "bad beam reordering arguments (state, strides and segments in 16-byte pieces)");
+  if ((n_seg > 1 && seg_stride < seg_bytes) ||
+      ((long long)groups * beams > 1 &&
+       (beam_stride < seg_bytes || (n_seg > 1 && (beam_stride - seg_bytes) / (n_seg - 1) < seg_stride))))
+    return fail(HY_ERR_ARG, "beam reordering: segments or states overlap");
+  if (beams > beam::kMaxBeams || groups > 65535 || n_seg > 65535)
+    return fail(HY_ERR_UNSUPPORTED, "beam reordering: at most %d beams, 65535 groups and 65535 segments",
+                beam::kMaxBeams);
+  unsigned* guard = nullptr;
+  int rc = op_guard(&guard);
+  if (rc != HY_OK) return rc;
+  beam::ReorderParams p;
+  memset(&p, 0, sizeof(p));
+  for (int i = 0; i < beams; ++i) {
+    p.base[i] = (uint8_t*)state_dev + i * beam_stride;
+    p.seg_stride[i] = seg_stride;
+  }
+  p.group_stride = beams * beam_stride;
+  p.seg_bytes = seg_bytes;
+  p.beams = beams;
+  p.n_seg = n_seg;
+  p.parent = parent_dev;
+  p.guard = guard;
+  cudaError_t e = beam::reorder(p, groups, n_seg, (cudaStream_t)stream);
+  if (e != cudaSuccess) return fail(HY_ERR_CUDA, "beam reordering launch: %s", cudaGetErrorString(e));
   return HY_OK;
 }
 

@@ -240,6 +240,50 @@ cudaError_t launch(const Params& p, int hd, int nsm, cudaStream_t st, bool pdl);
 cudaError_t append(const AppendParams& p, int hd, cudaStream_t st);
 }  // namespace kv4
 
+// ---------------------------------------------------------------- beam search
+// Selection over beams and vocabulary, and in-place reordering of the beams'
+// states (beam.cu).
+namespace beam {
+constexpr int kMaxBeams = 16;    // beams of a group
+constexpr int kMaxPicks = 32;    // picks of a group: a lane each
+constexpr int kChunk = 4096;     // logits of a CTA
+constexpr int kMaxLists = 32768; // beams x chunks of a group
+struct SelectParams {
+  const float* logits;           // [groups * beams][ld]
+  long long ld;
+  int vocab, beams, picks, chunks;
+  const float* score;            // [groups * beams]
+  const int* done;               // [groups * beams] (nullable)
+  int eos;
+  float* score_out;              // [groups * picks]
+  int* parent;
+  int* token;
+  int* done_out;                 // nullable
+  unsigned* counter;             // [groups], zero between launches
+  float2* stats;                 // [groups * beams][chunks]: maximum, sum of exponentials
+  uint64_t* lists;               // [groups * beams][chunks][picks]
+};
+int chunks(int vocab);
+cudaError_t select(const SelectParams& p, int groups, cudaStream_t st);
+
+// Segment s of state i of group z: seg_bytes bytes at base[i] + z * group_stride
+// + s * seg_stride[i] (all multiples of 16).  Paged (page_bytes > 0): rows
+// [first_row, end_row) of row_bytes bytes, row r of the segment in page
+// pages[i][r / page_rows], at base[i] + page * page_bytes + s * seg_stride[i].
+struct ReorderParams {
+  uint8_t* base[kMaxBeams];
+  long long seg_stride[kMaxBeams];
+  long long group_stride, seg_bytes;
+  int beams, n_seg;
+  const int* parent;             // [groups * beams]; null: every state becomes state 0
+  unsigned* guard;
+  const int* pages[kMaxBeams];
+  long long page_bytes;
+  int page_rows, row_bytes, first_row, end_row, first_page;
+};
+cudaError_t reorder(const ReorderParams& p, int groups, int segs, cudaStream_t st);
+}  // namespace beam
+
 // ---------------------------------------------------------------- batched GEMV
 // Up to kMaxB token vectors through one weight stream (tensor-core MMA), bf16
 // or 4-bit block weights.

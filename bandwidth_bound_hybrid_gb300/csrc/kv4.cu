@@ -30,7 +30,7 @@
 // equal span of it, its ends moved to a nearby border between heads.
 // An (sequence, head) that several CTAs share is joined from their partials
 //   R = max_i r_i,  o = sum_i 2^(r_i - R) o_i / sum_i 2^(r_i - R) l_i
-// without any CTA waiting: the last of each 16 sharers to arrive joins the 16,
+// without any CTA waiting: the last of each 24 sharers to arrive joins the 24,
 // and the last of those joins the rest.
 #include <cuda_fp16.h>
 
@@ -42,15 +42,17 @@ namespace kv4 {
 namespace {
 
 // Per head dim: warps of a CTA and CTAs per SM, rows of a warp's tile, and the
-// stages of its ring.  At hd 256 the 64 output accumulators of a lane leave no
-// room for more than 12 warps an SM, and tiles of 16 rows keep the rest small.
+// stages of its ring.  Registers set the warps: a lane holds hd / 4 output
+// accumulators (hd 128, 4 heads, 8 sequences of 120k-131k: 12 warps an SM 104
+// us, 16 warps in two CTAs 108, 8 warps 111; hd 256, 8 heads, 8 sequences of
+// 1k-16k: 8 warps 26.7 us, 12 warps 28.2, 10 warps 30.4).
 template <int HD>
 struct Shape {
-  static constexpr int W = HD == 256 ? 12 : 8;
+  static constexpr int W = HD == 128 ? 12 : 8;
   static constexpr int kThreads = W * 32;
-  static constexpr int kCtas = HD == 256 ? 1 : 2;    // per SM
+  static constexpr int kCtas = HD == 64 ? 2 : 1;     // per SM
   static constexpr int TR = HD == 256 ? 16 : 32;     // rows of a tile
-  static constexpr int S = HD == 64 ? 4 : HD == 128 ? 2 : 3;
+  static constexpr int S = HD == 128 ? 3 : 4;
   static constexpr int NB = HD / 32;                 // blocks of a row
   static constexpr int kCodes = TR * HD / 2;         // bytes of a tile's K or V codes
   static constexpr int kScales = TR * NB * 2;        // and of their scales
@@ -86,8 +88,8 @@ constexpr size_t smem_bytes() {
   return (size_t)Shape<HD>::kRing + Shape<HD>::kQ + sizeof(Small);
 }
 
-constexpr int kJoin = 16;       // partials joined at a time
-constexpr int kCounters = 32;   // of a (sequence, kv head): the last join's, then one per 16 sharers
+constexpr int kJoin = 24;       // partials joined at a time
+constexpr int kCounters = 32;   // of a (sequence, kv head): the last join's, then one per kJoin sharers
 // floats of a partial: outputs [G][HD], references [G], sums [G], in 16-byte pieces
 __host__ __device__ constexpr int part_size(int G, int HD) { return (G * (HD + 2) + 3) / 4 * 4; }
 // floats of a head's outputs in shared memory: padded, so that a quad's heads fall in different banks
@@ -360,6 +362,19 @@ __device__ __forceinline__ void set_sharers(const Params& p, Small& sm) {
   }
 }
 
+__device__ __forceinline__ void put_out(float* o, const float4& a, float f) {  // o has no alignment of its own
+  o[0] = a.x * f;
+  o[1] = a.y * f;
+  o[2] = a.z * f;
+  o[3] = a.w * f;
+}
+__device__ __forceinline__ void add_scaled(float4& a, float f, const float4& x) {
+  a.x = fmaf(f, x.x, a.x);
+  a.y = fmaf(f, x.y, a.y);
+  a.z = fmaf(f, x.z, a.z);
+  a.w = fmaf(f, x.w, a.w);
+}
+
 // The queries of the item as MMA operands, and the new row if the range ends with it.
 template <int HD, int G>
 __device__ __forceinline__ void prepare(const Params& p, Small& sm, uint32_t* qfrag) {
@@ -470,28 +485,79 @@ __device__ __forceinline__ void prepare(const Params& p, Small& sm, uint32_t* qf
   }
 }
 
+// Partials first, first + step, ... (n <= 32 of them) of the item joined into
+// the outputs (final) or into the first of them.  The first loads are on
+// their way while one warp per head turns the references into weights.  Not
+// inlined: its loads would cost the tile loop registers.
+template <int HD, int G>
+__device__ __noinline__ void join_parts(const Params& p, Small& sm, uint8_t* smem, int first, int step, int n,
+                                        bool final) {
+  using Sh = Shape<HD>;
+  constexpr int NV = G * HD / 4, NX = 8;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int c_lo = sm.c_lo, slot0 = sm.slot0;
+  auto part_of = [&](int i) { return p.part + (2ll * (c_lo + i) + (i == 0 ? slot0 : 0)) * part_size(G, HD); };
+  float* o = p.o + (long long)sm.b * p.ld_o + (long long)sm.g * G * HD;
+  float* wt = reinterpret_cast<float*>(smem);  // [32][G] weights, joined reference and sum per head
+  float4 x[NX];
+#pragma unroll
+  for (int i = 0; i < NX; ++i)
+    if (i < n && tid < NV) x[i] = __ldcg(reinterpret_cast<const float4*>(part_of(first + i * step)) + tid);
+  if (warp < G) {
+    const int j = warp;
+    float r = -INFINITY, l = 0.f;
+    if (lane < n) {
+      const float* q = part_of(first + lane * step) + G * HD;
+      r = __ldcg(q + j);
+      l = __ldcg(q + G + j);
+    }
+    const float R = warp_max(r);
+    const float f = lane < n ? ex2(r - R) : 0.f;
+    const float den = warp_sum(f * l);
+    wt[lane * G + j] = f;
+    if (lane == 0) {
+      wt[32 * G + j] = R;
+      wt[33 * G + j] = den;
+    }
+  }
+  __syncthreads();
+  float* dst = part_of(first);
+  for (int v = tid; v < NV; v += Sh::kThreads) {
+    const int j = v * 4 / HD;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < n; i0 += NX) {
+      if (i0 > 0 || v != tid) {
+#pragma unroll
+        for (int i = 0; i < NX; ++i)
+          if (i0 + i < n) x[i] = __ldcg(reinterpret_cast<const float4*>(part_of(first + (i0 + i) * step)) + v);
+      }
+#pragma unroll
+      for (int i = 0; i < NX; ++i)
+        if (i0 + i < n) add_scaled(a, wt[(i0 + i) * G + j], x[i]);
+    }
+    if (final) {
+      put_out(o + v * 4, a, 1.0f / wt[33 * G + j]);
+    } else {
+      reinterpret_cast<float4*>(dst)[v] = a;
+      if (v * 4 % HD == 0) {
+        dst[G * HD + j] = wt[32 * G + j];
+        dst[G * HD + G + j] = wt[33 * G + j];
+      }
+    }
+  }
+  __syncthreads();
+}
+
 // The warps' outputs joined, and those of the CTAs that share the item.
 template <int HD, int G>
 __device__ __forceinline__ void join_warps(const Params& p, Small& sm, uint8_t* smem, bool first_range) {
   using Sh = Shape<HD>;
   constexpr int W = Sh::W, OP = out_pitch(HD);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+  const int tid = threadIdx.x, cta = blockIdx.x;
   const int b = sm.b, g = sm.g, c_lo = sm.c_lo, np = sm.np;
   float* o = p.o + (long long)b * p.ld_o + (long long)g * G * HD;
   constexpr int NV = G * HD / 4;  // 4-vectors of the outputs
   float* part = p.part + (2ll * cta + (first_range ? 0 : 1)) * part_size(G, HD);
-  auto put_out = [&](int v, float4 a, float f) {  // o has no alignment of its own
-    o[v * 4] = a.x * f;
-    o[v * 4 + 1] = a.y * f;
-    o[v * 4 + 2] = a.z * f;
-    o[v * 4 + 3] = a.w * f;
-  };
-  auto add = [](float4& a, float f, const float4& x) {
-    a.x = fmaf(f, x.x, a.x);
-    a.y = fmaf(f, x.y, a.y);
-    a.z = fmaf(f, x.z, a.z);
-    a.w = fmaf(f, x.w, a.w);
-  };
   for (int v = tid; v < NV; v += Sh::kThreads) {
     const int j = v * 4 / HD;
     float R = -INFINITY;
@@ -502,11 +568,11 @@ __device__ __forceinline__ void join_warps(const Params& p, Small& sm, uint8_t* 
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       const float f = ex2(sm.r[w][j] - R);
-      add(a, f, *reinterpret_cast<const float4*>(smem + w * Sh::kWarpRing + (j * OP + v * 4 % HD) * 4));
+      add_scaled(a, f, *reinterpret_cast<const float4*>(smem + w * Sh::kWarpRing + (j * OP + v * 4 % HD) * 4));
       den = fmaf(f, sm.l[w][j], den);
     }
     if (np == 1) {
-      put_out(v, a, 1.0f / den);
+      put_out(o + v * 4, a, 1.0f / den);
     } else {
       reinterpret_cast<float4*>(part)[v] = a;
       if (v * 4 % HD == 0) {
@@ -518,10 +584,6 @@ __device__ __forceinline__ void join_warps(const Params& p, Small& sm, uint8_t* 
   __syncthreads();
   // ---------------------------------------------------- join the CTAs
   if (np > 1) {
-    const int slot0 = sm.slot0;
-    auto part_of = [&](int i) {
-      return p.part + (2ll * (c_lo + i) + (i == 0 ? slot0 : 0)) * part_size(G, HD);
-    };
     // Whether this CTA is the last of n to arrive at the counter, which is left at zero.
     auto last_of = [&](unsigned* ctr, int n) {
       if (tid == 0) {
@@ -534,65 +596,12 @@ __device__ __forceinline__ void join_warps(const Params& p, Small& sm, uint8_t* 
       __syncthreads();
       return sm.last != 0;
     };
-    // Join partials first, first + step, ... (n <= 32 of them): the first loads are on their way
-    // while one warp per head turns the references into weights.
-    float* wt = reinterpret_cast<float*>(smem);  // [32][G] weights, joined reference and sum per head
-    auto join = [&](int first, int step, int n, bool final) {
-      constexpr int NX = 2;
-      float4 x[NX];
-#pragma unroll
-      for (int i = 0; i < NX; ++i)
-        if (i < n && tid < NV) x[i] = __ldcg(reinterpret_cast<const float4*>(part_of(first + i * step)) + tid);
-      if (warp < G) {
-        const int j = warp;
-        float r = -INFINITY, l = 0.f;
-        if (lane < n) {
-          const float* q = part_of(first + lane * step) + G * HD;
-          r = __ldcg(q + j);
-          l = __ldcg(q + G + j);
-        }
-        const float R = warp_max(r);
-        const float f = lane < n ? ex2(r - R) : 0.f;
-        const float den = warp_sum(f * l);
-        wt[lane * G + j] = f;
-        if (lane == 0) {
-          wt[32 * G + j] = R;
-          wt[33 * G + j] = den;
-        }
-      }
-      __syncthreads();
-      float* dst = part_of(first);
-      for (int v = tid; v < NV; v += Sh::kThreads) {
-        const int j = v * 4 / HD;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i0 = 0; i0 < n; i0 += NX) {
-          if (i0 > 0 || v != tid) {
-#pragma unroll
-            for (int i = 0; i < NX; ++i)
-              if (i0 + i < n) x[i] = __ldcg(reinterpret_cast<const float4*>(part_of(first + (i0 + i) * step)) + v);
-          }
-#pragma unroll
-          for (int i = 0; i < NX; ++i)
-            if (i0 + i < n) add(a, wt[(i0 + i) * G + j], x[i]);
-        }
-        if (final) {
-          put_out(v, a, 1.0f / wt[33 * G + j]);
-        } else {
-          reinterpret_cast<float4*>(dst)[v] = a;
-          if (v * 4 % HD == 0) {
-            dst[G * HD + j] = wt[32 * G + j];
-            dst[G * HD + G + j] = wt[33 * G + j];
-          }
-        }
-      }
-      __syncthreads();
-    };
     const int me = cta - c_lo, grp = me / kJoin, ng = (np + kJoin - 1) / kJoin;
     unsigned* ctr = p.counter + (b * p.nkv + g) * kCounters;
     const int n1 = np - grp * kJoin < kJoin ? np - grp * kJoin : kJoin;
     if (last_of(ctr + 1 + grp, n1)) {
-      join(grp * kJoin, 1, n1, ng == 1);
-      if (ng > 1 && last_of(ctr, ng)) join(0, kJoin, ng, true);
+      join_parts<HD, G>(p, sm, smem, grp * kJoin, 1, n1, ng == 1);
+      if (ng > 1 && last_of(ctr, ng)) join_parts<HD, G>(p, sm, smem, 0, kJoin, ng, true);
     }
   }
 }
@@ -618,7 +627,6 @@ __global__ void __launch_bounds__(Shape<HD>::kThreads, Shape<HD>::kCtas) k_attn(
   uint8_t* ring = smem + warp * Sh::kWarpRing;
   const uint32_t ring_a = smem_addr(ring);
 
-  const int cta = blockIdx.x;
   if (warp == 0) {
     plan_work<TR, W>(p, sm);
     __syncwarp();

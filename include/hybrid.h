@@ -367,6 +367,43 @@ size_t hy_op_argmax_workspace(void);
 int hy_op_gemv_argmax(const void* W_dev, int32_t rows, int32_t cols, const float* x_dev, const float* norm_g_dev,
                       float eps, float* logits_dev, int32_t* id_dev, void* workspace_dev, void* stream);
 
+/* Beam search's selection: `groups` independent prompts of `beams` (1..16)
+ * hypotheses each.  logits_dev [groups * beams][ldl] FP32 are the beams' next
+ * token logits, score_dev [groups * beams] their log probabilities so far.
+ * Candidate (w, v) scores score[w] + logits[w][v] - log sum_u exp(logits[w][u]);
+ * each group's best `picks` (1..32, at most beams * vocab) candidates are
+ * written in order, best first: score_out_dev, parent_out_dev (beam w of the
+ * group) and token_out_dev (v), all [groups][picks].  Ties go to the lowest w *
+ * vocab + v; scores are compared in FP64 and written as FP32.  A beam with
+ * done_dev[w] != 0 (nullable: none) is not read and has one candidate, (w,
+ * eos) with its score unchanged; done_out_dev (nullable) tells which picks
+ * have ended (a done parent, or the token eos; eos < 0: no token ends a beam,
+ * only without done_dev).  A NaN logit counts as -infinity; a
+ * beam whose score is not finite, that has a +infinity logit or no finite
+ * one, has only candidates of score -infinity.  Those, like masked tokens,
+ * rank last in index order.  score_out_dev may be score_dev and done_out_dev
+ * may be done_dev where picks = beams.  workspace_dev:
+ * hy_op_beam_select_workspace() bytes, zeroed before its first use and then
+ * passed unmodified to later calls of the same sizes; calls that can overlap
+ * need a workspace each.  [Strata] "Act 0", pass 3 (selection on the device,
+ * a few bytes of result). */
+size_t hy_op_beam_select_workspace(int32_t groups, int32_t beams, int32_t vocab);
+int hy_op_beam_select(const float* logits_dev, int32_t ldl, int32_t groups, int32_t beams, int32_t vocab,
+                      int32_t picks, const float* score_dev, const int32_t* done_dev, int32_t eos,
+                      float* score_out_dev, int32_t* parent_out_dev, int32_t* token_out_dev, int32_t* done_out_dev,
+                      void* workspace_dev, void* stream);
+
+/* The states of groups * beams hypotheses reordered in place: state i of a
+ * group becomes what state parent_dev[group * beams + i] of the group was
+ * (repeats allowed; states that keep themselves are not touched).  State j
+ * starts at state_dev + j * beam_stride and consists of n_seg segments of
+ * seg_bytes bytes, seg_stride bytes apart; bytes between the segments stay.
+ * state_dev 16-byte aligned, strides and sizes (bytes) multiples of 16, and
+ * neither segments nor states may overlap.  A parent outside [0, beams)
+ * leaves its state as it is (HY_GUARD_BAD_INDEX). */
+int hy_op_beam_reorder(void* state_dev, int64_t beam_stride, int32_t n_seg, int64_t seg_stride, int64_t seg_bytes,
+                       int32_t groups, int32_t beams, const int32_t* parent_dev, void* stream);
+
 /* One Gated DeltaNet decode step of one layer at position *pos_dev:
  * y_dev = projection output [2*nh*dk + nh*dv + 2*nh] (q|k|v|a|b), conv_w
  * bf16 [channels][conv_k], conv_state FP32 ring [conv_k][channels] (slot
