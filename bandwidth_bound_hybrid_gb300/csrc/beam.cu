@@ -5,16 +5,21 @@
 //   s(w, v) = score_w + x_wv - lse_w,  lse_w = log sum_v exp(x_wv),
 // and the group's best `picks` are wanted, ties to the lowest w V + v.  Within
 // a beam the order is that of the logits, so one pass over the logits is
-// enough: every CTA takes a chunk of a beam's row into registers and leaves
-// the chunk's maximum, its sum of exponentials and its best `picks` logits;
-// the last CTA of the group turns the maxima and sums into lse_w (in FP64, as
-// the scores are: candidates of different beams differ in their last bits)
-// and selects among the chunks' lists.  Bound by reading the logits once.
+// enough.  A CTA takes a chunk of a beam's row and streams through it with a
+// running maximum and sum of exponentials per lane.  The picks-th largest of
+// the CTA's 256 running maxima is a bound that `picks` logits are known to
+// reach; it is worked out after 1, 2, 4, 8, ... steps (a bitonic network across
+// the lanes of each warp, then merges of the 8 lists), so that between two of
+// these about `picks` logits reach it.  Those few are kept, by each warp on its
+// own: 32 at a time are sorted and merged into the warp's best 32, a lane
+// each.  So the pass costs an exponential and a comparison a logit, and is
+// bound by reading the logits.
 //
-// A chunk's best: the picks-th largest of a warp's 32 lane maxima is a bound
-// that at least `picks` values reach, so only the values that reach the best
-// such bound of the CTA (a few dozen) are ranked, each counting its betters.
-// The group's best are found in the same way from the lists' heads.
+// The CTA leaves the chunk's maximum, sum and best `picks`; the last CTA of the
+// group turns maxima and sums into lse_w (log of the mantissa in FP32, the
+// rest in FP64, as the scores are: candidates of different beams differ in
+// their last bits) and selects among the chunks' lists by the same kind of
+// bound, from the lists' heads.
 //
 // Reordering.  State i of a group becomes what state parent[i] was, in place:
 // a thread owns one 16-byte column of all the group's states, reads the
@@ -32,7 +37,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kPer = kChunk / kThreads;  // logits of a thread
+constexpr int kCtas = 4;                 // CTAs of the selection per SM
+constexpr int kPer = 16;                 // logits of a lane at a time
+constexpr int kStep = kPer * 32;         // and of a warp
+constexpr int kFew = 4;                  // words of a thread in the final selection of few lists
 constexpr int kQual = 1024;              // lists looked into by the fast final selection
 constexpr int kBest = 2048;              // and their candidates
 
@@ -45,8 +53,8 @@ __device__ __forceinline__ uint64_t word_of(uint32_t key, uint32_t token) {
 __device__ __forceinline__ float word_logit(uint64_t c) { return key_value((uint32_t)(c >> 32)); }
 __device__ __forceinline__ uint32_t word_token(uint64_t c) { return 0xffffffffu - (uint32_t)c; }
 
-// The n-th largest (n in 1..32) of the lanes' keys: a bitonic sort across the warp.
-__device__ __forceinline__ uint32_t warp_nth(uint32_t v, int n, int lane) {
+// The lanes' keys sorted across the warp by a bitonic network, largest in lane 0.
+__device__ __forceinline__ uint32_t warp_sort32(uint32_t v, int lane) {
 #pragma unroll
   for (int k = 2; k <= 32; k <<= 1) {
 #pragma unroll
@@ -56,26 +64,68 @@ __device__ __forceinline__ uint32_t warp_nth(uint32_t v, int n, int lane) {
       v = larger ? max(v, o) : min(v, o);
     }
   }
-  return __shfl_sync(0xffffffffu, v, n - 1);
+  return v;
+}
+// The n-th largest (n in 1..32) of the lanes' keys.
+__device__ __forceinline__ uint32_t warp_nth(uint32_t v, int n, int lane) {
+  return __shfl_sync(0xffffffffu, warp_sort32(v, lane), n - 1);
 }
 
-// A candidate of the group: FP64 score and flat index w V + v.
+// Sorted across the warp, largest in lane 0: a step of a bitonic network, the
+// last log2 steps of it (the lanes' words a bitonic sequence), and all of it.
+__device__ __forceinline__ uint64_t keep(uint64_t x, int j, bool larger) {
+  const uint64_t o = __shfl_xor_sync(0xffffffffu, (unsigned long long)x, j);
+  return (o > x) == larger ? o : x;
+}
+__device__ __forceinline__ uint64_t warp_merge(uint64_t x, int lane) {
+#pragma unroll
+  for (int j = 16; j > 0; j >>= 1) x = keep(x, j, (lane & j) == 0);
+  return x;
+}
+__device__ __forceinline__ uint64_t warp_sort(uint64_t x, int lane) {
+#pragma unroll
+  for (int k = 2; k < 32; k <<= 1) {
+#pragma unroll
+    for (int j = k >> 1; j > 0; j >>= 1) x = keep(x, j, ((lane & k) == 0) == ((lane & j) == 0));
+  }
+  return warp_merge(x, lane);
+}
+// The best 32 of two sorted lists, sorted (`other` in reverse: lane 31 its largest).
+__device__ __forceinline__ uint64_t warp_join(uint64_t top, uint64_t other, int lane) {
+  return warp_merge(top > other ? top : other, lane);
+}
+
+// A candidate of the group: its FP64 score as an order key (0: none; integer
+// compares, since FP64 ones are slow here) and flat index w V + v.
 struct Cand {
-  double s;
+  uint64_t key;
   uint32_t i;
 };
-__device__ __forceinline__ bool better(const Cand& a, const Cand& b) { return a.s > b.s || (a.s == b.s && a.i < b.i); }
+__device__ __forceinline__ Cand cand_of(double s, uint32_t i) {
+  if (!(s >= -(double)FLT_MAX)) return {0, 0xffffffffu};  // the FP32 score is -infinity
+  const uint64_t b = (uint64_t)__double_as_longlong(s + 0.0);  // (-0 as +0)
+  return {(b >> 63) ? ~b : b | (1ull << 63), i};
+}
+__device__ __forceinline__ double cand_score(const Cand& c) {
+  if (c.key == 0) return -INFINITY;
+  return __longlong_as_double((long long)((c.key >> 63) ? c.key & ~(1ull << 63) : ~c.key));
+}
+__device__ __forceinline__ bool better(const Cand& a, const Cand& b) { return a.key > b.key || (a.key == b.key && a.i < b.i); }
 
 struct Shared {
   union {
-    uint64_t list[kChunk];             // a chunk's candidates
     struct {
-      double s[kBest];                 // the group's candidates
+      uint64_t buf[kWarps][64];        // candidates on their way into the warp's best
+      uint64_t list[kWarps][32];       // the warps' best
+    } w;
+    struct {
+      uint64_t key[kBest];             // the group's candidates
       uint32_t i[kBest];
       uint32_t qual[kQual];
     } best;
     uint8_t at[kMaxLists];             // one by one: the next candidate of every list
   };
+  uint32_t sorted[2][kWarps][32];      // running maxima of the warps' lanes
   uint32_t key[kWarps];
   float m[kWarps], sum[kWarps];
   double off[kMaxBeams];               // score_w - lse_w, or score_w of a done beam (-infinity: nothing counts)
@@ -84,7 +134,7 @@ struct Shared {
   int n, nq, last;
 };
 
-__global__ void __launch_bounds__(kThreads) k_select(const SelectParams p) {
+__global__ void __launch_bounds__(kThreads, kCtas) k_select(const SelectParams p) {
   __shared__ Shared sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nch = p.chunks, row = blockIdx.x / nch, chunk = blockIdx.x % nch, group = row / p.beams;
@@ -92,58 +142,109 @@ __global__ void __launch_bounds__(kThreads) k_select(const SelectParams p) {
   if (!(p.done && p.done[row])) {
     // ------------------------------------------------------ the chunk
     const float* x = p.logits + (long long)row * p.ld;
-    const int base = chunk * kChunk;
-    float v[kPer], m = -INFINITY;
+    const long long first = (long long)chunk * p.span;
+    const int end = (int)(first + p.span < V ? first + p.span : V);
+    uint64_t* buf = sm.w.buf[warp];
+    uint64_t top = 0;  // 0: none
+    int nb = 0;        // words in the buffer
+    float M = -INFINITY, s = 0.f;
+    auto flush = [&]() {  // the buffer's first 32 words into the best, the others to its front
+      __syncwarp();
+      const uint64_t w = lane < nb ? buf[lane] : 0, rest = buf[32 + lane];
+      __syncwarp();
+      buf[lane] = rest;
+      nb = nb > 32 ? nb - 32 : 0;
+      top = warp_join(top, __shfl_sync(0xffffffffu, (unsigned long long)warp_sort(w, lane), 31 - lane), lane);
+    };
+    float low = -FLT_MAX;  // -infinity is no candidate
+    const int steps = (int)((end - first + kWarps * kStep - 1) / (kWarps * kStep));
+    float v[kPer], next[kPer];  // a step's logits; the next step's are on their way meanwhile
+    auto load = [&](int it, float* d) {
+      const int i0 = (int)first + (it * kWarps + warp) * kStep;
+      const float* q = x + i0 + lane;
+      if (i0 + kStep <= end) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int i = base + k * kThreads + tid;
-      v[k] = i < V ? __ldcs(x + i) : -INFINITY;
-    }
+        for (int k = 0; k < kPer; ++k) d[k] = __ldcs(q + k * 32);
+      } else {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      v[k] = v[k] == v[k] ? v[k] : -INFINITY;  // a NaN counts as -infinity
-      m = fmaxf(m, v[k]);
+        for (int k = 0; k < kPer; ++k) d[k] = i0 + k * 32 + lane < end ? __ldcs(q + k * 32) : -INFINITY;
+      }
+    };
+    load(0, next);
+#pragma unroll 2
+    for (int it = 0; it < steps; ++it) {
+      const int i0 = (int)first + (it * kWarps + warp) * kStep + lane;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) v[k] = next[k];
+      if (it + 1 < steps) load(it + 1, next);
+      float m = v[0];
+#pragma unroll
+      for (int k = 1; k < kPer; ++k) m = fmaxf(m, v[k]);
+      m = fmaxf(m, -INFINITY);
+      const float Mn = fmaxf(M, m), ref = Mn == -INFINITY ? 0.f : Mn;
+      float add = 0.f;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) add += __expf(v[k] - ref);
+      if (add != add) {  // a NaN counts as -infinity (+infinity leaves NaN: the beam has no finite scores)
+        add = 0.f;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) add += __expf(fmaxf(v[k], -INFINITY) - ref);
+      }
+      s = s * __expf(M - ref) + add;
+      M = Mn;
+      if ((it & (it + 1)) == 0 && (it == 0 || it + 1 < steps)) {  // 1, 2, 4, ... steps done
+        uint32_t(*sorted)[32] = sm.sorted[__popc(it) & 1];
+        sorted[warp][lane] = warp_sort32(order_key(M), lane);
+        __syncthreads();
+        uint32_t best = sorted[0][lane];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+          best = max(best, sorted[w][31 - lane]);
+#pragma unroll
+          for (int j = 16; j > 0; j >>= 1) {
+            const uint32_t o = __shfl_xor_sync(0xffffffffu, best, j);
+            best = (lane & j) == 0 ? max(best, o) : min(best, o);
+          }
+        }
+        low = fmaxf(low, key_value(__shfl_sync(0xffffffffu, best, P - 1)));
+      }
+      if (__any_sync(0xffffffffu, m >= low)) {
+        uint32_t hit = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) hit |= v[k] >= low ? 1u << k : 0u;
+        for (unsigned in; (in = __ballot_sync(0xffffffffu, hit != 0)) != 0; hit &= hit - 1) {
+          if (hit) {
+            const int i = i0 + (__ffs(hit) - 1) * 32;
+            buf[nb + __popc(in & ((1u << lane) - 1))] = word_of(order_key(x[i]), i);
+          }
+          nb += __popc(in);
+          if (nb >= 32) flush();
+        }
+      }
     }
-    const uint32_t nth = warp_nth(order_key(m), P, lane);
-    const float wm = warp_max(m);
+    flush();
+    // the warps' lists, maxima and sums
+    const float Mw = warp_max(M);
+    const float sw = warp_sum(M > -INFINITY ? s * __expf(M - Mw) : 0.f);
     if (lane == 0) {
-      sm.key[warp] = nth;
-      sm.m[warp] = wm;
+      sm.m[warp] = Mw;
+      sm.sum[warp] = sw;
     }
-    if (tid == 0) sm.n = 0;
-    __syncthreads();
-    uint32_t bound = order_key(-INFINITY) + 1;  // -infinity is no candidate
-    float M = -INFINITY;
+    sm.w.list[warp][lane] = top;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      bound = max(bound, sm.key[w]);
-      M = fmaxf(M, sm.m[w]);
+    for (int half = kWarps / 2; half > 0; half >>= 1) {
+      __syncthreads();
+      if (warp < half) sm.w.list[warp][lane] = top = warp_join(top, sm.w.list[warp + half][31 - lane], lane);
     }
-    const float low = key_value(bound);
-    float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      s += __expf(v[k] - M);
-      if (v[k] >= low) sm.list[atomicAdd(&sm.n, 1)] = word_of(order_key(v[k]), base + k * kThreads + tid);
-    }
-    s = warp_sum(s);
-    if (lane == 0) sm.sum[warp] = s;
-    __syncthreads();
-    const int n = sm.n;
     const long long slot = (long long)row * nch + chunk;
-    uint64_t* out = p.lists + slot * P;
-    for (int a = tid; a < n; a += kThreads) {
-      const uint64_t c = sm.list[a];
-      int rank = 0;
-      for (int b = 0; b < n && rank < P; ++b) rank += sm.list[b] > c;
-      if (rank < P) out[rank] = c;
-    }
-    if (tid >= n && tid < P) out[tid] = 0;
+    if (warp == 0 && lane < P) p.lists[slot * P + lane] = top;
     if (tid == 0) {
-      float S = 0.f;
+      float Mc = sm.m[0], S = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) S += sm.sum[w];
-      p.stats[slot] = make_float2(M, S);  // M -infinity: S is NaN and not read
+      for (int w = 1; w < kWarps; ++w) Mc = fmaxf(Mc, sm.m[w]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) S += sm.m[w] > -INFINITY ? sm.sum[w] * __expf(sm.m[w] - Mc) : 0.f;
+      p.stats[slot] = make_float2(Mc, S);
     }
   }
   // -------------------------------------------------------- the last CTA of the group
@@ -159,22 +260,34 @@ __global__ void __launch_bounds__(kThreads) k_select(const SelectParams p) {
   __syncthreads();
   if (!sm.last) return;
   const int row0 = group * p.beams, nl = p.beams * nch;
+  const unsigned long long* lists = reinterpret_cast<const unsigned long long*>(p.lists) + (long long)row0 * nch * P;
+  // up to kFew words a thread: all of the group's lists at once, on their way while lse is worked out
+  const bool few = nl * P <= kFew * kThreads;
+  uint64_t words[kFew];
+#pragma unroll
+  for (int k = 0; k < kFew; ++k) words[k] = few && tid + k * kThreads < nl * P ? __ldcg(lists + tid + k * kThreads) : 0;
   for (int w = warp; w < p.beams; w += kWarps) {  // lse and offset of every beam
-    const int r = row0 + w, done = p.done && p.done[r];
+    const int r = row0 + w;
+    const float2* st = p.stats + (long long)r * nch;
+    const float2 t0 = lane < nch ? __ldcg(st + lane) : make_float2(-INFINITY, 0.f);
+    const int done = p.done ? p.done[r] != 0 : 0;
     double off = (double)p.score[r];
     if (!done) {
-      const float2* st = p.stats + (long long)r * nch;
-      float M = -INFINITY;
-      for (int c = lane; c < nch; c += 32) M = fmaxf(M, __ldcg(st + c).x);
+      float M = t0.x;
+      for (int c = lane + 32; c < nch; c += 32) M = fmaxf(M, __ldcg(st + c).x);
       M = warp_max(M);
-      double S = 0;
-      for (int c = lane; c < nch; c += 32) {
+      double S = t0.x > -INFINITY ? (double)(t0.y * expf(t0.x - M)) : 0.0;
+      for (int c = lane + 32; c < nch; c += 32) {
         const float2 t = __ldcg(st + c);
-        if (t.x > -INFINITY) S += (double)t.y * exp((double)t.x - (double)M);
+        if (t.x > -INFINITY) S += (double)(t.y * expf(t.x - M));
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
-      off -= (double)M + log(S);
+      // S = 2^e f, f in [0.75, 1.5): the FP32 logarithm of f errs by 2^-25 at most, e log 2 is FP64
+      const float Sf = (float)S;
+      const int e = (int)((__float_as_uint(Sf) + 0x00400000u) >> 23) - 127;
+      const float f = __uint_as_float(__float_as_uint(Sf) - ((uint32_t)e << 23));
+      off -= (double)M + (double)e * 0.69314718055994530942 + (double)(logf(f) + (float)(S - (double)Sf) / Sf);
     }
     if (lane == 0) {
       sm.off[w] = off - off == 0.0 ? off : -INFINITY;
@@ -182,57 +295,63 @@ __global__ void __launch_bounds__(kThreads) k_select(const SelectParams p) {
     }
   }
   __syncthreads();
-  // candidate k of list l = (beam, chunk); -infinity: none
-  auto get = [&](int l, int k) {
-    const int w = l / nch, c = l % nch;
-    Cand a = {-INFINITY, 0xffffffffu};
+  // candidate k of list l = (beam, chunk), its word given
+  auto cand = [&](int l, int k, uint64_t word) {
+    const int w = l / nch;
     const double off = sm.off[w];
-    if (off == -INFINITY) return a;
-    if (sm.done[w]) {  // a beam that has ended goes on as it is
-      if (c == 0 && k == 0) a = {off, (uint32_t)w * V + p.eos};
-      return a;
-    }
-    const uint64_t word = __ldcg(reinterpret_cast<const unsigned long long*>(p.lists) + ((long long)row0 * nch + l) * P + k);
-    if (word) a = {off + (double)word_logit(word), (uint32_t)w * V + word_token(word)};
-    if (a.s < -(double)FLT_MAX) a = {-INFINITY, 0xffffffffu};  // the FP32 score is -infinity
-    return a;
+    if (sm.done[w])  // a beam that has ended goes on as it is
+      return l == w * nch && k == 0 ? cand_of(off, (uint32_t)w * V + p.eos) : Cand{0, 0xffffffffu};
+    return word ? cand_of(off + (double)word_logit(word), (uint32_t)w * V + word_token(word)) : Cand{0, 0xffffffffu};
   };
-  // order key of a score rounded down: at least as many candidates reach it as reach the score
-  auto key_of = [](double s) { return order_key(__double2float_rd(s)); };
-  uint32_t mine = 0;
-  for (int l = tid; l < nl; l += kThreads) mine = max(mine, key_of(get(l, 0).s));
-  const uint32_t nth = warp_nth(mine, P, lane);
+  auto get = [&](int l, int k) { return cand(l, k, sm.done[l / nch] ? 0 : __ldcg(lists + (long long)l * P + k)); };
+  auto keep_if = [&](const Cand& a, uint32_t bound) {
+    if ((uint32_t)(a.key >> 32) < bound) return;
+    const int at = atomicAdd(&sm.n, 1);
+    if (at < kBest) {
+      sm.best.key[at] = a.key;
+      sm.best.i[at] = a.i;
+    }
+  };
+  // a bound on the upper half of the keys that at least P candidates reach: the P-th largest of a warp's lanes
+  Cand mine[kFew];
+  uint32_t top_key = 0;
+  if (few) {
+#pragma unroll
+    for (int k = 0; k < kFew; ++k) {
+      const int at = tid + k * kThreads;
+      mine[k] = at < nl * P ? cand(at / P, at % P, words[k]) : Cand{0, 0xffffffffu};
+      top_key = max(top_key, (uint32_t)(mine[k].key >> 32));
+    }
+  } else {
+    for (int l = tid; l < nl; l += kThreads) top_key = max(top_key, (uint32_t)(get(l, 0).key >> 32));
+  }
+  const uint32_t nth = warp_nth(top_key, P, lane);
   if (lane == 0) sm.key[warp] = nth;
   __syncthreads();
-  uint32_t bound = order_key(-INFINITY) + 1;
+  uint32_t bound = 1;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) bound = max(bound, sm.key[w]);
-  for (int l = tid; l < nl; l += kThreads)
-    if (key_of(get(l, 0).s) >= bound) {
-      const int q = atomicAdd(&sm.nq, 1);
-      if (q < kQual) sm.best.qual[q] = l;
-    }
-  __syncthreads();
-  const int nq = sm.nq;
-  if (nq <= kQual) {
-    for (int q = warp; q < nq; q += kWarps) {
-      const Cand a = lane < P ? get(sm.best.qual[q], lane) : Cand{-INFINITY, 0xffffffffu};
-      if (key_of(a.s) >= bound) {
-        const int at = atomicAdd(&sm.n, 1);
-        if (at < kBest) {
-          sm.best.s[at] = a.s;
-          sm.best.i[at] = a.i;
-        }
+  if (few) {
+#pragma unroll
+    for (int k = 0; k < kFew; ++k) keep_if(mine[k], bound);
+  } else {
+    for (int l = tid; l < nl; l += kThreads)
+      if ((uint32_t)(get(l, 0).key >> 32) >= bound) {
+        const int q = atomicAdd(&sm.nq, 1);
+        if (q < kQual) sm.best.qual[q] = l;
       }
-    }
+    __syncthreads();
+    for (int q = warp; q < min(sm.nq, kQual); q += kWarps)
+      if (lane < P) keep_if(get(sm.best.qual[q], lane), bound);
   }
   __syncthreads();
+  const int nq = sm.nq;
   int n = sm.n;
   if (nq <= kQual && n <= kBest) {
     for (int a = tid; a < n; a += kThreads) {
-      const Cand c = {sm.best.s[a], sm.best.i[a]};
+      const Cand c = {sm.best.key[a], sm.best.i[a]};
       int rank = 0;
-      for (int b = 0; b < n && rank < P; ++b) rank += better({sm.best.s[b], sm.best.i[b]}, c);
+      for (int b = 0; b < n && rank < P; ++b) rank += better({sm.best.key[b], sm.best.i[b]}, c);
       if (rank < P) sm.sel[rank] = c;
     }
     if (n > P) n = P;
@@ -241,7 +360,7 @@ __global__ void __launch_bounds__(kThreads) k_select(const SelectParams p) {
     __syncthreads();
     for (int l = tid; l < nl; l += kThreads) sm.at[l] = 0;
     for (n = 0; n < P; ++n) {
-      Cand best = {-INFINITY, 0xffffffffu};
+      Cand best = {0, 0xffffffffu};
       int from = -1;
       for (int l = tid; l < nl; l += kThreads) {
         if (sm.at[l] >= P) continue;
@@ -254,7 +373,8 @@ __global__ void __launch_bounds__(kThreads) k_select(const SelectParams p) {
       Cand top = best;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
-        const Cand a = {__shfl_xor_sync(0xffffffffu, top.s, o), __shfl_xor_sync(0xffffffffu, top.i, o)};
+        const Cand a = {__shfl_xor_sync(0xffffffffu, (unsigned long long)top.key, o),
+                        __shfl_xor_sync(0xffffffffu, top.i, o)};
         if (better(a, top)) top = a;
       }
       if (lane == 0) sm.top[warp] = top;
@@ -263,7 +383,7 @@ __global__ void __launch_bounds__(kThreads) k_select(const SelectParams p) {
 #pragma unroll
       for (int w = 1; w < kWarps; ++w)
         if (better(sm.top[w], top)) top = sm.top[w];
-      if (top.s == -INFINITY) break;  // the same for every thread
+      if (top.key == 0) break;  // the same for every thread
       if (from >= 0 && best.i == top.i) ++sm.at[from];
       if (tid == 0) sm.sel[n] = top;
       __syncthreads();
@@ -279,13 +399,13 @@ __global__ void __launch_bounds__(kThreads) k_select(const SelectParams p) {
     for (int k = 0; k < n; ++k) taken |= sm.sel[k].i == (uint32_t)lane;
     const unsigned free = __ballot_sync(0xffffffffu, !taken && lane < P);
     const int before = __popc(free & ((1u << lane) - 1));
-    if (!taken && lane < P && n + before < P) sm.sel[n + before] = {-INFINITY, (uint32_t)lane};
+    if (!taken && lane < P && n + before < P) sm.sel[n + before] = {0, (uint32_t)lane};
     __syncwarp();
     if (lane < P) {
       const Cand c = sm.sel[lane];
       const int w = (int)(c.i / (uint32_t)V), token = (int)(c.i % (uint32_t)V);
       const long long at = (long long)group * P + lane;
-      p.score_out[at] = (float)c.s;
+      p.score_out[at] = (float)cand_score(c);
       p.parent[at] = w;
       p.token[at] = token;
       if (p.done_out) p.done_out[at] = (sm.done[w] || token == p.eos) ? 1 : 0;
@@ -336,6 +456,22 @@ __global__ void __launch_bounds__(kThreads) k_reorder(const ReorderParams p) {
 }  // namespace
 
 int chunks(int vocab) { return (int)(((long long)vocab + kChunk - 1) / kChunk); }
+
+// Tiles of kChunk logits a CTA takes: the split of a row whose waves of CTAs
+// (kCtas an SM) take least, a CTA costing about three tiles besides its own.
+void set_span(SelectParams* p, int groups, int nsm) {
+  const long long rows = (long long)groups * p->beams, n = chunks(p->vocab), slots = (long long)nsm * kCtas;
+  long long best = -1;
+  for (long long c = 1; c <= n && c <= 4096; ++c) {
+    const long long t = (n + c - 1) / c, parts = (n + t - 1) / t;
+    const long long cost = (rows * parts + slots - 1) / slots * (t + 3);
+    if (best < 0 || cost < best) {
+      best = cost;
+      p->chunks = (int)parts;
+      p->span = t * kChunk;
+    }
+  }
+}
 
 cudaError_t select(const SelectParams& p, int groups, cudaStream_t st) {
   const long long grid = (long long)groups * p.beams * p.chunks;

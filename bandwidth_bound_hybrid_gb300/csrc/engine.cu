@@ -2279,7 +2279,7 @@ int hy_op_beam_select(const float* logits_dev, int32_t ldl, int32_t groups, int3
   p.vocab = vocab;
   p.beams = beams;
   p.picks = picks;
-  p.chunks = beam::chunks(vocab);
+  beam::set_span(&p, groups, op_nsm());
   p.score = score_dev;
   p.done = done_dev;
   p.eos = eos;

@@ -246,12 +246,14 @@ cudaError_t append(const AppendParams& p, int hd, cudaStream_t st);
 namespace beam {
 constexpr int kMaxBeams = 16;    // beams of a group
 constexpr int kMaxPicks = 32;    // picks of a group: a lane each
-constexpr int kChunk = 4096;     // logits of a CTA
+constexpr int kChunk = 4096;     // logits of a CTA: a multiple of this
 constexpr int kMaxLists = 32768; // beams x chunks of a group
 struct SelectParams {
   const float* logits;           // [groups * beams][ld]
   long long ld;
-  int vocab, beams, picks, chunks;
+  int vocab, beams, picks;
+  int chunks;                    // of a row, span logits each (set_span)
+  long long span;
   const float* score;            // [groups * beams]
   const int* done;               // [groups * beams] (nullable)
   int eos;
@@ -263,7 +265,8 @@ struct SelectParams {
   float2* stats;                 // [groups * beams][chunks]: maximum, sum of exponentials
   uint64_t* lists;               // [groups * beams][chunks][picks]
 };
-int chunks(int vocab);
+int chunks(int vocab);           // the most a row is cut into
+void set_span(SelectParams* p, int groups, int nsm);
 cudaError_t select(const SelectParams& p, int groups, cudaStream_t st);
 
 // Segment s of state i of group z: seg_bytes bytes at base[i] + z * group_stride

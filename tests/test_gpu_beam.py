@@ -112,7 +112,8 @@ def inputs(groups, beams, V, seed, spread=2.5):
 
 @pytest.mark.parametrize("groups,beams,V,picks", [
     (1, 1, 1, 1), (1, 1, 2, 2), (1, 2, 3, 6), (3, 2, 31, 4), (1, 4, 1024, 4), (2, 8, 4096, 8), (2, 8, 4097, 16),
-    (1, 16, 5000, 32), (5, 3, 12289, 6), (1, 1, 151936, 32), (70, 1, 700, 2), (1, 7, 33000, 9)])
+    (1, 16, 5000, 32), (5, 3, 12289, 6), (1, 1, 151936, 32), (70, 1, 700, 2), (1, 7, 33000, 9),
+    (8, 16, 60000, 8), (130, 2, 40001, 3), (1000, 1, 4500, 2)])
 def test_select(L, groups, beams, V, picks):
     _, logits, score = inputs(groups, beams, V, V + picks)
     got = run_select(L, logits, score, None, -1, groups, beams, picks, ld=V + (V % 3))
@@ -156,6 +157,8 @@ def test_select_masked_tokens(L):
     for picks in (1, 6, 20):
         got = run_select(L, masked, score, None, 4, 4, 3, picks)
         check(got, masked, score, None, 4, 4, 3, picks)
+    lowest = np.full_like(masked, np.finfo(np.float32).min)  # every token alike, at the lowest value
+    check(run_select(L, lowest, score, None, 4, 4, 3, 6), lowest, score, None, 4, 4, 3, 6)
     masked[9:] = np.nan  # nothing at all: the first candidates in index order, with score -infinity
     got = run_select(L, masked, score, None, 4, 4, 3, 5)
     check(got, masked, score, None, 4, 4, 3, 5)
