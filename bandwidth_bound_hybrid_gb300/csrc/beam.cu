@@ -66,9 +66,21 @@ __device__ __forceinline__ uint32_t warp_sort32(uint32_t v, int lane) {
   }
   return v;
 }
-// The n-th largest (n in 1..32) of the lanes' keys.
-__device__ __forceinline__ uint32_t warp_nth(uint32_t v, int n, int lane) {
-  return __shfl_sync(0xffffffffu, warp_sort32(v, lane), n - 1);
+// The n-th largest (n in 1..32) of all the CTA's keys: the warps' sorted lists merged (every warp by itself).
+__device__ __forceinline__ uint32_t cta_nth(uint32_t (*sorted)[32], uint32_t v, int n, int lane, int warp) {
+  sorted[warp][lane] = warp_sort32(v, lane);
+  __syncthreads();
+  uint32_t best = sorted[0][lane];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) {
+    best = max(best, sorted[w][31 - lane]);
+#pragma unroll
+    for (int j = 16; j > 0; j >>= 1) {
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, best, j);
+      best = (lane & j) == 0 ? max(best, o) : min(best, o);
+    }
+  }
+  return __shfl_sync(0xffffffffu, best, n - 1);
 }
 
 // Sorted across the warp, largest in lane 0: a step of a bitonic network, the
@@ -126,7 +138,6 @@ struct Shared {
     uint8_t at[kMaxLists];             // one by one: the next candidate of every list
   };
   uint32_t sorted[2][kWarps][32];      // running maxima of the warps' lanes
-  uint32_t key[kWarps];
   float m[kWarps], sum[kWarps];
   double off[kMaxBeams];               // score_w - lse_w, or score_w of a done beam (-infinity: nothing counts)
   int done[kMaxBeams];
@@ -193,20 +204,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_select(const SelectParams p
       s = s * __expf(M - ref) + add;
       M = Mn;
       if ((it & (it + 1)) == 0 && (it == 0 || it + 1 < steps)) {  // 1, 2, 4, ... steps done
-        uint32_t(*sorted)[32] = sm.sorted[__popc(it) & 1];
-        sorted[warp][lane] = warp_sort32(order_key(M), lane);
-        __syncthreads();
-        uint32_t best = sorted[0][lane];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-          best = max(best, sorted[w][31 - lane]);
-#pragma unroll
-          for (int j = 16; j > 0; j >>= 1) {
-            const uint32_t o = __shfl_xor_sync(0xffffffffu, best, j);
-            best = (lane & j) == 0 ? max(best, o) : min(best, o);
-          }
-        }
-        low = fmaxf(low, key_value(__shfl_sync(0xffffffffu, best, P - 1)));
+        low = fmaxf(low, key_value(cta_nth(sm.sorted[__popc(it) & 1], order_key(M), P, lane, warp)));
       }
       if (__any_sync(0xffffffffu, m >= low)) {
         uint32_t hit = 0;
@@ -312,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_select(const SelectParams p
       sm.best.i[at] = a.i;
     }
   };
-  // a bound on the upper half of the keys that at least P candidates reach: the P-th largest of a warp's lanes
+  // a bound on the upper half of the keys that at least P candidates reach: the P-th largest of the threads'
   Cand mine[kFew];
   uint32_t top_key = 0;
   if (few) {
@@ -325,12 +323,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_select(const SelectParams p
   } else {
     for (int l = tid; l < nl; l += kThreads) top_key = max(top_key, (uint32_t)(get(l, 0).key >> 32));
   }
-  const uint32_t nth = warp_nth(top_key, P, lane);
-  if (lane == 0) sm.key[warp] = nth;
-  __syncthreads();
-  uint32_t bound = 1;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) bound = max(bound, sm.key[w]);
+  const uint32_t bound = max(cta_nth(sm.sorted[0], top_key, P, lane, warp), 1u);
   if (few) {
 #pragma unroll
     for (int k = 0; k < kFew; ++k) keep_if(mine[k], bound);
