@@ -34,7 +34,10 @@ def gdn_state_bytes_per_layer(nh: int, dk: int, dv: int) -> int:
 
 def kv_bytes_per_token(n_attn: int, nkv: int, hd: int, elem: int = BF16, kv_format: int = 0) -> int:
     """K and V of one position over all attention layers: bf16 elements, or
-    int8 codes plus one FP32 scale per cached vector (kv_format 1)."""
+    int8 codes plus one FP32 scale per cached vector (kv_format 1), or 4-bit
+    codes plus one fp16 scale per 32 values (kv_format 2)."""
+    if kv_format == 2:
+        return n_attn * 2 * nkv * (hd // 2 + hd // 32 * 2)
     if kv_format == 1:
         return n_attn * 2 * nkv * (hd + F32)
     return n_attn * 2 * nkv * hd * elem

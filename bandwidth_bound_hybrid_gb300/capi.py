@@ -70,6 +70,8 @@ SIGNATURES = {
     "hy_seq_reset": (ctypes.c_int, [vp, i32, vp]),
     "hy_seq_len": (i32, [vp, i32]),
     "hy_seq_capacity": (i32, [vp, i32]),
+    "hy_seq_copy": (ctypes.c_int, [vp, i32, i32, vp]),
+    "hy_seq_reorder": (ctypes.c_int, [vp, P(i32), i32, vp, i32, vp]),
     "hy_step_kernels": (i32, [vp]),
     "hy_step_splits": (i32, [vp, i32]),
     "hy_experts_read": (ctypes.c_int, [vp, vp, vp]),

@@ -22,6 +22,7 @@
 #include "../../include/hybrid.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "kv4_dev.cuh"
 
 using namespace hy;
 
@@ -111,6 +112,18 @@ __global__ void k_fill_i8(int8_t* dst, float* scales, long long rows, int row_le
   }
 }
 
+// 4-bit cache rows: the same seeded values, each block of 32 quantised by the
+// cache's rule.  One warp per block.
+__global__ void k_fill_q4(uint8_t* codes, uint16_t* scales, long long blocks, uint64_t seed) {
+  const int lane = threadIdx.x & 31;
+  for (long long r = (blockIdx.x * (long long)blockDim.x + threadIdx.x) >> 5; r < blocks;
+       r += ((long long)gridDim.x * blockDim.x) >> 5) {
+    int code;
+    const uint16_t s = kv4::quant_block(synth_value(seed, (uint64_t)(r * 32 + lane), 1.0f), &code);
+    kv4::store_block(s, code, codes + r * 16, scales + r, nullptr, lane);
+  }
+}
+
 __global__ void k_fill_f32(float* dst, long long n, uint64_t seed, float scale) {
   for (long long e = blockIdx.x * (long long)blockDim.x + threadIdx.x; e < n; e += (long long)gridDim.x * blockDim.x)
     dst[e] = synth_value(seed, (uint64_t)e, scale);
@@ -161,6 +174,8 @@ struct hy_cache {
   float *rlog = nullptr, *moe_w = nullptr, *logits_buf = nullptr;
   int *am_idx = nullptr, *tok = nullptr, *ids = nullptr, *moe_ids = nullptr;
   unsigned *cnt_attn = nullptr, *cnt_am = nullptr, *guard = nullptr;
+  float* kv4_part = nullptr;  // 4-bit cache: the attention's partials and counters
+  unsigned* kv4_cnt = nullptr;
   float2* rope = nullptr;
   float *dbg_hidden = nullptr, *dbg_rlog = nullptr;
   int* dbg_rids = nullptr;
@@ -229,14 +244,15 @@ float kv4_scale(int hd) { return (float)(1.4426950408889634 / sqrt((double)hd));
 int cap_scales(int cap) { return (cap + 3) & ~3; }
 
 // K (which = 0) or V rows of attention layer ai: bf16 [nkv][cap][hd], or with
-// the int8 cache the codes [nkv][cap][hd] (bytes, returned as uint16_t*).
+// the int8 cache the codes [nkv][cap][hd], with the 4-bit cache [nkv][cap][hd/2]
+// (bytes, returned as uint16_t*).
 uint16_t* kv_cache(hy_cache* c, int seq, int ai, int which) {
   const hy_model* m = c->m;
   if (c->page_tokens)  // this layer's K or V block in page 0 of the pool; kv rows then go through the page table
     return c->pool + ((size_t)ai * 2 + which) * m->cfg.attn_kv_heads * c->page_tokens * m->cfg.head_dim;
   const size_t per = (size_t)m->cfg.attn_kv_heads * c->cap[seq] * m->cfg.head_dim;
-  const size_t esz = m->cfg.kv_format == 1 ? 1 : 2;
-  return reinterpret_cast<uint16_t*>(c->mem[seq] + c->off_kv[seq] + ((size_t)ai * 2 + which) * per * esz);
+  const size_t bytes = m->cfg.kv_format == 2 ? per / 2 : m->cfg.kv_format == 1 ? per : per * 2;
+  return reinterpret_cast<uint16_t*>(c->mem[seq] + c->off_kv[seq] + ((size_t)ai * 2 + which) * bytes);
 }
 
 const int* seq_page_table(hy_cache* c, int seq) {
@@ -254,15 +270,55 @@ float* kv_scales(hy_cache* c, int seq, int ai, int which) {
   return reinterpret_cast<float*>(c->mem[seq] + base) + ((size_t)ai * 2 + which) * per;
 }
 
+// 4-bit cache: the fp16 scales [nkv][cap_scales(cap)][hd/32] of K (which = 0)
+// or V of attention layer ai, after every layer's codes.
+uint16_t* kv4_scales(hy_cache* c, int seq, int ai, int which) {
+  const hy_model* m = c->m;
+  const size_t codes = (size_t)m->n_attn * m->cfg.attn_kv_heads * c->cap[seq] * m->cfg.head_dim;
+  const size_t base = c->off_kv[seq] + ((codes + 255) & ~(size_t)255);
+  const size_t per = (size_t)m->cfg.attn_kv_heads * cap_scales(c->cap[seq]) * (m->cfg.head_dim / 32);
+  return reinterpret_cast<uint16_t*>(c->mem[seq] + base) + ((size_t)ai * 2 + which) * per;
+}
+
+// The decode attention of layer ai over the 4-bit caches of the sequences
+// seqs: projections y, outputs o (a row for each sequence).
+kv4::Params kv4_params(hy_cache* c, const std::vector<int>& seqs, int ai, const float* y, float* o) {
+  const hy_model* m = c->m;
+  kv4::Params a;
+  memset(&a, 0, sizeof(a));
+  a.y = y;
+  a.ld_y = m->y_len;
+  a.o = o;
+  a.ld_o = m->o_len;
+  a.rope = c->rope;
+  a.nq = m->cfg.attn_q_heads;
+  a.nkv = m->cfg.attn_kv_heads;
+  a.nb = (int)seqs.size();
+  a.scale_log2e = kv4_scale(m->cfg.head_dim);
+  a.part = c->kv4_part;
+  a.counter = c->kv4_cnt;
+  a.guard = c->guard;
+  for (int b = 0; b < a.nb; ++b) {
+    a.K[b] = reinterpret_cast<uint8_t*>(kv_cache(c, seqs[b], ai, 0));
+    a.V[b] = reinterpret_cast<uint8_t*>(kv_cache(c, seqs[b], ai, 1));
+    a.Ks[b] = kv4_scales(c, seqs[b], ai, 0);
+    a.Vs[b] = kv4_scales(c, seqs[b], ai, 1);
+    a.len[b] = c->d_len + seqs[b];
+    a.cap[b] = c->cap[seqs[b]];
+  }
+  return a;
+}
+
 // One kernel of the decode step, recorded before any is launched so that each
 // GEMV can be told what the kernels after it read first.
 struct StepOp {
-  enum Kind { kGemv, kGdn, kAttn, kCopy } kind;
+  enum Kind { kGemv, kGdn, kAttn, kAttn4, kCopy } kind;
   gemv::Params g;
   int src, in, epi;
   const char* what;
   gdn::Params d;
   attn::Params a;
+  kv4::Params a4;
   const float* csrc;
   float* cdst;
   int cn;
@@ -318,6 +374,8 @@ int launch_ops(hy_model* m, std::vector<StepOp>& ops, cudaStream_t st) {
       e = gdn::launch(o.d, st, pdl);
     } else if (o.kind == StepOp::kAttn) {
       e = attn::launch(o.a, st, pdl);
+    } else if (o.kind == StepOp::kAttn4) {
+      e = kv4::launch(o.a4, m->cfg.head_dim, m->nsm, st, pdl);
     } else {
       e = launch_k(k_copy_f32, dim3((o.cn + 255) / 256), dim3(256), 0, st, pdl, o.csrc, o.cdst, o.cn);
     }
@@ -380,7 +438,13 @@ int collect_ops(hy_cache* c, int seq, float* logits, int* ids, std::vector<StepO
       }
       if ((rc = run(p, gemv::kSrcDense, in, gemv::kEpiStore, "in-proj")) != HY_OK) return rc;
     }
-    if (attn_l) {
+    if (attn_l && cf.kv_format == 2) {
+      StepOp o;
+      memset(&o, 0, sizeof(o));
+      o.kind = StepOp::kAttn4;
+      o.a4 = kv4_params(c, {seq}, m->sub[l], c->y, c->o);
+      ops.push_back(o);
+    } else if (attn_l) {
       attn::Params a;
       memset(&a, 0, sizeof(a));
       a.y = c->y;
@@ -668,7 +732,11 @@ int record_batch(hy_cache* c, const std::vector<int>& seqs, float* logits, int* 
       p.ldy = m->y_len;
       if ((rc = dense(p, "in-proj")) != HY_OK) return rc;
     }
-    if (attn_l) {
+    if (attn_l && cf.kv_format == 2) {
+      if ((rc = ck(kv4::launch(kv4_params(c, seqs, m->sub[l], c->by, c->bo), cf.head_dim, m->nsm, st, pdl),
+                   "4-bit attention")) != HY_OK)
+        return rc;
+    } else if (attn_l) {
       attn::Params a;
       memset(&a, 0, sizeof(a));
       a.y = c->by;
@@ -984,7 +1052,7 @@ int check_model_cfg(const hy_config* c) {
     if ((c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) || (G != 1 && G != 2 && G != 4 && G != 8))
       return fail(HY_ERR_UNSUPPORTED, "attention: head_dim must be 64/128/256 and nq/nkv in {1,2,4,8}");
   }
-  if (c->kv_format != 0 && c->kv_format != 1) return fail(HY_ERR_ARG, "kv_format must be 0 or 1");
+  if (c->kv_format < 0 || c->kv_format > 2) return fail(HY_ERR_ARG, "kv_format must be 0, 1 or 2");
   if (c->ffn < 0) return fail(HY_ERR_ARG, "ffn < 0");
   if (c->ffn == 0) {
     if (c->n_experts <= 0 || c->top_k <= 0 || c->top_k > 16 || c->top_k > c->n_experts || c->expert_ffn <= 0 ||
@@ -1220,6 +1288,12 @@ int prefill_chunk(hy_cache* c, int seq, const int* tok, int n, int t0, bool last
       a.ldy = m->y_len;
       a.K = kv_cache(c, seq, m->sub[l], 0);
       a.V = kv_cache(c, seq, m->sub[l], 1);
+      a.kv4 = cf.kv_format == 2;
+      if (a.kv4) {
+        a.Ks = kv4_scales(c, seq, m->sub[l], 0);
+        a.Vs = kv4_scales(c, seq, m->sub[l], 1);
+      }
+      a.guard = c->guard;
       a.cap = c->cap[seq];
       a.rope = c->rope;
       a.Qr = c->pf_qr;
@@ -1392,7 +1466,7 @@ int hy_model_create(const hy_config* cfg, const hy_weights* w, hy_model** out) {
     const bool ffn_ok = m->moe ? (c.expert_ffn % 8 == 0 && c.shared_ffn % 8 == 0 && c.shared_ffn > 0 &&
                                   c.n_experts <= 512 && c.top_k <= 16)
                                : c.ffn % 8 == 0;
-    m->chunk_prefill = !m->q4 && c.kv_format == 0 && !(c.flags & HY_FLAG_TOKEN_PREFILL) && H % 8 == 0 && ffn_ok &&
+    m->chunk_prefill = !m->q4 && c.kv_format != 1 && !(c.flags & HY_FLAG_TOKEN_PREFILL) && H % 8 == 0 && ffn_ok &&
                        od % 8 == 0;
   }
   *out = m;
@@ -1422,6 +1496,10 @@ static int cache_alloc(hy_model* m, int32_t max_seqs, const int32_t* capacity_ho
     if (c->cap[s] <= 0) { delete c; return fail(HY_ERR_ARG, "capacity of sequence %d must be positive", s); }
     max_cap = std::max(max_cap, c->cap[s]);
   }
+  if (cf.kv_format == 2 && (long long)kv4::kMaxB * cf.attn_kv_heads * ((max_cap - 1) / 16 + 1) > (1 << 30)) {
+    delete c;
+    return fail(HY_ERR_UNSUPPORTED, "4-bit cache: %d x kv heads x capacity above 2^34 rows", kv4::kMaxB);
+  }
   const size_t state_b = (size_t)m->n_gdn * cf.gdn_heads * cf.gdn_dv * cf.gdn_dk * 4;
   const size_t conv_b = (size_t)m->n_gdn * std::max(cf.conv_k, 1) * m->CC * 4;
   c->off_conv = (state_b + 255) & ~(size_t)255;
@@ -1431,6 +1509,11 @@ static int cache_alloc(hy_model* m, int32_t max_seqs, const int32_t* capacity_ho
     if (cf.kv_format == 1) {  // int8 codes, then the per-vector scales
       const size_t codes = (size_t)m->n_attn * 2 * cf.attn_kv_heads * c->cap[s] * cf.head_dim;
       kv_b = ((codes + 255) & ~(size_t)255) + (size_t)m->n_attn * 2 * cf.attn_kv_heads * cap_scales(c->cap[s]) * 4;
+    }
+    if (cf.kv_format == 2) {  // packed codes, then the fp16 block scales
+      const size_t codes = (size_t)m->n_attn * cf.attn_kv_heads * c->cap[s] * cf.head_dim;
+      kv_b = ((codes + 255) & ~(size_t)255) +
+             (size_t)m->n_attn * 2 * cf.attn_kv_heads * cap_scales(c->cap[s]) * (cf.head_dim / 32) * 2;
     }
     void* p = nullptr;
     cudaError_t e = cudaMalloc(&p, off_kv + kv_b + 256);
@@ -1479,6 +1562,14 @@ static int cache_alloc(hy_model* m, int32_t max_seqs, const int32_t* capacity_ho
         (rc = dalloc(c, &c->brids, (size_t)B * K)) ||
         (rc = dalloc(c, &c->bcnt_attn, (size_t)B * std::max(cf.attn_kv_heads, 1))) || (rc = dalloc(c, &c->bcnt_am, 1)) ||
         (rc = dalloc(c, &c->experts_read, 1))) {
+      free_cache_mem(c);
+      delete c;
+      return rc;
+    }
+  }
+  if (m->n_attn && cf.kv_format == 2) {
+    if ((rc = dalloc(c, &c->kv4_part, kv4::part_floats(cf.attn_q_heads, cf.attn_kv_heads, cf.head_dim, m->nsm))) ||
+        (rc = dalloc(c, &c->kv4_cnt, kv4::counters(kv4::kMaxB, cf.attn_kv_heads)))) {
       free_cache_mem(c);
       delete c;
       return rc;
@@ -1604,6 +1695,10 @@ int hy_seq_fill_synthetic(hy_cache* c, int32_t seq, int32_t len, uint64_t seed, 
           int8_t* base = reinterpret_cast<int8_t*>(kv_cache(c, seq, a, w)) + (size_t)g * c->cap[seq] * cf.head_dim;
           float* sc = kv_scales(c, seq, a, w) + (size_t)g * cap_scales(c->cap[seq]);
           k_fill_i8<<<1024, 256, 0, st>>>(base, sc, len, cf.head_dim, key);
+        } else if (cf.kv_format == 2) {
+          uint8_t* base = reinterpret_cast<uint8_t*>(kv_cache(c, seq, a, w)) + (size_t)g * c->cap[seq] * (cf.head_dim / 2);
+          uint16_t* sc = kv4_scales(c, seq, a, w) + (size_t)g * cap_scales(c->cap[seq]) * (cf.head_dim / 32);
+          k_fill_q4<<<1024, 256, 0, st>>>(base, sc, (long long)len * (cf.head_dim / 32), key);
         } else if (c->page_tokens) {  // block by block through the sequence's pages
           const int P = c->page_tokens;
           for (int j = 0; j * P < len; ++j) {
@@ -1627,6 +1722,114 @@ int hy_seq_fill_synthetic(hy_cache* c, int32_t seq, int32_t len, uint64_t seed, 
   HY_CK(cudaStreamSynchronize(st));  // &len is a host stack value
   c->len[seq] = len;
   return HY_OK;
+}
+
+namespace {
+// The states of the sequences seqs (positions [first, len) of their caches, and
+// the recurrent and conv state) moved: sequence i takes what sequence parent[i]
+// holds (parent null: what the first holds).  All of length len.
+int move_states(hy_cache* c, const std::vector<int>& seqs, const int32_t* parent, int first, int len, cudaStream_t st) {
+  const hy_model* m = c->m;
+  const hy_config& cf = m->cfg;
+  const int n = (int)seqs.size(), hd = cf.head_dim, nkv = cf.attn_kv_heads;
+  beam::ReorderParams p;
+  auto run = [&](int segs) -> int {
+    p.beams = n;
+    p.parent = parent;
+    p.guard = c->guard;
+    cudaError_t e = beam::reorder(p, 1, segs, st);
+    if (e != cudaSuccess) return fail(HY_ERR_CUDA, "state move launch: %s", cudaGetErrorString(e));
+    return HY_OK;
+  };
+  auto region = [&](auto base, long long bytes, int segs, auto pitch) -> int {
+    if (bytes <= 0 || segs <= 0) return HY_OK;
+    memset(&p, 0, sizeof(p));
+    for (int i = 0; i < n; ++i) {
+      p.base[i] = base(seqs[i]);
+      p.seg_stride[i] = pitch(seqs[i]);
+    }
+    p.n_seg = segs;
+    p.seg_bytes = bytes;
+    return run(segs);
+  };
+  auto none = [](int) { return 0ll; };
+  int rc = HY_OK;
+  if (m->n_gdn) {  // DeltaNet states and conv rings; both regions are 256-byte aligned and padded to 16 bytes
+    const long long state = (long long)m->n_gdn * cf.gdn_heads * cf.gdn_dv * cf.gdn_dk * 4;
+    const long long ring = ((long long)m->n_gdn * cf.conv_k * m->CC * 4 + 15) / 16 * 16;
+    if ((rc = region([&](int s) { return c->mem[s]; }, state, 1, none)) != HY_OK) return rc;
+    if ((rc = region([&](int s) { return c->mem[s] + c->off_conv; }, ring, 1, none)) != HY_OK) return rc;
+  }
+  if (!m->n_attn || first >= len) return HY_OK;
+  const int segs = m->n_attn * 2 * nkv;  // one for each layer, K or V, and kv head
+  if (c->page_tokens) {
+    memset(&p, 0, sizeof(p));
+    for (int i = 0; i < n; ++i) {
+      p.base[i] = reinterpret_cast<uint8_t*>(c->pool);
+      p.seg_stride[i] = (long long)c->page_tokens * hd * 2;
+      p.pages[i] = seq_page_table(c, seqs[i]);
+    }
+    p.n_seg = segs;
+    p.page_bytes = c->page_elems * 2;
+    p.page_rows = c->page_tokens;
+    p.row_bytes = hd * 2;
+    p.first_page = first / c->page_tokens;
+    p.first_row = first;
+    p.end_row = len;
+    const long long pages = (len - 1) / c->page_tokens - p.first_page + 1;
+    for (long long j = 0; j < pages; j += 65535 / segs) {  // the grid's limit of segments
+      const int here = (int)std::min<long long>(pages - j, 65535 / segs);
+      p.first_page = first / c->page_tokens + (int)j;
+      if ((rc = run(here * segs)) != HY_OK) return rc;
+    }
+    return HY_OK;
+  }
+  const int row = cf.kv_format == 2 ? hd / 2 : cf.kv_format == 1 ? hd : hd * 2;  // bytes of a cached vector
+  rc = region([&](int s) { return reinterpret_cast<uint8_t*>(kv_cache(c, s, 0, 0)) + (long long)first * row; },
+              (long long)(len - first) * row, segs, [&](int s) { return (long long)c->cap[s] * row; });
+  if (rc != HY_OK || cf.kv_format == 0) return rc;
+  // scales, from a multiple of 8 rows on (16-byte pieces; the rows before are alike) to one of 4 within the padding
+  const int r0 = first & ~7, r1 = cap_scales(len), sb = cf.kv_format == 1 ? 4 : hd / 16;
+  return region(
+      [&](int s) {
+        uint8_t* base = cf.kv_format == 1 ? reinterpret_cast<uint8_t*>(kv_scales(c, s, 0, 0))
+                                          : reinterpret_cast<uint8_t*>(kv4_scales(c, s, 0, 0));
+        return base + (long long)r0 * sb;
+      },
+      (long long)(r1 - r0) * sb, segs, [&](int s) { return (long long)cap_scales(c->cap[s]) * sb; });
+}
+}  // namespace
+
+int hy_seq_copy(hy_cache* c, int32_t src, int32_t dst, void* stream) {
+  if (!valid_seq(c, src) || !valid_seq(c, dst)) return fail(HY_ERR_ARG, "bad sequence handle %d or %d", src, dst);
+  if (src == dst) return HY_OK;
+  const int len = c->len[src];
+  if (len > c->cap[dst])
+    return fail(HY_ERR_CAPACITY, "sequence %d: length %d exceeds capacity %d", dst, len, c->cap[dst]);
+  cudaStream_t st = (cudaStream_t)stream;
+  int rc = ensure_pages(c, {{dst, len}}, st);
+  if (rc == HY_OK) rc = move_states(c, {src, dst}, nullptr, 0, len, st);
+  if (rc != HY_OK) return rc;
+  cudaError_t e = prefill::set_len(c->d_len + dst, len, st);
+  if (e != cudaSuccess) return fail(HY_ERR_CUDA, "position update: %s", cudaGetErrorString(e));
+  c->len[dst] = len;
+  return HY_OK;
+}
+
+int hy_seq_reorder(hy_cache* c, const int32_t* seqs_host, int32_t n, const int32_t* parent_dev, int32_t first,
+                   void* stream) {
+  if (!c || !seqs_host || !parent_dev || n < 1 || n > beam::kMaxBeams || first < 0)
+    return fail(HY_ERR_ARG, "bad reordering arguments (1..%d sequences)", beam::kMaxBeams);
+  const std::vector<int> seqs(seqs_host, seqs_host + n);
+  for (int i = 0; i < n; ++i) {
+    if (!valid_seq(c, seqs[i])) return fail(HY_ERR_ARG, "bad sequence handle %d", seqs[i]);
+    for (int j = 0; j < i; ++j)
+      if (seqs[j] == seqs[i]) return fail(HY_ERR_ARG, "sequence %d appears twice", seqs[i]);
+    if (c->len[seqs[i]] != c->len[seqs[0]])
+      return fail(HY_ERR_ARG, "sequences %d and %d have different lengths (%d, %d)", seqs[0], seqs[i], c->len[seqs[0]],
+                  c->len[seqs[i]]);
+  }
+  return move_states(c, seqs, parent_dev, first, c->len[seqs[0]], (cudaStream_t)stream);
 }
 
 int hy_prefill(hy_model* m, hy_cache* c, int32_t seq, const int32_t* tokens_dev, int32_t n, float* logits_dev,

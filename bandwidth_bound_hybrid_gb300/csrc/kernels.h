@@ -228,7 +228,8 @@ struct AppendParams {
   uint16_t* Ks;
   uint16_t* Vs;
   int cap, nq, nkv;
-  const int* len;          // position of the first row
+  const int* len;          // position of the first row (null: t0)
+  int t0;
   const float2* rope;
   float* kv_new;           // [n][2][nkv][hd] (nullable)
   unsigned* guard;
@@ -453,8 +454,12 @@ struct GdnArgs {
 struct AttnArgs {
   const float* Y;          // projection rows q|k|v of the chunk [n][ldy]
   int ldy;
-  uint16_t* K;             // bf16 cache [nkv][cap][hd]; rows t0 .. t0+n-1 are written
-  uint16_t* V;
+  uint16_t* K;             // bf16 cache [nkv][cap][hd]; rows t0 .. t0+n-1 are written.  kv4: the 4-bit cache's
+  uint16_t* V;             //   codes [nkv][cap][hd/2], with scales [nkv][cap rounded up to 4][hd/32] in Ks, Vs
+  int kv4;
+  uint16_t* Ks;
+  uint16_t* Vs;
+  unsigned* guard;
   int cap;
   const float2* rope;      // (cos, sin) [>= t0 + n][hd/2]
   float* Qr;               // scratch: rotated, scaled queries [n][nq][hd]

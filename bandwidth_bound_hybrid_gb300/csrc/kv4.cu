@@ -36,6 +36,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "kv4_dev.cuh"
 
 namespace hy {
 namespace kv4 {
@@ -188,35 +189,6 @@ template <int NB>
 __device__ __forceinline__ uint32_t place(int r, int c) {
   const int id = r * NB + c, line = id >> 3;
   return (uint32_t)((line * 8 + ((id & 7) ^ (line & (NB - 1)))) * 16);
-}
-
-// ------------------------------------------------------------ quantisation
-// One block of 32 values, one per lane of a full warp: its fp16 scale (bits)
-// and the lane's code.  s = fp16(min(max |x| * fp32(1 / 7), 65504)), code =
-// round-half-even(x * (1 / s)) clamped to [-7, 7]; an infinity or NaN in the
-// block makes the scale NaN, so that it shows in whatever reads the block.
-__device__ __forceinline__ uint16_t quant_block(float x, int* code) {
-  // |x| as bits: the order of finite values, infinities above, NaN above those
-  const uint32_t a = __reduce_max_sync(0xffffffffu, __float_as_uint(x) & 0x7fffffffu);
-  float s = NAN;
-  if (a < 0x7f800000u) s = fminf(__fmul_rn(__uint_as_float(a), 1.0f / 7.0f), 65504.0f);
-  const __half sh = __float2half_rn(s);
-  const float sf = __half2float(sh);
-  const float inv = sf > 0.f ? __fdiv_rn(1.0f, sf) : 0.f;
-  const float r = fminf(fmaxf(rintf(__fmul_rn(x, inv)), -7.f), 7.f);
-  *code = (int)r;
-  return __half_as_ushort(sh);
-}
-
-// Store a quantised block: byte i (lanes 0..15) of the codes, the scale, and
-// the values it stands for (nullable).
-__device__ __forceinline__ void store_block(uint16_t s, int code, uint8_t* codes, uint16_t* scale, float* values,
-                                            int lane) {
-  const uint32_t n = (uint32_t)(code + 8);
-  const uint32_t up = __shfl_down_sync(0xffffffffu, n, 16);
-  if (lane < 16) codes[lane] = (uint8_t)(n | (up << 4));
-  if (lane == 0) *scale = s;
-  if (values) values[lane] = __fmul_rn(__half2float(__ushort_as_half(s)), (float)code);
 }
 
 // (x0, x1) of a rotate-half pair, each product and sum rounded on its own, so
@@ -940,7 +912,7 @@ template <int HD>
 __global__ void __launch_bounds__(256) k_append(const AppendParams p) {
   constexpr int NB = HD / 32, NH = NB / 2;
   const int lane = threadIdx.x & 31;
-  const int T = *p.len;
+  const int T = p.len ? *p.len : p.t0;
   if (T < 0 || (long long)T + p.n > p.cap) {
     if (blockIdx.x == 0 && threadIdx.x == 0) set_guard(p.guard, kGuardBadPosition);
     return;

@@ -24,6 +24,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "kv4_dev.cuh"
 
 namespace hy {
 namespace prefill {
@@ -282,6 +283,7 @@ __global__ void k_attn_prep(AttnArgs a) {
     q[d] = (x0 * cs.x - x1 * cs.y) * a.scale;
     q[d + half] = (x1 * cs.x + x0 * cs.y) * a.scale;
   }
+  if (a.kv4) return;  // the 4-bit cache's rows are appended by kv4::append
   for (int e = threadIdx.x; e < a.nkv * half; e += blockDim.x) {
     const int g = e / half, d = e % half;
     const float2 cs = rope[d];
@@ -303,18 +305,20 @@ __global__ void k_attn_prep(AttnArgs a) {
 // P V, hd / 16 output dims (dims kgroup * hd / 16 ...).
 constexpr int kQV = 64, kTK = 64, kCausalThreads = 256;
 
-template <int HD>
+// KV4: the cache is in 4 bits; its values are widened to FP32 rows (a bf16 row
+// would round a code times an fp16 scale).
+template <int HD, bool KV4>
 struct CausalSmem {
-  static constexpr int kRow = HD * 2 + 16;  // padded bf16 row (bytes): the 16 key rows of a warp spread over the banks
+  static constexpr int kRow = HD * (KV4 ? 4 : 2) + 16;  // padded row (bytes): the 16 key rows of a warp spread over the banks
   static constexpr size_t q = (size_t)kQV * HD * 4;
   static constexpr size_t kv = (size_t)kTK * kRow;
   static constexpr size_t p = (size_t)kQV * (kTK + 1) * 4;
   static constexpr size_t total = q + 2 * kv + p;
 };
 
-template <int HD>
+template <int HD, bool KV4>
 __global__ void __launch_bounds__(kCausalThreads) k_attn_causal(AttnArgs a) {
-  using SM = CausalSmem<HD>;
+  using SM = CausalSmem<HD, KV4>;
   constexpr int DPT = HD / 16;  // output dims per thread
   extern __shared__ __align__(16) uint8_t smem[];
   float* Qs = reinterpret_cast<float*>(smem);
@@ -349,7 +353,27 @@ __global__ void __launch_bounds__(kCausalThreads) k_attn_causal(AttnArgs a) {
   for (int tt = 0; tt < ntiles; ++tt) {
     const int p0 = tt * kTK;
     __syncthreads();  // the previous tile's K, V and P are no longer read
-    for (int e = tid; e < kTK * (HD / 8); e += kCausalThreads) {
+    if (KV4) {  // word c of a row: 8 values of K and of V
+      const long long cap_s = ((long long)a.cap + 3) & ~3ll;
+      for (int e = tid; e < kTK * (HD / 8); e += kCausalThreads) {
+        const int r = e / (HD / 8), c = e % (HD / 8), blk = c / 4, d0 = blk * 32 + c % 4 * 4;
+        float k[8] = {}, v[8] = {};
+        if (p0 + r <= last) {
+          const long long row = (long long)g * a.cap + p0 + r, row_s = (long long)g * cap_s + p0 + r;
+          const float ks = __half2float(__ushort_as_half(a.Ks[row_s * (HD / 32) + blk]));
+          const float vs = __half2float(__ushort_as_half(a.Vs[row_s * (HD / 32) + blk]));
+          kv4::unpack_word(reinterpret_cast<const uint32_t*>(a.K)[row * (HD / 8) + c], ks, k, k + 4);
+          kv4::unpack_word(reinterpret_cast<const uint32_t*>(a.V)[row * (HD / 8) + c], vs, v, v + 4);
+        }
+        float* kd = reinterpret_cast<float*>(Ks + r * SM::kRow) + d0;
+        float* vd = reinterpret_cast<float*>(Vs + r * SM::kRow) + d0;
+        *reinterpret_cast<float4*>(kd) = make_float4(k[0], k[1], k[2], k[3]);
+        *reinterpret_cast<float4*>(kd + 16) = make_float4(k[4], k[5], k[6], k[7]);
+        *reinterpret_cast<float4*>(vd) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(vd + 16) = make_float4(v[4], v[5], v[6], v[7]);
+      }
+    }
+    for (int e = tid; !KV4 && e < kTK * (HD / 8); e += kCausalThreads) {
       const int r = e / (HD / 8), c = e % (HD / 8);
       uint4 kv = make_uint4(0, 0, 0, 0), vv = make_uint4(0, 0, 0, 0);
       if (p0 + r <= last) {
@@ -373,8 +397,20 @@ __global__ void __launch_bounds__(kCausalThreads) k_attn_causal(AttnArgs a) {
       for (int r = 0; r < 4; ++r) q4[r] = *reinterpret_cast<const float4*>(Qs + (qg * 4 + r) * HD + d);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const uint2 kb = *reinterpret_cast<const uint2*>(Ks + (kg + 16 * c) * SM::kRow + d * 2);
-        const float k0 = bf16_lo(kb.x), k1 = bf16_hi(kb.x), k2 = bf16_lo(kb.y), k3 = bf16_hi(kb.y);
+        float k0, k1, k2, k3;
+        if (KV4) {
+          const float4 kf = *reinterpret_cast<const float4*>(Ks + (kg + 16 * c) * SM::kRow + d * 4);
+          k0 = kf.x;
+          k1 = kf.y;
+          k2 = kf.z;
+          k3 = kf.w;
+        } else {
+          const uint2 kb = *reinterpret_cast<const uint2*>(Ks + (kg + 16 * c) * SM::kRow + d * 2);
+          k0 = bf16_lo(kb.x);
+          k1 = bf16_hi(kb.x);
+          k2 = bf16_lo(kb.y);
+          k3 = bf16_hi(kb.y);
+        }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           s[r][c] = fmaf(q4[r].x, k0, s[r][c]);
@@ -423,8 +459,20 @@ __global__ void __launch_bounds__(kCausalThreads) k_attn_causal(AttnArgs a) {
       const uint16_t* vrow = reinterpret_cast<const uint16_t*>(Vs + k * SM::kRow) + kg * DPT;
 #pragma unroll
       for (int d = 0; d < DPT; d += 4) {  // 4 bf16 (8 bytes) at a time: DPT is a multiple of 4
-        const uint2 vb = *reinterpret_cast<const uint2*>(vrow + d);
-        const float vf[4] = {bf16_lo(vb.x), bf16_hi(vb.x), bf16_lo(vb.y), bf16_hi(vb.y)};
+        float vf[4];
+        if (KV4) {
+          const float4 v4 = *reinterpret_cast<const float4*>(Vs + k * SM::kRow + (kg * DPT + d) * 4);
+          vf[0] = v4.x;
+          vf[1] = v4.y;
+          vf[2] = v4.z;
+          vf[3] = v4.w;
+        } else {
+          const uint2 vb = *reinterpret_cast<const uint2*>(vrow + d);
+          vf[0] = bf16_lo(vb.x);
+          vf[1] = bf16_hi(vb.x);
+          vf[2] = bf16_lo(vb.y);
+          vf[3] = bf16_hi(vb.y);
+        }
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -452,20 +500,27 @@ cudaError_t launch_causal(const AttnArgs& a, cudaStream_t st) {
   const int G = a.nq / a.nkv;
   const int QT = kQV / G;
   const dim3 grid(a.nkv, (a.n + QT - 1) / QT);
-  return launch_k(k_attn_causal<HD>, grid, dim3(kCausalThreads), CausalSmem<HD>::total, st, false, a);
+  if (a.kv4)
+    return launch_k(k_attn_causal<HD, true>, grid, dim3(kCausalThreads), CausalSmem<HD, true>::total, st, false, a);
+  return launch_k(k_attn_causal<HD, false>, grid, dim3(kCausalThreads), CausalSmem<HD, false>::total, st, false, a);
+}
+
+template <int HD>
+cudaError_t init_causal() {
+  cudaError_t e = cudaFuncSetAttribute(k_attn_causal<HD, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)CausalSmem<HD, false>::total);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_attn_causal<HD, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)CausalSmem<HD, true>::total);
+  return e;
 }
 
 }  // namespace
 
 cudaError_t init() {
-  cudaError_t e = cudaFuncSetAttribute(k_attn_causal<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)CausalSmem<64>::total);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k_attn_causal<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)CausalSmem<128>::total);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k_attn_causal<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)CausalSmem<256>::total);
+  cudaError_t e = init_causal<64>();
+  if (e == cudaSuccess) e = init_causal<128>();
+  if (e == cudaSuccess) e = init_causal<256>();
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(k_gdn_scan<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)scan_smem(64));
   if (e == cudaSuccess)
@@ -508,6 +563,23 @@ cudaError_t attention(const AttnArgs& a, cudaStream_t st) {
   if (a.nkv <= 0 || a.nq % a.nkv || (G != 1 && G != 2 && G != 4 && G != 8)) return cudaErrorInvalidValue;
   k_attn_prep<<<a.n, 256, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess && a.kv4) {
+    kv4::AppendParams p = {};
+    p.y = a.Y;
+    p.ld_y = a.ldy;
+    p.n = a.n;
+    p.K = reinterpret_cast<uint8_t*>(a.K);
+    p.V = reinterpret_cast<uint8_t*>(a.V);
+    p.Ks = a.Ks;
+    p.Vs = a.Vs;
+    p.cap = a.cap;
+    p.nq = a.nq;
+    p.nkv = a.nkv;
+    p.t0 = a.t0;
+    p.rope = a.rope;
+    p.guard = a.guard;
+    e = kv4::append(p, a.hd, st);
+  }
   if (e != cudaSuccess) return e;
   switch (a.hd) {
     case 64: return launch_causal<64>(a, st);

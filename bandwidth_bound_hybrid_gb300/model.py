@@ -47,6 +47,27 @@ def make_config(shape, splits: int = 0, flags: int = 0) -> hy_config:
     return c
 
 
+class BeamState:
+    """What HybridModel.beam_step keeps of n beams (CUDA tensors): the tokens
+    to decode next, the scores (log probabilities so far), which beams have
+    ended, and each beam's parent in the last step.  All beams start alike, so
+    only the first counts in the first step (the others' scores are
+    -infinity)."""
+
+    def __init__(self, n: int, vocab: int, token: int):
+        import torch
+        i32 = dict(dtype=torch.int32, device="cuda")
+        self.tokens = torch.full((n,), int(token), **i32)
+        self.scores = torch.full((n,), float("-inf"), dtype=torch.float32, device="cuda")
+        self.scores[0] = 0.0
+        self.done = torch.zeros((n,), **i32)
+        self.parent = torch.zeros((n,), **i32)
+        self.ids = torch.zeros((n,), **i32)
+        self.logits = torch.empty((n, vocab), dtype=torch.float32, device="cuda")
+        self.workspace = torch.zeros(capi.lib().hy_op_beam_select_workspace(1, n, vocab), dtype=torch.uint8,
+                                     device="cuda")
+
+
 class HybridModel:
     """One model plus its cache of ``len(capacities)`` sequences.
 
@@ -159,6 +180,32 @@ class HybridModel:
 
     def reset(self, seq: int, stream=None) -> None:
         check(capi.lib().hy_seq_reset(self.c, seq, _stream(stream)), "hy_seq_reset")
+
+    def copy(self, src: int, dst: int, stream=None) -> None:
+        """Make sequence `dst` a copy of sequence `src`."""
+        check(capi.lib().hy_seq_copy(self.c, src, dst, _stream(stream)), "hy_seq_copy")
+
+    def reorder(self, seqs, parent, first: int = 0, stream=None) -> None:
+        """Sequence seqs[i] takes the state of seqs[parent[i]] (parent: int32
+        CUDA tensor); KV rows before position `first` stay as they are."""
+        arr = (ctypes.c_int32 * len(seqs))(*[int(s) for s in seqs])
+        check(capi.lib().hy_seq_reorder(self.c, arr, len(seqs), _ptr(parent), int(first), _stream(stream)),
+              "hy_seq_reorder")
+
+    def beam_step(self, seqs, beams, eos: int = -1, first: int = 0, stream=None) -> None:
+        """One step of beam search over the sequences `seqs` (a beam each):
+        decodes beams.tokens, selects the best continuations of all beams, and
+        moves every sequence to its parent's state (KV rows from position
+        `first`, the prompt's length, on).  `beams`: a BeamState, updated in
+        place."""
+        n, V = len(seqs), self.shape.vocab
+        self.decode_batch(seqs, beams.tokens, beams.ids, beams.logits, stream)
+        check(capi.lib().hy_op_beam_select(_ptr(beams.logits), V, 1, n, V, n, _ptr(beams.scores),
+                                           _ptr(beams.done) if eos >= 0 else None, int(eos), _ptr(beams.scores),
+                                           _ptr(beams.parent), _ptr(beams.tokens),
+                                           _ptr(beams.done) if eos >= 0 else None, _ptr(beams.workspace),
+                                           _stream(stream)), "hy_op_beam_select")
+        self.reorder(seqs, beams.parent, first, stream)
 
     def check_device(self, stream=None) -> int:
         bits = ctypes.c_uint32(0)

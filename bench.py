@@ -431,7 +431,8 @@ def run_ours(args):
             "scaling": "weak", "vs_baseline": None, "dtype": "f32", "data": "synthetic",
             "config": {"workload": w.name, "shape": shape.name, "batch": 1, "prompt": prompt,
                        "context_timed": [ctx0, ctx0 + args.steps], "weights": "bf16",
-                       "kv": "int8 + FP32 scale per vector" if getattr(shape, "kv_format", 0) else "bf16",
+                       "kv": ("bf16", "int8 + FP32 scale per vector",
+                              "4-bit + fp16 scale per 32 values")[getattr(shape, "kv_format", 0)],
                        "outputs": "FP32 logits [V] and the greedy id per step",
                        "context_fill": "seeded synthetic KV rows and recurrent state (no prompt replay)"
                        if synthetic_fill else "prefill of the prompt",
@@ -610,7 +611,7 @@ def timed_prefill(model, toks, shape, logits):
     n = int(toks.numel())
     fl = acc.prefill_flops(shape, n)
     _, sustained, kind = load_tensor_peak()
-    chunked = getattr(shape, "weight_format", 0) == 0 and getattr(shape, "kv_format", 0) == 0
+    chunked = getattr(shape, "weight_format", 0) == 0 and getattr(shape, "kv_format", 0) != 1
     gemms = ("tcgen05 GEMMs (the experts as grouped GEMMs over the tokens that picked them)" if shape.is_moe
              else "tcgen05 GEMMs")
     return {"tokens": n, "ttft_ms": t * 1e3, "tokens_per_s": n / t,

@@ -84,7 +84,8 @@ typedef struct {
   int32_t weight_format;   /* 0 = bf16; 1 = 4-bit blocks of 32 for the linear weights (see hy_tensor) */
   int32_t attn_splits;     /* split-KV chunks per kv head; 0 = chosen from the SM count */
   uint32_t flags;          /* HY_FLAG_* */
-  int32_t kv_format;       /* 0 = bf16 KV cache; 1 = int8 codes with one FP32 scale per cached k or v vector */
+  int32_t kv_format;       /* 0 = bf16 KV cache; 1 = int8 codes with one FP32 scale per cached k or v vector;
+                            * 2 = 4-bit codes with one fp16 scale per 32 values (see hy_op_attention_q4) */
 } hy_config;
 
 /* One linear weight [rows][cols]: bf16 in `w` (`scales` unused), or with
@@ -162,7 +163,7 @@ void hy_cache_free(hy_cache* c);
  * lengths share the pool and may join or leave a batch between steps.
  * capacity_host[s] still bounds each sequence's length.  Recurrent state and
  * scratch are as for hy_cache_alloc.  bf16 K/V only (HY_ERR_UNSUPPORTED with
- * kv_format 1). */
+ * kv_format 1 or 2). */
 int hy_cache_alloc_paged(hy_model* m, int32_t max_seqs, const int32_t* capacity_host, int32_t page_tokens,
                          int32_t pool_pages, hy_cache** out);
 /* Pages left in the pool of a paged cache, or -1 for a cache without pages. */
@@ -199,6 +200,25 @@ int32_t hy_seq_capacity(const hy_cache* c, int32_t seq);
  * A host copy of the same values lets a CPU reference start from this state. */
 int hy_seq_fill_synthetic(hy_cache* c, int32_t seq, int32_t len, uint64_t seed, void* stream);
 
+/* Make sequence `dst` a copy of sequence `src` (KV rows, DeltaNet state, conv
+ * rings, length), as a beam search starts its beams from one prompt.  What
+ * dst held is lost.  HY_ERR_CAPACITY, with nothing changed, if src's length
+ * exceeds dst's capacity or the page pool is short.  Stream-ordered. */
+int hy_seq_copy(hy_cache* c, int32_t src, int32_t dst, void* stream);
+
+/* Reorder the states of the n (1..16) distinct sequences seqs_host, all of the
+ * same length, in place: sequence i takes what sequence parent_dev[i] (an index
+ * into seqs_host, on the device: a selection's result) held, repeats allowed.
+ * Only KV rows from position `first` on are moved (rows before it are taken to
+ * be alike in all of them, as a common prompt's are: 0 moves every row); the
+ * DeltaNet states and conv rings are moved whole.  A parent outside [0, n)
+ * leaves its sequence as it is (HY_GUARD_BAD_INDEX, see hy_check_device).
+ * Every KV format, paged or not.  Stream-ordered.  "hanzo-engine: A Portable
+ * Single-Binary LLM Inference Engine...", section "System Architecture"
+ * (sequences that share and leave a batch between steps). */
+int hy_seq_reorder(hy_cache* c, const int32_t* seqs_host, int32_t n, const int32_t* parent_dev, int32_t first,
+                   void* stream);
+
 /* Distinct routed experts the batched MoE steps (hy_decode_step with several
  * sequences, or 4-bit weights) read since the last call, summed over layers
  * and steps: each layer reads the union of its tokens' picks once.  Resets
@@ -224,7 +244,7 @@ int32_t hy_step_splits(const hy_cache* c, int32_t seq);
  * model at positions len .. len+n-1, filling its caches.  logits_dev
  * (nullable) receives the FP32 logits [V] of the last token.
  * HY_ERR_CAPACITY (nothing launched) if len + n > capacity.  bf16 models
- * (dense and MoE) with the bf16 cache run the prompt in chunks of up to 2048
+ * (dense and MoE) with the bf16 or the 4-bit cache run the prompt in chunks of up to 2048
  * tokens (HY_PREFILL_CHUNK in the environment overrides) through tensor-core
  * GEMMs (tcgen05, the activations as bf16 hi + lo parts, FP32 accumulation;
  * the MoE experts as grouped GEMMs over the chunk's picks) and prompt

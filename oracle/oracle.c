@@ -219,6 +219,67 @@ void orc_quant_i8(const double* x, int32_t n, int8_t* q, float* scale) {
   *scale = amax / 127.0f;
 }
 
+/* 4-bit quantisation of a cached vector: blocks of 32, each with one fp16
+ * scale and codes in [-7, 7].  FP32, every operation rounded on its own: a =
+ * max_i |x_i|, s = fp16(min(a * r, 65504)) with r = 1/7 rounded to FP32, code =
+ * round-half-even(x_i * (1 / s)) clamped to [-7, 7]; s = 0 gives codes 0.  The
+ * scale is returned as the FP32 value of its fp16 (finite inputs). */
+static float round_fp16(float v) { /* v >= 0, at most 65504: round to nearest even */
+  if (v == 0.0f) return 0.0f;
+  int e;
+  frexpf(v, &e);                      /* v = m 2^e, m in [0.5, 1) */
+  int step = e - 11 < -24 ? -24 : e - 11; /* 11 significant bits, or the subnormals' spacing */
+  return ldexpf(rintf(ldexpf(v, -step)), step);
+}
+
+void orc_quant_q4(const double* x, int32_t n, int8_t* q, float* scale) {
+  for (int32_t b = 0; b < n / 32; ++b) {
+    float amax = 0.0f;
+    for (int32_t i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf((float)x[b * 32 + i]));
+    volatile float seventh = 1.0f / 7.0f;
+    volatile float raw = amax * seventh;
+    float s = round_fp16(raw > 65504.0f ? 65504.0f : raw);
+    volatile float inv = s > 0.0f ? 1.0f / s : 0.0f;
+    for (int32_t i = 0; i < 32; ++i) {
+      volatile float prod = (float)x[b * 32 + i] * inv;
+      float r = rintf(prod);
+      q[b * 32 + i] = (int8_t)(r > 7.0f ? 7.0f : (r < -7.0f ? -7.0f : r));
+    }
+    scale[b] = s;
+  }
+}
+
+/* Attention of orc_attention over a 4-bit cache: codes [nkv][cap][hd] (one a
+ * byte here), scales [nkv][cap][hd/32]. */
+void orc_attention_q4(const double* q, const int8_t* Kq, const float* Ks, const int8_t* Vq, const float* Vs,
+                      int32_t nq, int32_t nkv, int32_t hd, int32_t cap, int32_t npos, double* o) {
+  int32_t group = nq / nkv, nb = hd / 32;
+  double scale = 1.0 / sqrt((double)hd);
+  double* s = (double*)malloc(sizeof(double) * (size_t)(npos > 0 ? npos : 1));
+  for (int32_t j = 0; j < nq; ++j) {
+    int64_t row0 = (int64_t)(j / group) * cap;
+    double mx = -INFINITY, den = 0.0;
+    for (int32_t p = 0; p < npos; ++p) {
+      double acc = 0.0;
+      for (int32_t d = 0; d < hd; ++d)
+        acc += q[(int64_t)j * hd + d] * ((double)Kq[(row0 + p) * hd + d] * (double)Ks[(row0 + p) * nb + d / 32]);
+      s[p] = acc * scale;
+      if (s[p] > mx) mx = s[p];
+    }
+    for (int32_t p = 0; p < npos; ++p) {
+      s[p] = exp(s[p] - mx);
+      den += s[p];
+    }
+    for (int32_t d = 0; d < hd; ++d) {
+      double acc = 0.0;
+      for (int32_t p = 0; p < npos; ++p)
+        acc += s[p] * ((double)Vq[(row0 + p) * hd + d] * (double)Vs[(row0 + p) * nb + d / 32]);
+      o[(int64_t)j * hd + d] = acc / den;
+    }
+  }
+  free(s);
+}
+
 /* Attention of orc_attention over an int8 cache: K and V values are the
  * stored codes times their vector's scale. */
 void orc_attention_i8(const double* q, const int8_t* Kq, const float* Ks, const int8_t* Vq, const float* Vs,
@@ -411,8 +472,8 @@ int orc_cache_create(const orc_config* cfg, int32_t capacity, orc_cache* out) {
   out->conv_state = (double*)calloc((size_t)(cs > 0 ? cs : 1), sizeof(double));
   out->k_cache = (uint16_t*)calloc((size_t)(kv > 0 ? kv : 1), sizeof(uint16_t));
   out->v_cache = (uint16_t*)calloc((size_t)(kv > 0 ? kv : 1), sizeof(uint16_t));
-  if (cfg->kv_format == 1) {
-    int64_t ns = na * (int64_t)cfg->attn_kv_heads * capacity;
+  if (cfg->kv_format == 1 || cfg->kv_format == 2) {
+    int64_t ns = na * (int64_t)cfg->attn_kv_heads * capacity * (cfg->kv_format == 2 ? cfg->head_dim / 32 : 1);
     out->k_q = (int8_t*)calloc((size_t)(kv > 0 ? kv : 1), 1);
     out->v_q = (int8_t*)calloc((size_t)(kv > 0 ? kv : 1), 1);
     out->k_s = (float*)calloc((size_t)(ns > 0 ? ns : 1), sizeof(float));
@@ -521,6 +582,19 @@ int orc_forward_token(const orc_config* cfg, const orc_weights* w, orc_cache* c,
           orc_quant_i8(v + (int64_t)g * hd, hd, Vq + row * hd, Vs + row);
         }
         orc_attention_i8(q, Kq, Ks, Vq, Vs, nq, nkv, hd, c->capacity, pos + 1, o);
+      } else if (cfg->kv_format == 2) {
+        /* 4-bit cache: every block of 32 of each new k and v vector with its own scale */
+        int32_t nb = hd / 32;
+        int8_t* Kq = c->k_q + (int64_t)ai * nkv * c->capacity * hd;
+        int8_t* Vq = c->v_q + (int64_t)ai * nkv * c->capacity * hd;
+        float* Ks = c->k_s + (int64_t)ai * nkv * c->capacity * nb;
+        float* Vs = c->v_s + (int64_t)ai * nkv * c->capacity * nb;
+        for (int32_t g = 0; g < nkv; ++g) {
+          int64_t row = (int64_t)g * c->capacity + pos;
+          orc_quant_q4(k + (int64_t)g * hd, hd, Kq + row * hd, Ks + row * nb);
+          orc_quant_q4(v + (int64_t)g * hd, hd, Vq + row * hd, Vs + row * nb);
+        }
+        orc_attention_q4(q, Kq, Ks, Vq, Vs, nq, nkv, hd, c->capacity, pos + 1, o);
       } else {
         uint16_t* Kc = c->k_cache + (int64_t)ai * nkv * c->capacity * hd;
         uint16_t* Vc = c->v_cache + (int64_t)ai * nkv * c->capacity * hd;

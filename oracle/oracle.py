@@ -78,6 +78,8 @@ def lib():
         L.orc_attention_split.argtypes = [c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp]
         L.orc_quant_i8.argtypes = [c_vp, c_i32, c_vp, c_vp]
         L.orc_attention_i8.argtypes = [c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp]
+        L.orc_quant_q4.argtypes = [c_vp, c_i32, c_vp, c_vp]
+        L.orc_attention_q4.argtypes = [c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp]
         L.orc_argmax.argtypes, L.orc_argmax.restype = [c_vp, c_i64], c_i32
         L.orc_topk.argtypes = [c_vp, c_i32, c_i32, c_vp]
         L.orc_softmax.argtypes = [c_vp, c_i32, c_vp]
@@ -90,7 +92,7 @@ def lib():
         L.orc_set_threads.argtypes = [ctypes.c_int]
         for f in (L.orc_mat_row, L.orc_gemv, L.orc_rmsnorm, L.orc_l2norm, L.orc_rope, L.orc_conv_step,
                   L.orc_gdn_step, L.orc_attention, L.orc_attention_split, L.orc_topk, L.orc_softmax,
-                  L.orc_quant_i8, L.orc_attention_i8,
+                  L.orc_quant_i8, L.orc_attention_i8, L.orc_quant_q4, L.orc_attention_q4,
                   L.orc_cache_destroy, L.orc_cache_reset, L.orc_set_threads):
             f.restype = None
     return _lib
@@ -217,6 +219,27 @@ def attention_i8(q, Kq, Ks, Vq, Vs, npos: int) -> np.ndarray:
     nkv, cap, _ = Kq.shape
     o = np.zeros_like(q)
     lib().orc_attention_i8(_p(q), _p(Kq), _p(Ks), _p(Vq), _p(Vs), nq, nkv, hd, cap, npos, _p(o))
+    return o
+
+
+def quant_q4(x):
+    """(codes int8 [n], scales float32 [n / 32]) of one cached vector in the 4-bit format."""
+    x = f64(x)
+    q = np.zeros(x.size, dtype=np.int8)
+    sc = np.zeros(x.size // 32, dtype=np.float32)
+    lib().orc_quant_q4(_p(x), x.size, _p(q), _p(sc))
+    return q, sc
+
+
+def attention_q4(q, Kq, Ks, Vq, Vs, npos: int) -> np.ndarray:
+    """q: [nq][hd]; Kq, Vq: codes [nkv][cap][hd]; Ks, Vs: scales [nkv][cap][hd / 32]."""
+    q = f64(q)
+    nq, hd = q.shape
+    Kq, Vq = np.ascontiguousarray(Kq, dtype=np.int8), np.ascontiguousarray(Vq, dtype=np.int8)
+    Ks, Vs = np.ascontiguousarray(Ks, dtype=np.float32), np.ascontiguousarray(Vs, dtype=np.float32)
+    nkv, cap, _ = Kq.shape
+    o = np.zeros_like(q)
+    lib().orc_attention_q4(_p(q), _p(Kq), _p(Ks), _p(Vq), _p(Vs), nq, nkv, hd, cap, npos, _p(o))
     return o
 
 

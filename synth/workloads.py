@@ -72,7 +72,8 @@ class ModelShape:
     rms_eps: float = 1e-6
     rope_theta: float = 1e4
     weight_format: int = 0        # 0 bf16, 1 4-bit blocks of 32
-    kv_format: int = 0            # 0 bf16 KV cache, 1 int8 codes with one FP32 scale per cached vector
+    kv_format: int = 0            # 0 bf16 KV cache, 1 int8 codes with one FP32 scale per cached vector, 2 4-bit codes
+                                  # with one fp16 scale per 32 values
     seed: int = 0
 
     @property
@@ -137,6 +138,8 @@ WORKLOADS = {
                             splits=(1, 2, 4, 8, 16)),
     "dense4b-32k-kv8": Workload("dense 4B-shaped hybrid, int8 KV cache, prompt 32768 + 128 decode",
                                 dataclasses.replace(DENSE4B, name="dense-4b-kv8", kv_format=1), 32768, 128),
+    "dense4b-32k-kv4": Workload("dense 4B-shaped hybrid, 4-bit KV cache, prompt 32768 + 128 decode",
+                                dataclasses.replace(DENSE4B, name="dense-4b-kv4", kv_format=2), 32768, 128),
     "moe35b": Workload("MoE 35B-A3B-shaped hybrid, prompt 2048 + 256 decode", MOE35B, 2048, 256),
     "moe35b-q4-b8": Workload("MoE 35B-A3B-shaped hybrid, 4-bit, batch 8, ragged context 1024..16384, 128 decode",
                              MOE35B_Q4, 0, 128, batch=8, ragged_context=(1024, 16384)),
