@@ -76,6 +76,7 @@ struct alignas(16) Small {
   // the work (set by warp 0, so that no warp holds it over its tiles)
   int T[kMaxB];                    // positions of the new rows (-1: refused)
   int at[kMaxB + 1];               // first unit of each sequence: tiles (spans) or ranges
+  int per[kMaxB];                  // units of one of its heads
   int m;                           // most tiles of a range; 0: spans
   int q, rem, near;
   int unit, unit_end;              // this CTA's units
@@ -212,8 +213,7 @@ struct Item {
 __device__ __forceinline__ Item item_at(const Params& p, const Small& sm, int t) {
   const int lane = threadIdx.x & 31;
   const int b = __ffs(__ballot_sync(0xffffffffu, lane < p.nb && t < sm.at[lane < p.nb ? lane + 1 : 0])) - 1;
-  const int n = (sm.at[b + 1] - sm.at[b]) / p.nkv;
-  const int g = (int)((unsigned)(t - sm.at[b]) / (unsigned)n);
+  const int n = sm.per[b], g = (int)((unsigned)(t - sm.at[b]) / (unsigned)n);
   return {b, g, sm.at[b] + g * n, sm.at[b] + g * n + n};
 }
 __device__ __forceinline__ int span_first(const Params& p, const Small& sm, unsigned c) {
@@ -247,24 +247,27 @@ __device__ __forceinline__ void plan_work(const Params& p, Small& sm) {
   const int total = p.nkv * (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
   const int items = p.nkv * __popc(__ballot_sync(0xffffffffu, n > 0));
   const int grid = gridDim.x;
-  // least m: 32 candidates from an equal share (at least a tile per warp) up
-  // to total / (grid - items), which always suffices, a candidate a lane
-  int m = 0;
-  if (items <= grid) {
-    const int lo = max(W, (total + grid - 1) / grid);
-    const int hi = max(lo, items < grid ? (total + grid - items - 1) / (grid - items) : total);
-    const int mine = lane < 31 ? lo + (int)((long long)(hi - lo) * lane / 31) : hi;
-    int ranges = 0;
-    for (int b = 0; b < p.nb; ++b) {
-      const int nb = __shfl_sync(0xffffffffu, n, b);
-      ranges += (int)((unsigned)(nb + mine - 1) / (unsigned)mine);
+  // least m: a tile per warp if the CTAs suffice, else 32 candidates, a lane
+  // each, from an equal share up to total / (grid - items), which always does
+  int m = 0, per = (n + W - 1) / W;
+  if (p.nkv * (int)__reduce_add_sync(0xffffffffu, (unsigned)per) <= grid) {
+    m = W;
+  } else {
+    if (items <= grid) {
+      const int lo = max(W, (int)((unsigned)(total + grid - 1) / (unsigned)grid));
+      const int hi = max(lo, items < grid ? (int)((unsigned)(total + grid - items - 1) / (unsigned)(grid - items)) : total);
+      const unsigned mine = lane < 31 ? lo + (unsigned)(hi - lo) / 31u * lane : hi;
+      unsigned ranges = 0;
+#pragma unroll 1
+      for (int b = 0; b < p.nb; ++b) ranges += ((unsigned)__shfl_sync(0xffffffffu, n, b) + mine - 1) / mine;
+      const unsigned fits = __ballot_sync(0xffffffffu, p.nkv * (int)ranges <= grid);
+      m = fits ? (int)__shfl_sync(0xffffffffu, mine, __ffs(fits) - 1) : 0;
+      // a second range costs a CTA about what three tiles of every warp do
+      if (m > lo + 3 * W) m = 0;
     }
-    const unsigned fits = __ballot_sync(0xffffffffu, p.nkv * ranges <= grid);
-    m = fits ? __shfl_sync(0xffffffffu, mine, __ffs(fits) - 1) : 0;
-    // a second range costs a CTA about what three tiles of every warp do
-    if (m > lo + 3 * W) m = 0;
+    per = m ? (int)((unsigned)(n + m - 1) / (unsigned)m) : n;
   }
-  int units = p.nkv * (m ? (n + m - 1) / m : n), incl = units;
+  int incl = p.nkv * per;
 #pragma unroll
   for (int o = 1; o < kMaxB; o <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -273,11 +276,16 @@ __device__ __forceinline__ void plan_work(const Params& p, Small& sm) {
   if (lane == 0) {
     sm.at[0] = 0;
     sm.m = m;
-    sm.q = total / grid;
-    sm.rem = total % grid;
-    sm.near = min(sm.q / 4, 2 * W);
+    if (!m) {
+      sm.q = (unsigned)total / (unsigned)grid;
+      sm.rem = total - sm.q * grid;
+      sm.near = min(sm.q / 4, 2 * W);
+    }
   }
-  if (lane < kMaxB) sm.at[lane + 1] = incl;
+  if (lane < kMaxB) {
+    sm.at[lane + 1] = incl;
+    sm.per[lane] = per;
+  }
   __syncwarp();
   const int c = blockIdx.x, all = sm.at[p.nb];
   const int u0 = all == 0 ? 0 : m ? min(c, all) : span_first(p, sm, c);
@@ -289,7 +297,7 @@ __device__ __forceinline__ void plan_work(const Params& p, Small& sm) {
 }
 
 // The range of this CTA that begins at unit t < unit_end, and where its rows are.
-template <int HD, int TR>
+template <int HD, int TR, int W>
 __device__ __forceinline__ void set_range(const Params& p, Small& sm, int t) {
   const Item it = item_at(p, sm, t);
   const int n = sm.T[it.b] / TR + 1, parts = it.end - it.first, k = t - it.first;
@@ -299,10 +307,13 @@ __device__ __forceinline__ void set_range(const Params& p, Small& sm, int t) {
     sm.g = it.g;
     sm.first = it.first;
     sm.end = it.end;
-    if (sm.m) {
-      const int t0 = (int)((long long)k * n / parts), t1 = (int)((long long)(k + 1) * n / parts);
-      sm.tile0 = t0;
-      sm.ntile = t1 - t0;
+    if (sm.m == W) {
+      sm.tile0 = k * W;
+      sm.ntile = min(W, n - k * W);
+    } else if (sm.m) {
+      const int len = (unsigned)n / (unsigned)parts, more = n - len * parts;
+      sm.tile0 = k * len + min(k, more);
+      sm.ntile = len + (k < more);
     } else {
       sm.tile0 = k;
       sm.ntile = end - t;
@@ -405,12 +416,12 @@ __device__ __forceinline__ void prepare(const Params& p, Small& sm, uint32_t* qf
       e = min(max(e, -103), 100);
       // codes reach the MMA as n 2^-24 (low nibbles) or n 2^-20 (high), so q is divided by 16 against the latter
       const int k16 = lane >> 4;
-      const float up = __uint_as_float((uint32_t)(127 + e - 4 * k16) << 23);
+      const float up = __uint_as_float((uint32_t)(127 + e) << 23), down = k16 ? 0.0625f : 1.f;
       if (lane == 0) sm.qf[j] = __uint_as_float((uint32_t)(127 + 24 - e) << 23);
 #pragma unroll
       for (int hb = 0; hb < 2; ++hb) {
         const int c = c0 + hb * (NB / 2);
-        const float v = x[k][hb] * up;
+        const float q = x[k][hb] * up, v = q * down;
         const __half h = __float2half_rn(v);
         const float hf = __half2float(h);
         const __half l = __float2half_rn(v - hf);
@@ -421,8 +432,9 @@ __device__ __forceinline__ void prepare(const Params& p, Small& sm, uint32_t* qf
         auto put = [&](int col, int part, __half val) {  // part: second fragment (low parts of 8 heads)
           f[((((c * NH + part) * 32 + col * 4 + w) * 4) + k16 * 2 + (i & 1)) * 2 + (i >> 1)] = val;
         };
-        // n = code + 8: -8 sum q goes on top
-        const float t = warp_sum((k16 ? -0x1p-17f : -0x1p-21f) * (hf + __half2float(l)));
+        // n = code + 8: -8 sum q goes on top.  The sum in steps of 2^-15 (|q| < 2^10, a
+        // row's score errs by 8 x 32 x 2^-16 of it at most); an infinite or NaN q is in the operands.
+        const float t = -0x1p-36f * (float)__reduce_add_sync(0xffffffffu, __float2int_rn(q * 32768.f));
         if (G == 8) {
           const int col = (j & 3) * 2 + (j >> 2);
           put(col, 0, h);
@@ -465,16 +477,22 @@ template <int HD, int G>
 __device__ __noinline__ void join_parts(const Params& p, Small& sm, uint8_t* smem, int first, int step, int n,
                                         bool final) {
   using Sh = Shape<HD>;
-  constexpr int NV = G * HD / 4, NX = 8;
+  constexpr int NV = G * HD / 4, VT = (NV + Sh::kThreads - 1) / Sh::kThreads, NX = VT == 1 ? 8 : 12;  // vectors of a thread
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c_lo = sm.c_lo, slot0 = sm.slot0;
   auto part_of = [&](int i) { return p.part + (2ll * (c_lo + i) + (i == 0 ? slot0 : 0)) * part_size(G, HD); };
   float* o = p.o + (long long)sm.b * p.ld_o + (long long)sm.g * G * HD;
   float* wt = reinterpret_cast<float*>(smem);  // [32][G] weights, joined reference and sum per head
-  float4 x[NX];
+  float4 x[VT][NX];
+  auto load = [&](int i0) {
 #pragma unroll
-  for (int i = 0; i < NX; ++i)
-    if (i < n && tid < NV) x[i] = __ldcg(reinterpret_cast<const float4*>(part_of(first + i * step)) + tid);
+    for (int i = 0; i < NX; ++i)
+#pragma unroll
+      for (int t = 0; t < VT; ++t)
+        if (i0 + i < n && tid + t * Sh::kThreads < NV)
+          x[t][i] = __ldcg(reinterpret_cast<const float4*>(part_of(first + (i0 + i) * step)) + tid + t * Sh::kThreads);
+  };
+  load(0);
   if (warp < G) {
     const int j = warp;
     float r = -INFINITY, l = 0.f;
@@ -494,23 +512,26 @@ __device__ __noinline__ void join_parts(const Params& p, Small& sm, uint8_t* sme
   }
   __syncthreads();
   float* dst = part_of(first);
-  for (int v = tid; v < NV; v += Sh::kThreads) {
-    const int j = v * 4 / HD;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < n; i0 += NX) {
-      if (i0 > 0 || v != tid) {
+  float4 a[VT];
 #pragma unroll
-        for (int i = 0; i < NX; ++i)
-          if (i0 + i < n) x[i] = __ldcg(reinterpret_cast<const float4*>(part_of(first + (i0 + i) * step)) + v);
-      }
+  for (int t = 0; t < VT; ++t) a[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += NX) {
+    if (i0 > 0) load(i0);
 #pragma unroll
-      for (int i = 0; i < NX; ++i)
-        if (i0 + i < n) add_scaled(a, wt[(i0 + i) * G + j], x[i]);
-    }
+    for (int i = 0; i < NX; ++i)
+#pragma unroll
+      for (int t = 0; t < VT; ++t)
+        if (i0 + i < n && tid + t * Sh::kThreads < NV)
+          add_scaled(a[t], wt[(i0 + i) * G + (tid + t * Sh::kThreads) * 4 / HD], x[t][i]);
+  }
+#pragma unroll
+  for (int t = 0; t < VT; ++t) {
+    const int v = tid + t * Sh::kThreads, j = v * 4 / HD;
+    if (v >= NV) break;
     if (final) {
-      put_out(o + v * 4, a, 1.0f / wt[33 * G + j]);
+      put_out(o + v * 4, a[t], 1.0f / wt[33 * G + j]);
     } else {
-      reinterpret_cast<float4*>(dst)[v] = a;
+      reinterpret_cast<float4*>(dst)[v] = a[t];
       if (v * 4 % HD == 0) {
         dst[G * HD + j] = wt[32 * G + j];
         dst[G * HD + G + j] = wt[33 * G + j];
@@ -602,7 +623,7 @@ __global__ void __launch_bounds__(Shape<HD>::kThreads, Shape<HD>::kCtas) k_attn(
   if (warp == 0) {
     plan_work<TR, W>(p, sm);
     __syncwarp();
-    if (sm.unit < sm.unit_end) set_range<HD, TR>(p, sm, sm.unit);
+    if (sm.unit < sm.unit_end) set_range<HD, TR, W>(p, sm, sm.unit);
   }
   __syncthreads();
   if (sm.at[p.nb] == 0) pdl_wait();  // the next kernel counts on this one for all before it
@@ -898,19 +919,30 @@ __global__ void __launch_bounds__(Shape<HD>::kThreads, Shape<HD>::kCtas) k_attn(
     more = sm.next < sm.unit_end;
     __syncthreads();
     if (more) {
-      if (warp == 0) set_range<HD, TR>(p, sm, sm.next);
+      if (warp == 0) set_range<HD, TR, W>(p, sm, sm.next);
       __syncthreads();
     }
   }
 }
 
 // ------------------------------------------------------------ append
-// Rows of n tokens at positions T .. T + n - 1 of one sequence: a warp takes
-// blocks c and c + NB / 2 of one k or v vector (for k they hold the halves of
-// the rotate-half pairs), a value of each per lane.
-template <int HD>
+// Rows of n tokens at positions T .. T + n - 1 of one sequence.  A lane holds 4
+// adjacent values (hd 256: two such groups, which are the halves of its
+// rotate-half pairs; else the other half is hd / 8 lanes away), 8 lanes a block,
+// a warp two vectors (hd 64) or one; the loads of kUnits of them are on their
+// way together.  Bound by its bytes: one pass, 16-byte accesses.  VEC: y, the
+// table and kv_new are 16-byte aligned with rows of whole 16 bytes.
+constexpr int kUnits = 2;
+
+template <bool VEC>
+__device__ __forceinline__ float4 load4(const float* p) {
+  return VEC ? *reinterpret_cast<const float4*>(p) : make_float4(p[0], p[1], p[2], p[3]);
+}
+
+template <int HD, bool VEC>
 __global__ void __launch_bounds__(256) k_append(const AppendParams p) {
-  constexpr int NB = HD / 32, NH = NB / 2;
+  constexpr int NB = HD / 32, NH = HD == 256 ? 2 : 1;  // groups of 4 values of a lane
+  constexpr int VW = HD == 64 ? 2 : 1, LV = 32 / VW;     // vectors of a warp, lanes of a vector
   const int lane = threadIdx.x & 31;
   const int T = p.len ? *p.len : p.t0;
   if (T < 0 || (long long)T + p.n > p.cap) {
@@ -918,31 +950,97 @@ __global__ void __launch_bounds__(256) k_append(const AppendParams p) {
     return;
   }
   const long long cap_s = ((long long)p.cap + 3) & ~3ll;
-  const long long units = (long long)p.n * 2 * p.nkv * NH;
-  const long long step = (long long)gridDim.x * (blockDim.x >> 5);
-  for (long long u = blockIdx.x * (long long)(blockDim.x >> 5) + (threadIdx.x >> 5); u < units; u += step) {
-    const int c = (int)(u % NH);
-    const int g = (int)(u / NH % p.nkv);
-    const int kv = (int)(u / NH / p.nkv % 2);
-    const long long i = u / NH / p.nkv / 2;
-    const float* x = p.y + i * p.ld_y + (long long)(p.nq + kv * p.nkv + g) * HD + c * 32 + lane;
-    float x0 = x[0], x1 = x[HD / 2];
-    if (kv == 0) {
-      const float2 cs = p.rope[(T + i) * (HD / 2) + c * 32 + lane];
-      float r0, r1;
-      rotate(x0, x1, cs, &r0, &r1);
-      x0 = r0;
-      x1 = r1;
-    }
-    uint8_t* codes = (kv ? p.V : p.K) + ((long long)g * p.cap + T + i) * (HD / 2);
-    uint16_t* scales = (kv ? p.Vs : p.Ks) + ((long long)g * cap_s + T + i) * NB;
-    float* val = p.kv_new ? p.kv_new + ((i * 2 + kv) * p.nkv + g) * HD : nullptr;
+  const long long vecs = (long long)p.n * 2 * p.nkv;  // token, k or v, kv head
+  const long long step = (long long)gridDim.x * (blockDim.x >> 5) * VW;
+  const int e = (lane % LV) * 4;  // the lane's first element
+  for (long long v0 = (blockIdx.x * (long long)(blockDim.x >> 5) + (threadIdx.x >> 5)) * VW; v0 < vecs;
+       v0 += step * kUnits) {
+    float4 x[kUnits][NH], c0[kUnits], c1[kUnits];
+    bool in[kUnits];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int cc = c + h * NH;
-      int code;
-      const uint16_t s = quant_block(h ? x1 : x0, &code);
-      store_block(s, code, codes + cc * 16, scales + cc, val ? val + cc * 32 : nullptr, lane);
+    for (int u = 0; u < kUnits; ++u) {
+      const long long v = v0 + u * step + lane / LV;
+      in[u] = v < vecs;
+      const long long vv = in[u] ? v : 0, i = vv / (2 * p.nkv);
+      const int kg = (int)(vv % (2 * p.nkv));  // kv * nkv + g
+      const float* y = p.y + i * p.ld_y + (long long)(p.nq + kg) * HD + e;
+#pragma unroll
+      for (int h = 0; h < NH; ++h) x[u][h] = load4<VEC>(y + h * (HD / 2));
+      if (kg < p.nkv) {
+        const float* cs = reinterpret_cast<const float*>(p.rope + (T + i) * (HD / 2) + e % (HD / 2));
+        c0[u] = load4<VEC>(cs);
+        c1[u] = load4<VEC>(cs + 4);
+      } else {
+        c0[u] = c1[u] = make_float4(1.f, 0.f, 1.f, 0.f);  // v is not rotated: x * 1 - y * 0 below is not taken
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const long long v = v0 + u * step + lane / LV;
+      if (!__any_sync(0xffffffffu, in[u])) break;
+      const long long vv = in[u] ? v : 0, i = vv / (2 * p.nkv);
+      const int kg = (int)(vv % (2 * p.nkv)), kv = kg >= p.nkv, g = kv ? kg - p.nkv : kg;
+      float f[NH][4] = {{x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w}};
+      if (NH == 2) {
+        f[NH - 1][0] = x[u][NH - 1].x;
+        f[NH - 1][1] = x[u][NH - 1].y;
+        f[NH - 1][2] = x[u][NH - 1].z;
+        f[NH - 1][3] = x[u][NH - 1].w;
+      }
+      const float2 cs[4] = {{c0[u].x, c0[u].y}, {c0[u].z, c0[u].w}, {c1[u].x, c1[u].y}, {c1[u].z, c1[u].w}};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float r0, r1;
+        if (NH == 2) {
+          rotate(f[0][k], f[NH - 1][k], cs[k], &r0, &r1);
+          if (!kv) {
+            f[0][k] = r0;
+            f[NH - 1][k] = r1;
+          }
+        } else {
+          const float o = __shfl_xor_sync(0xffffffffu, f[0][k], LV / 2);
+          const bool second = e >= HD / 2;
+          rotate(second ? o : f[0][k], second ? f[0][k] : o, cs[k], &r0, &r1);
+          if (!kv) f[0][k] = second ? r1 : r0;
+        }
+      }
+      const long long row = (long long)g * p.cap + T + i, row_s = (long long)g * cap_s + T + i;
+      uint8_t* codes = (kv ? p.V : p.K) + row * (HD / 2);
+      uint16_t* scales = (kv ? p.Vs : p.Ks) + row_s * NB;
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        const int el = e + h * (HD / 2), blk = el / 32;
+        uint32_t a = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) a = max(a, __float_as_uint(f[h][k]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+        float inv;
+        const __half sh = block_scale(a, &inv);
+        const float sf = __half2float(sh);
+        uint32_t n = 0;
+        float val[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = quant_code(f[h][k], inv);
+          n |= (uint32_t)(c + 8) << (8 * k);
+          val[k] = __fmul_rn(sf, (float)c);
+        }
+        const uint32_t up = __shfl_down_sync(0xffffffffu, n, 4);  // elements 16 .. 31 of the block: lanes 4 .. 7
+        if (in[u]) {
+          if ((lane & 7) < 4) *reinterpret_cast<uint32_t*>(codes + blk * 16 + (lane & 7) * 4) = n | (up << 4);
+          if ((lane & 7) == 0) scales[blk] = __half_as_ushort(sh);
+          if (p.kv_new) {
+            float* d = p.kv_new + (i * 2 * p.nkv + kg) * HD + el;
+            if (VEC) {
+              *reinterpret_cast<float4*>(d) = make_float4(val[0], val[1], val[2], val[3]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) d[k] = val[k];
+            }
+          }
+        }
+      }
     }
   }
 }
@@ -1001,15 +1099,19 @@ cudaError_t launch(const Params& p, int hd, int nsm, cudaStream_t st, bool pdl) 
 
 cudaError_t append(const AppendParams& p, int hd, cudaStream_t st) {
   if (p.n <= 0) return cudaSuccess;
-  const long long units = (long long)p.n * 2 * p.nkv * (hd / 64);
-  long long blocks = (units + 7) / 8;
-  if (blocks > 4096) blocks = 4096;
+  const long long warps = (long long)p.n * 2 * p.nkv / (hd == 64 ? 2 : 1) / kUnits + 1;
+  long long blocks = (warps + 7) / 8;
+  if (blocks > 1 << 20) blocks = 1 << 20;
+  auto ok = [](const void* q) { return ((uintptr_t)q & 15) == 0; };
+  const bool vec = ok(p.y) && p.ld_y % 4 == 0 && ok(p.rope) && ok(p.kv_new);
+  void (*k)(AppendParams) = nullptr;
   switch (hd) {
-    case 64: k_append<64><<<(unsigned)blocks, 256, 0, st>>>(p); break;
-    case 128: k_append<128><<<(unsigned)blocks, 256, 0, st>>>(p); break;
-    case 256: k_append<256><<<(unsigned)blocks, 256, 0, st>>>(p); break;
+    case 64: k = vec ? k_append<64, true> : k_append<64, false>; break;
+    case 128: k = vec ? k_append<128, true> : k_append<128, false>; break;
+    case 256: k = vec ? k_append<256, true> : k_append<256, false>; break;
     default: return cudaErrorInvalidValue;
   }
+  k<<<(unsigned)blocks, 256, 0, st>>>(p);
   return cudaGetLastError();
 }
 

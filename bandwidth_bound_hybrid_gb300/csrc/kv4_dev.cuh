@@ -10,20 +10,29 @@
 namespace hy {
 namespace kv4 {
 
-// One block of 32 values, one per lane of a full warp: its fp16 scale (bits)
-// and the lane's code.  s = fp16(min(max |x| * fp32(1 / 7), 65504)), code =
-// round-half-even(x * (1 / s)) clamped to [-7, 7]; an infinity or NaN in the
-// block makes the scale NaN, so that it shows in whatever reads the block.
-__device__ __forceinline__ uint16_t quant_block(float x, int* code) {
-  // |x| as bits: the order of finite values, infinities above, NaN above those
-  const uint32_t a = __reduce_max_sync(0xffffffffu, __float_as_uint(x) & 0x7fffffffu);
+// The scale of a block whose largest |x| has the bits a (the order of finite
+// values, infinities above, NaN above those): s = fp16(min(max |x| * fp32(1 /
+// 7), 65504)), and what the values are multiplied by, 1 / s (0 for s = 0).  An
+// infinity or NaN in the block makes the scale NaN, so that it shows in
+// whatever reads the block.
+__device__ __forceinline__ __half block_scale(uint32_t a, float* inv) {
   float s = NAN;
   if (a < 0x7f800000u) s = fminf(__fmul_rn(__uint_as_float(a), 1.0f / 7.0f), 65504.0f);
   const __half sh = __float2half_rn(s);
   const float sf = __half2float(sh);
-  const float inv = sf > 0.f ? __fdiv_rn(1.0f, sf) : 0.f;
-  const float r = fminf(fmaxf(rintf(__fmul_rn(x, inv)), -7.f), 7.f);
-  *code = (int)r;
+  *inv = sf > 0.f ? __fdiv_rn(1.0f, sf) : 0.f;
+  return sh;
+}
+// code = round-half-even(x * (1 / s)) clamped to [-7, 7]
+__device__ __forceinline__ int quant_code(float x, float inv) {
+  return (int)fminf(fmaxf(rintf(__fmul_rn(x, inv)), -7.f), 7.f);
+}
+
+// One block of 32 values, one per lane of a full warp: its fp16 scale (bits) and the lane's code.
+__device__ __forceinline__ uint16_t quant_block(float x, int* code) {
+  float inv;
+  const __half sh = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(x) & 0x7fffffffu), &inv);
+  *code = quant_code(x, inv);
   return __half_as_ushort(sh);
 }
 
