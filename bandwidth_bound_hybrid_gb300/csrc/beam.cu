@@ -8,9 +8,9 @@
 // enough.  A CTA takes a chunk of a beam's row and streams through it with a
 // running maximum and sum of exponentials per lane.  The picks-th largest of
 // the CTA's 256 running maxima is a bound that `picks` logits are known to
-// reach; it is worked out after 1, 2, 4, 8, ... steps (a bitonic network across
+// reach; it is worked out after 1, 4, 16, 64, ... steps (a bitonic network across
 // the lanes of each warp, then merges of the 8 lists), so that between two of
-// these about `picks` logits reach it.  Those few are kept, by each warp on its
+// these a few times `picks` logits reach it.  Those few are kept, by each warp on its
 // own: 32 at a time are sorted and merged into the warp's best 32, a lane
 // each.  So the pass costs an exponential and a comparison a logit, and is
 // bound by reading the logits.
@@ -43,6 +43,23 @@ constexpr int kStep = kPer * 32;         // and of a warp
 constexpr int kFew = 4;                  // words of a thread in the final selection of few lists
 constexpr int kQual = 1024;              // lists looked into by the fast final selection
 constexpr int kBest = 2048;              // and their candidates
+
+// Sums of exponentials are held as S = sum 2^(x log2 e - c(M)) with the largest x
+// = M and c(M) the FP32 product M log2 e: one fused multiply-add, one ex2 and one
+// addition a logit, and the product's rounding is part of the reference and
+// cancels.  From 2^30 on the rounding leaves ex2's range; FP32 numbers of that
+// size are 64 apart or equal, so S then counts the x that equal M.
+constexpr float kLog2e = 1.44269504088896340736f;
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ bool large(float M) { return !(fabsf(M) < 0x1p30f); }
+// what a sum with reference Ma counts for beside Mb >= Ma
+__device__ __forceinline__ float carry(float Ma, float Mb) {
+  return Ma == Mb ? 1.f : large(Ma) || large(Mb) ? 0.f : ex2(__fmul_rn(Ma, kLog2e) - __fmul_rn(Mb, kLog2e));
+}
 
 // A candidate of a chunk in one word: the logit's order key above the
 // complement of the token, so that the larger word is the better candidate
@@ -168,6 +185,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_select(const SelectParams p
       top = warp_join(top, __shfl_sync(0xffffffffu, (unsigned long long)warp_sort(w, lane), 31 - lane), lane);
     };
     float low = -FLT_MAX;  // -infinity is no candidate
+    int due = 1, turn = 0;
     const int steps = (int)((end - first + kWarps * kStep - 1) / (kWarps * kStep));
     float v[kPer], next[kPer];  // a step's logits; the next step's are on their way meanwhile
     auto load = [&](int it, float* d) {
@@ -182,7 +200,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_select(const SelectParams p
       }
     };
     load(0, next);
-#pragma unroll 2
     for (int it = 0; it < steps; ++it) {
       const int i0 = (int)first + (it * kWarps + warp) * kStep + lane;
 #pragma unroll
@@ -192,19 +209,25 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_select(const SelectParams p
 #pragma unroll
       for (int k = 1; k < kPer; ++k) m = fmaxf(m, v[k]);
       m = fmaxf(m, -INFINITY);
-      const float Mn = fmaxf(M, m), ref = Mn == -INFINITY ? 0.f : Mn;
+      const float Mn = fmaxf(M, m), c = __fmul_rn(Mn, kLog2e);
       float add = 0.f;
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) add += __expf(v[k] - ref);
-      if (add != add) {  // a NaN counts as -infinity (+infinity leaves NaN: the beam has no finite scores)
+      for (int k = 0; k < kPer; ++k) add += ex2(fmaf(v[k], kLog2e, -c));
+      if (!(add <= FLT_MAX) || large(Mn)) {  // a NaN, which counts as -infinity, or large logits
         add = 0.f;
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) add += __expf(fmaxf(v[k], -INFINITY) - ref);
+        for (int k = 0; k < kPer; ++k) {
+          if (large(Mn))
+            add += v[k] == Mn && Mn > -INFINITY ? 1.f : 0.f;
+          else
+            add += ex2(fmaf(fmaxf(v[k], -INFINITY), kLog2e, -c));
+        }
       }
-      s = s * __expf(M - ref) + add;
+      s = s * carry(M, Mn) + add;
       M = Mn;
-      if ((it & (it + 1)) == 0 && (it == 0 || it + 1 < steps)) {  // 1, 2, 4, ... steps done
-        low = fmaxf(low, key_value(cta_nth(sm.sorted[__popc(it) & 1], order_key(M), P, lane, warp)));
+      if (it + 1 == due && (it == 0 || due < steps)) {  // 1, 4, 16, ... steps done
+        due *= 4;
+        low = fmaxf(low, key_value(cta_nth(sm.sorted[turn ^= 1], order_key(M), P, lane, warp)));
       }
       if (__any_sync(0xffffffffu, m >= low)) {
         uint32_t hit = 0;
@@ -223,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_select(const SelectParams p
     flush();
     // the warps' lists, maxima and sums
     const float Mw = warp_max(M);
-    const float sw = warp_sum(M > -INFINITY ? s * __expf(M - Mw) : 0.f);
+    const float sw = warp_sum(s * carry(M, Mw));
     if (lane == 0) {
       sm.m[warp] = Mw;
       sm.sum[warp] = sw;
@@ -241,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_select(const SelectParams p
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) Mc = fmaxf(Mc, sm.m[w]);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) S += sm.m[w] > -INFINITY ? sm.sum[w] * __expf(sm.m[w] - Mc) : 0.f;
+      for (int w = 0; w < kWarps; ++w) S += sm.sum[w] * carry(sm.m[w], Mc);
       p.stats[slot] = make_float2(Mc, S);
     }
   }
@@ -274,18 +297,25 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_select(const SelectParams p
       float M = t0.x;
       for (int c = lane + 32; c < nch; c += 32) M = fmaxf(M, __ldcg(st + c).x);
       M = warp_max(M);
-      double S = t0.x > -INFINITY ? (double)(t0.y * expf(t0.x - M)) : 0.0;
+      double S = lane < nch ? (double)(t0.y * carry(t0.x, M)) : 0.0;
       for (int c = lane + 32; c < nch; c += 32) {
         const float2 t = __ldcg(st + c);
-        if (t.x > -INFINITY) S += (double)(t.y * expf(t.x - M));
+        S += (double)(t.y * carry(t.x, M));
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
-      // S = 2^e f, f in [0.75, 1.5): the FP32 logarithm of f errs by 2^-25 at most, e log 2 is FP64
+      // log of S = 2^e f, f in [0.75, 1.5): the FP32 logarithm of f errs by 2^-25 at most, e log 2 is FP64
       const float Sf = (float)S;
       const int e = (int)((__float_as_uint(Sf) + 0x00400000u) >> 23) - 127;
       const float f = __uint_as_float(__float_as_uint(Sf) - ((uint32_t)e << 23));
-      off -= (double)M + (double)e * 0.69314718055994530942 + (double)(logf(f) + (float)(S - (double)Sf) / Sf);
+      const double log2 = 0.69314718055994530942;
+      double top = (double)M;
+      if (!large(M)) {
+        // the reference's value; kLog2e = (1 - d) log2 e makes the sums those of exp((1 - d) x), which lacks d times
+        // the mean of x (here: the largest)
+        top = (double)__fmul_rn(M, kLog2e) * log2 + (1.0 - (double)kLog2e * log2) * (double)M;
+      }
+      off -= top + (double)e * log2 + (double)(logf(f) + (float)(S - (double)Sf) / Sf);
     }
     if (lane == 0) {
       sm.off[w] = off - off == 0.0 ? off : -INFINITY;

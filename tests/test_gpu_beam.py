@@ -2,10 +2,12 @@
 against plain FP64 / numpy forms.
 
 Scores: |error| <= 2^-19 + 2^-24 |score|.  The last is the rounding of the FP32
-output; lse errs by the relative error of the FP32 sum of exponentials, at
-most 2^-21 of each fast exponential, 2 u |x - max| of its argument weighted by
-the probabilities (below 2^-21 for a mean |x - max| under 8), and gamma(16 +
-16) of the sums in a thread and across the CTA (the chunks are added in FP64).
+output; lse errs by the relative error of the FP32 sum of exponentials: at
+most 2^-21 of each ex2.approx and its argument's rounding (an argument below 8
+in the terms that matter: 2^-22), and gamma(16 + 16) of the sums in a lane,
+across the CTA and its carries (the chunks are added in FP64); the constant
+log2 e of FP32 moves lse by 2^-26 times the distance of the mean logit from
+the largest, 2^-22 below a distance of 16.
 Picks have to be equal: wherever the reference has two candidates of
 different beams closer than twice that bound the case would be ambiguous, so
 every case asserts that it has none (within a beam the logits' order is
