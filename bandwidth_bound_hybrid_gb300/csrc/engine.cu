@@ -47,6 +47,9 @@ int fail(int code, const char* fmt, ...) {
   } while (0)
 
 bool aligned16(const void* p) { return p && ((uintptr_t)p & 15u) == 0; }
+// Not null and aligned for FP32 / int32 (or, of 8, for pairs of them).
+bool aligned(const void* p, size_t n = 4) { return p && ((uintptr_t)p & (n - 1)) == 0; }
+bool null_or_aligned(const void* p) { return !p || aligned(p); }
 
 std::mutex g_init_mu;
 std::map<int, bool> g_inited;
@@ -1660,7 +1663,7 @@ int32_t hy_seq_len(const hy_cache* c, int32_t seq) { return valid_seq(c, seq) ? 
 int32_t hy_seq_capacity(const hy_cache* c, int32_t seq) { return valid_seq(c, seq) ? c->cap[seq] : -1; }
 int32_t hy_step_kernels(const hy_cache* c) { return c ? c->last_kernels : 0; }
 int32_t hy_step_splits(const hy_cache* c, int32_t seq) {
-  if (!c || seq < 0 || seq >= (int32_t)c->cap.size() || !c->m->n_attn) return 0;
+  if (!c || seq < 0 || seq >= (int32_t)c->cap.size() || !c->m->n_attn || c->m->cfg.kv_format == 2) return 0;
   return c->cap[seq] >= attn::kLongContext ? c->m->splits_long : c->m->splits;
 }
 
@@ -1818,7 +1821,7 @@ int hy_seq_copy(hy_cache* c, int32_t src, int32_t dst, void* stream) {
 
 int hy_seq_reorder(hy_cache* c, const int32_t* seqs_host, int32_t n, const int32_t* parent_dev, int32_t first,
                    void* stream) {
-  if (!c || !seqs_host || !parent_dev || n < 1 || n > beam::kMaxBeams || first < 0)
+  if (!c || !seqs_host || !aligned(parent_dev) || n < 1 || n > beam::kMaxBeams || first < 0)
     return fail(HY_ERR_ARG, "bad reordering arguments (1..%d sequences)", beam::kMaxBeams);
   const std::vector<int> seqs(seqs_host, seqs_host + n);
   for (int i = 0; i < n; ++i) {
@@ -2371,7 +2374,7 @@ static int check_q4_cache(const void* K, const void* Ks, const void* V, const vo
 size_t hy_op_attention_q4_workspace(int32_t batch, int32_t nq, int32_t nkv, int32_t hd) {
   if (batch < 1 || batch > kv4::kMaxB || nkv <= 0 || nq <= 0 || nq % nkv || hd <= 0) return 0;
   if ((hd != 64 && hd != 128 && hd != 256) || nq / nkv > 8 || ((nq / nkv) & (nq / nkv - 1))) return 0;
-  return (kv4::counters(batch, nkv) * 4 + 255) / 256 * 256 + kv4::part_floats(nq, nkv, hd, op_nsm()) * 4;
+  return (kv4::counters(kv4::kMaxB, nkv) * 4 + 255) / 256 * 256 + kv4::part_floats(nq, nkv, hd, op_nsm()) * 4;
 }
 
 int hy_op_attention_q4(const float* y_dev, int32_t ldy, int32_t batch, void* Kq_dev, void* Ks_dev, void* Vq_dev,
@@ -2380,7 +2383,8 @@ int hy_op_attention_q4(const float* y_dev, int32_t ldy, int32_t batch, void* Kq_
                        void* stream) {
   int rc = check_q4_cache(Kq_dev, Ks_dev, Vq_dev, Vs_dev, batch, cap, nq, nkv, hd);
   if (rc != HY_OK) return rc;
-  if (!y_dev || !len_dev || !rope_table_dev || !o_dev || !aligned16(workspace_dev) || batch < 1 ||
+  if (!aligned(y_dev) || !aligned(len_dev) || !aligned(rope_table_dev, 8) || !aligned(o_dev) ||
+      !null_or_aligned(kv_new_dev) || !aligned16(workspace_dev) || batch < 1 ||
       batch > kv4::kMaxB || (long long)ldy < ((long long)nq + 2 * nkv) * hd || (long long)ldo < (long long)nq * hd)
     return fail(HY_ERR_ARG, "bad 4-bit attention arguments (batch 1..%d, ldy >= (nq + 2 nkv) hd, ldo >= nq hd)",
                 kv4::kMaxB);
@@ -2399,7 +2403,7 @@ int hy_op_attention_q4(const float* y_dev, int32_t ldy, int32_t batch, void* Kq_
   a.nb = batch;
   a.scale_log2e = kv4_scale(hd);
   a.counter = (unsigned*)workspace_dev;
-  a.part = (float*)((uint8_t*)workspace_dev + (kv4::counters(batch, nkv) * 4 + 255) / 256 * 256);
+  a.part = (float*)((uint8_t*)workspace_dev + (kv4::counters(kv4::kMaxB, nkv) * 4 + 255) / 256 * 256);  // the same for every batch
   a.guard = guard;
   for (int b = 0; b < batch; ++b) {
     const size_t row = (size_t)b * nkv * cap, row_s = (size_t)b * nkv * cap_scales(cap);
@@ -2420,7 +2424,8 @@ int hy_op_kv_append_q4(const float* y_dev, int32_t ldy, int32_t n, void* Kq_dev,
                        const float* rope_table_dev, float* kv_new_dev, void* stream) {
   int rc = check_q4_cache(Kq_dev, Ks_dev, Vq_dev, Vs_dev, 1, cap, nq, nkv, hd);
   if (rc != HY_OK) return rc;
-  if ((n > 0 && !y_dev) || !len_dev || !rope_table_dev || n < 0 ||
+  if ((n > 0 && !aligned(y_dev)) || !aligned(len_dev) || !aligned(rope_table_dev, 8) || !null_or_aligned(kv_new_dev) ||
+      n < 0 ||
       (long long)ldy < ((long long)nq + 2 * nkv) * hd)
     return fail(HY_ERR_ARG, "bad 4-bit append arguments (ldy >= (nq + 2 nkv) hd)");
   if (n > cap) return fail(HY_ERR_CAPACITY, "%d rows exceed the capacity %d", n, cap);
@@ -2463,8 +2468,9 @@ int hy_op_beam_select(const float* logits_dev, int32_t ldl, int32_t groups, int3
                       int32_t picks, const float* score_dev, const int32_t* done_dev, int32_t eos,
                       float* score_out_dev, int32_t* parent_out_dev, int32_t* token_out_dev, int32_t* done_out_dev,
                       void* workspace_dev, void* stream) {
-  if (!logits_dev || !score_dev || !score_out_dev || !parent_out_dev || !token_out_dev || !aligned16(workspace_dev) ||
-      groups <= 0 || beams <= 0 || vocab <= 0 || picks <= 0 || ldl < vocab)
+  if (!aligned(logits_dev) || !aligned(score_dev) || !aligned(score_out_dev) || !aligned(parent_out_dev) ||
+      !aligned(token_out_dev) || !null_or_aligned(done_dev) || !null_or_aligned(done_out_dev) ||
+      !aligned16(workspace_dev) || groups <= 0 || beams <= 0 || vocab <= 0 || picks <= 0 || ldl < vocab)
     return fail(HY_ERR_ARG, "bad beam selection arguments");
   if ((long long)picks > (long long)beams * vocab)
     return fail(HY_ERR_ARG, "%d picks of %d beams x %d tokens", picks, beams, vocab);
@@ -2500,7 +2506,7 @@ int hy_op_beam_select(const float* logits_dev, int32_t ldl, int32_t groups, int3
 
 int hy_op_beam_reorder(void* state_dev, int64_t beam_stride, int32_t n_seg, int64_t seg_stride, int64_t seg_bytes,
                        int32_t groups, int32_t beams, const int32_t* parent_dev, void* stream) {
-  if (!aligned16(state_dev) || !parent_dev || groups <= 0 || beams <= 0 || n_seg <= 0 || seg_bytes < 0 ||
+  if (!aligned16(state_dev) || !aligned(parent_dev) || groups <= 0 || beams <= 0 || n_seg <= 0 || seg_bytes < 0 ||
       beam_stride % 16 || seg_stride % 16 || seg_bytes % 16)
     return fail(HY_ERR_ARG, "bad beam reordering arguments (state, strides and segments in 16-byte pieces)");
   if ((n_seg > 1 && seg_stride < seg_bytes) ||

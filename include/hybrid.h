@@ -232,7 +232,8 @@ int hy_experts_read(hy_cache* c, void* stream, uint64_t* total_out);
 int32_t hy_step_kernels(const hy_cache* c);
 
 /* Split-KV chunks per kv head that a batch-1 decode step of sequence `seq`
- * uses: hy_config.attn_splits when set, else one CTA per SM across the kv
+ * uses (bf16 and int8 caches; 0 for the 4-bit cache, whose attention shares
+ * the cached rows over the GPU by itself and takes no count): hy_config.attn_splits when set, else one CTA per SM across the kv
  * heads, or, for a cache of 16384 positions or more with up to 4 query heads
  * per kv head, 64 splits run as two CTAs per SM.  0 for a bad sequence index
  * or a model without attention layers.  (A step of several sequences with
@@ -484,9 +485,9 @@ int hy_op_attention_i8(const float* y_dev, void* Kq_dev, float* Ks_dev, void* Vq
  * o and kv_new unwritten (HY_GUARD_BAD_POSITION); the others run.
  * rope_table_dev has at least cap rows.  The work is shared over the GPU by
  * cached rows whatever the mix of lengths.  workspace_dev:
- * hy_op_attention_q4_workspace() bytes, zeroed before its first use and then
- * passed unmodified to later calls; calls that can overlap on the GPU need a
- * workspace each. */
+ * hy_op_attention_q4_workspace() bytes (the same for every batch), zeroed
+ * before its first use and then passed unmodified to later calls of the same
+ * nq, nkv and hd; calls that can overlap on the GPU need a workspace each. */
 size_t hy_op_attention_q4_workspace(int32_t batch, int32_t nq, int32_t nkv, int32_t hd);
 int hy_op_attention_q4(const float* y_dev, int32_t ldy, int32_t batch, void* Kq_dev, void* Ks_dev, void* Vq_dev,
                        void* Vs_dev, int32_t cap, int32_t nq, int32_t nkv, int32_t hd, const int32_t* len_dev,

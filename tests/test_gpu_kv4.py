@@ -237,6 +237,29 @@ def test_attention_ragged_batches(L, nq, nkv, hd, lens):
     assert c.torch.equal(first, c.o)
 
 
+@pytest.mark.parametrize("nkv,hd,lens", [(64, 64, [300, 0, 299, 31, 310, 64, 5, 290]),  # more heads than CTAs
+                                          (13, 256, [2600, 2590, 2555, 2601])])  # 52 heads of equal length on 152 CTAs
+def test_attention_in_spans(L, nkv, hd, lens):
+    """Ranges of several heads in one CTA: spans of the tile list."""
+    c = Case(nkv, nkv, hd, lens, seed=4).upload()
+    ws = c.workspace(L)
+    for _ in range(2):
+        assert c.call(L, ws) == 0, L.hy_last_error()
+    c.check()
+    assert not ws[:8 * nkv * 32 * 4].any().item()
+
+
+def test_attention_workspace_serves_every_batch(L):
+    """One workspace, calls of different batches in turn."""
+    a = Case(16, 4, 128, [1500, 40, 900, 2000, 3, 77, 1200, 600], seed=20).upload()
+    b = Case(16, 4, 128, [5000], seed=21).upload()
+    ws = a.workspace(L)
+    assert ws.numel() == b.workspace(L).numel()
+    for c in (a, b, a, b):
+        assert c.call(L, ws) == 0
+        c.check()
+
+
 @pytest.mark.parametrize("qmul,kmul,vmul", [(40.0, 1.0, 1.0), (1e-3, 1.0, 1e4), (1.0, 30.0, 1e-5), (1e20, 1e-20, 1.0),
                                             (1.5, 1.0, 2e5), (0.0, 1.0, 1.0)])
 def test_attention_magnitudes(L, qmul, kmul, vmul):

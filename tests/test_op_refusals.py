@@ -25,7 +25,8 @@ def attn(L, **over):
 @pytest.mark.parametrize("over", [dict(y=None), dict(Kq=None), dict(Ks=A + 8), dict(Vq=A + 4), dict(Vs=None), dict(len=None),
                                   dict(rope=None), dict(o=None), dict(ws=None), dict(ws=A + 1), dict(cap=0), dict(cap=-3),
                                   dict(batch=0), dict(batch=9), dict(nq=0), dict(nkv=0), dict(nq=7), dict(ldy=12 * 64 - 1),
-                                  dict(ldo=8 * 64 - 1), dict(ldy=-1)])
+                                  dict(ldo=8 * 64 - 1), dict(ldy=-1), dict(y=A + 2), dict(len=A + 1),
+                                  dict(rope=A + 4), dict(o=A + 3), dict(new=A + 2)])
 def test_attention_q4_bad_arguments(L, over):
     assert attn(L, **over) == capi.HY_ERR_ARG
     assert L.hy_last_error()
@@ -52,7 +53,7 @@ def append(L, **over):
 
 def test_append_q4_refusals(L):
     for over in (dict(y=None), dict(Kq=A + 2), dict(Ks=None), dict(Vq=None), dict(Vs=None), dict(n=-1), dict(cap=0), dict(len=None),
-                 dict(rope=None), dict(ldy=12 * 64 - 1), dict(nq=3)):
+                 dict(rope=None), dict(ldy=12 * 64 - 1), dict(nq=3), dict(y=A + 1), dict(rope=A + 4), dict(new=A + 2), dict(len=A + 2)):
         assert append(L, **over) == capi.HY_ERR_ARG, over
     assert append(L, hd=80, ldy=10 ** 6) == capi.HY_ERR_UNSUPPORTED
     assert append(L, nq=32, ldy=10 ** 6) == capi.HY_ERR_UNSUPPORTED
@@ -72,7 +73,8 @@ def select(L, **over):
 def test_beam_select_refusals(L):
     for over in (dict(logits=None), dict(score=None), dict(so=None), dict(po=None), dict(to=None), dict(ws=None), dict(ws=A + 8),
                  dict(ldl=999), dict(groups=0), dict(beams=0), dict(vocab=0), dict(picks=0), dict(done=A), dict(done=A, eos=1000),
-                 dict(beams=1, vocab=3, ldl=3, picks=4), dict(groups=-1), dict(beams=-2)):
+                 dict(beams=1, vocab=3, ldl=3, picks=4), dict(groups=-1), dict(beams=-2), dict(logits=A + 2), dict(score=A + 1),
+                 dict(so=A + 2), dict(po=A + 2), dict(to=A + 2), dict(do=A + 2), dict(done=A + 2, eos=1)):
         assert select(L, **over) == capi.HY_ERR_ARG, over
     for over in (dict(beams=17), dict(picks=33), dict(beams=16, vocab=2 ** 28, ldl=2 ** 28), dict(groups=2 ** 30)):
         assert select(L, **over) == capi.HY_ERR_UNSUPPORTED, over
@@ -91,7 +93,7 @@ def reorder(L, **over):
 def test_beam_reorder_refusals(L):
     for over in (dict(state=None), dict(state=A + 4), dict(parent=None), dict(stride=4104), dict(pitch=1032), dict(seg=520),
                  dict(seg=-16), dict(groups=0), dict(beams=0), dict(n_seg=0), dict(pitch=496), dict(stride=3568),
-                 dict(n_seg=1, stride=496), dict(stride=-4096), dict(pitch=-1024)):
+                 dict(n_seg=1, stride=496), dict(stride=-4096), dict(pitch=-1024), dict(parent=A + 2)):
         assert reorder(L, **over) == capi.HY_ERR_ARG, over
     for over in (dict(beams=17), dict(groups=65536), dict(n_seg=65536, pitch=512, stride=2 ** 40)):
         assert reorder(L, **over) == capi.HY_ERR_UNSUPPORTED, over
