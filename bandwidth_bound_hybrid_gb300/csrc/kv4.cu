@@ -44,9 +44,9 @@ namespace {
 
 // Per head dim: warps of a CTA and CTAs per SM, rows of a warp's tile, and the
 // stages of its ring.  Registers set the warps: a lane holds hd / 4 output
-// accumulators (hd 128, 4 heads, 8 sequences of 120k-131k: 12 warps an SM 104
-// us, 16 warps in two CTAs 108, 8 warps 111; hd 256, 8 heads, 8 sequences of
-// 1k-16k: 8 warps 26.7 us, 12 warps 28.2, 10 warps 30.4).
+// accumulators (hd 128, 4 heads, 8 sequences of 120k-131k: 12 warps an SM 112
+// us, 16 warps in two CTAs 116, 8 warps 118, 10 warps 130; hd 256, 8 heads, 8
+// sequences of 1k-16k: 8 warps 26.7 us, 12 warps 28.2, 10 warps 30.4).
 template <int HD>
 struct Shape {
   static constexpr int W = HD == 128 ? 12 : 8;
@@ -70,7 +70,6 @@ struct alignas(16) Small {
   uint16_t scales[2][8];
   uint32_t amax[8][4];             // per head and pair of blocks: largest |q| (bits)
   float qf[8];                     // per head: 2^-e of the query normalisation
-  float2 qb[8][4];                 // per block and column pair: -8 sum q of the block
   float r[12][8], l[12][8];
   int last;
   // the work (set by warp 0, so that no warp holds it over its tiles)
@@ -112,17 +111,13 @@ __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t b
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
   return r;
 }
-// The nibbles n of two 16-bit halves as fp16 pairs, without arithmetic: a
-// nibble in the low bits of a half is the subnormal n 2^-24 (h[0], h[1]: of the
-// low and the high byte), one above it n 2^-20 (h[2], h[3]).
-__device__ __forceinline__ void nibbles(uint32_t w, uint32_t* h) {
-  const uint32_t w8 = w >> 8;
-  h[0] = w & 0x000f000fu;
-  h[1] = w8 & 0x000f000fu;
-  h[2] = w & 0x00f000f0u;
-  h[3] = w8 & 0x00f000f0u;
-}
-// The codes n - 8 themselves, in the same order: 1024 + n - 1032 and (1024 + 16 n) / 16 - 72.
+// The codes n - 8 of a word's nibbles n as fp16 pairs, one of each 16-bit
+// half: the low nibbles of the low and of the high bytes, then their high
+// nibbles.  1024 + n - 1032 and (1024 + 16 n) / 16 - 72, all exact.  (Leaving n
+// in the scores' operand and subtracting 8 sum q afterwards saves the
+// subtractions, 108 us for 114 at 8 x 125k rows, but the tensor cores round
+// the larger sums: errors of 0.4e-6 to 1.2e-6 of the outputs for 0.1e-6 to
+// 0.4e-6.)
 __device__ __forceinline__ void codes(uint32_t w, uint32_t* v) {
   const __half2 k1032 = u2h(0x64086408u), k16th = u2h(0x2c002c00u), k72 = u2h(0xd480d480u);
   const uint32_t w8 = w >> 8;
@@ -414,14 +409,13 @@ __device__ __forceinline__ void prepare(const Params& p, Small& sm, uint32_t* qf
       for (int i = 0; i < NB / 2; ++i) a = max(a, sm.amax[j][i]);
       int e = 9 + 127 - (int)(a >> 23);
       e = min(max(e, -103), 100);
-      // codes reach the MMA as n 2^-24 (low nibbles) or n 2^-20 (high), so q is divided by 16 against the latter
       const int k16 = lane >> 4;
-      const float up = __uint_as_float((uint32_t)(127 + e) << 23), down = k16 ? 0.0625f : 1.f;
-      if (lane == 0) sm.qf[j] = __uint_as_float((uint32_t)(127 + 24 - e) << 23);
+      const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+      if (lane == 0) sm.qf[j] = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
       for (int hb = 0; hb < 2; ++hb) {
         const int c = c0 + hb * (NB / 2);
-        const float q = x[k][hb] * up, v = q * down;
+        const float v = x[k][hb] * up;
         const __half h = __float2half_rn(v);
         const float hf = __half2float(h);
         const __half l = __float2half_rn(v - hf);
@@ -432,21 +426,16 @@ __device__ __forceinline__ void prepare(const Params& p, Small& sm, uint32_t* qf
         auto put = [&](int col, int part, __half val) {  // part: second fragment (low parts of 8 heads)
           f[((((c * NH + part) * 32 + col * 4 + w) * 4) + k16 * 2 + (i & 1)) * 2 + (i >> 1)] = val;
         };
-        // n = code + 8: -8 sum q goes on top.  The sum in steps of 2^-15 (|q| < 2^10, a
-        // row's score errs by 8 x 32 x 2^-16 of it at most); an infinite or NaN q is in the operands.
-        const float t = -0x1p-36f * (float)__reduce_add_sync(0xffffffffu, __float2int_rn(q * 32768.f));
         if (G == 8) {
           const int col = (j & 3) * 2 + (j >> 2);
           put(col, 0, h);
           put(col, 1, l);
-          if (lane == 0) (j < 4 ? sm.qb[c][j & 3].x : sm.qb[c][j & 3].y) = t;
         } else {
 #pragma unroll
           for (int m = 0; m < 4; ++m)
             if (m % G == j) {
               put(2 * m, 0, h);
               put(2 * m + 1, 0, l);
-              if (lane == 0) sm.qb[c][m] = make_float2(t, 0.f);
             }
         }
       }
@@ -696,14 +685,14 @@ __global__ void __launch_bounds__(Shape<HD>::kThreads, Shape<HD>::kCtas) k_attn(
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[c][t][k] = 0.f;
-    float mx[NH], ref[NH], lsum[NH], qf[NH];
+    float mx[NH], lsum[NH], qf[NH];
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
-      mx[h] = ref[h] = -INFINITY;
+      mx[h] = -INFINITY;
       lsum[h] = 0.f;
       qf[h] = sm.qf[G == 8 ? quad + 4 * h : quad % G];
     }
-    int sh = 29;  // probabilities are held as 2^sh p: p sV then fills fp16's range from above
+    int sh = 29;  // the products with V take 2^sh p, so that p sV fills fp16's range from above
     // ldmatrix row of this lane: 8-row groups of one block, or (16-row tiles) of two
     auto frag = [&](int cp, int half) {
       return NR == 4 ? place<NB>(lane, cp * 2 + half) : place<NB>(lane & 15, cp * 2 + (lane >> 4));
@@ -753,10 +742,9 @@ __global__ void __launch_bounds__(Shape<HD>::kThreads, Shape<HD>::kCtas) k_attn(
           const uint4 q0 = *reinterpret_cast<const uint4*>(qfrag + (c * NH * 32 + lane) * 4);
           uint4 q1;
           if (G == 8) q1 = *reinterpret_cast<const uint4*>(qfrag + ((c * NH + 1) * 32 + lane) * 4);
-          const float2 qb = sm.qb[c][quad];
           uint32_t h[NR][4];
 #pragma unroll
-          for (int n = 0; n < NR; ++n) nibbles(w[half][n], h[n]);
+          for (int n = 0; n < NR; ++n) codes(w[half][n], h[n]);
           // 16 rows a product; the products into one accumulator are apart
           float d[NR / 2][4];
 #pragma unroll
@@ -786,19 +774,18 @@ __global__ void __launch_bounds__(Shape<HD>::kThreads, Shape<HD>::kCtas) k_attn(
             const float f = half ? hi_f(sc[n]) : lo_f(sc[n]);
             const float *dn = d[n / 2] + (n & 1) * 2;
             if (G == 8) {
-              s[n][0] = fmaf(f, dn[0] + qb.x, s[n][0]);
-              s[n][NH - 1] = fmaf(f, dn[1] + qb.y, s[n][NH - 1]);
+              s[n][0] = fmaf(f, dn[0], s[n][0]);
+              s[n][NH - 1] = fmaf(f, dn[1], s[n][NH - 1]);
             } else {
-              s[n][0] = fmaf(f, (dn[0] + qb.x) + dn[1], s[n][0]);
+              s[n][0] = fmaf(f, dn[0] + dn[1], s[n][0]);
             }
           }
         }
       }
       // sV < 2^(E - 14) with E the exponent field of the largest, so 2^sh p sV <= 2^15
-      const int fit = 29 - (int)(vmax >> 10);
-      sh = fit < sh ? fit : sh;
-      float nref[NH];
-      bool moved = false;
+      const int fit = min(29 - (int)(vmax >> 10), sh);
+      bool moved = fit != sh;
+      float mn[NH];
       if (valid < TR) {
 #pragma unroll
         for (int n = 0; n < NR; ++n)
@@ -814,18 +801,20 @@ __global__ void __launch_bounds__(Shape<HD>::kThreads, Shape<HD>::kCtas) k_attn(
         tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 4));
         tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 8));
         tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
-        mx[h] = fmaxf(mx[h], tm * qf[h]);
-        nref[h] = mx[h] - (float)sh;
-        moved |= nref[h] != ref[h];
+        mn[h] = fmaxf(mx[h], tm * qf[h]);
+        moved |= mn[h] != mx[h];
       }
       if (__any_sync(0xffffffffu, moved)) {
         float corr[NH];
+        const float down = __uint_as_float((uint32_t)(127 + fit - sh) << 23);
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          corr[h] = ex2(ref[h] - nref[h]);
+          corr[h] = ex2(mx[h] - mn[h]);
           lsum[h] *= corr[h];
-          ref[h] = nref[h];
+          corr[h] *= down;
+          mx[h] = mn[h];
         }
+        sh = fit;
 #pragma unroll
         for (int c = 0; c < NB; ++c)
 #pragma unroll
@@ -833,12 +822,15 @@ __global__ void __launch_bounds__(Shape<HD>::kThreads, Shape<HD>::kCtas) k_attn(
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc[c][t][k] *= corr[G == 8 ? (k & 1) * (NH - 1) : 0];
       }
+      const float up = __uint_as_float((uint32_t)(127 + sh) << 23);
 #pragma unroll
       for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          s[n][h] = ex2(fmaf(s[n][h], qf[h], -ref[h]));
-          lsum[h] += s[n][h];
+          // the argument is near 0 where the weight is large: its rounding stays below 2^-24 of the weight
+          const float w = ex2(fmaf(s[n][h], qf[h], -mx[h]));
+          lsum[h] += w;
+          s[n][h] = w * up;
         }
       // outputs, two blocks at a time
 #pragma unroll
@@ -869,17 +861,27 @@ __global__ void __launch_bounds__(Shape<HD>::kThreads, Shape<HD>::kCtas) k_attn(
           uint32_t v[NR][4];
 #pragma unroll
           for (int n = 0; n < NR; ++n) codes(w[half][n], v[n]);
+          // a tile's products on their own, added to the running outputs in FP32: the tensor cores truncate
+          // what they add to an accumulator, which over a long context would be 2^-24 a product, all one way
+          float d[2][4];
 #pragma unroll
-          for (int part = 0; part < (G == 8 ? 2 : 1); ++part) {
+          for (int part = 0; part < NH; ++part) {
             const uint32_t* pp = part ? pl : ph;
 #pragma unroll
-            for (int m = 0; m < NR / 2; ++m) {
-              const int n = m * 2;
+            for (int n = 0; n < NR; n += 2)
 #pragma unroll
-              for (int t = 0; t < 2; ++t)
-                mma(acc[c][t], v[n][2 * t], v[n][2 * t + 1], v[n + 1][2 * t], v[n + 1][2 * t + 1], pp[n], pp[n + 1]);
-            }
+              for (int t = 0; t < 2; ++t) {
+                const uint32_t a0 = v[n][2 * t], a1 = v[n][2 * t + 1], a2 = v[n + 1][2 * t], a3 = v[n + 1][2 * t + 1];
+                if (part == 0 && n == 0)
+                  mma_c(d[t], a0, a1, a2, a3, pp[n], pp[n + 1], 0.f, 0.f, 0.f, 0.f);
+                else
+                  mma(d[t], a0, a1, a2, a3, pp[n], pp[n + 1]);
+              }
           }
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[c][t][k] += d[t][k];
         }
       }
       __syncwarp();  // every lane has read the stage before it is fetched into again
@@ -892,6 +894,7 @@ __global__ void __launch_bounds__(Shape<HD>::kThreads, Shape<HD>::kCtas) k_attn(
     // ---------------------------------------------------- join the warps
     constexpr int OP = out_pitch(HD);
     float* ow = reinterpret_cast<float*>(ring);  // [G][OP] of this warp, in its own ring
+    const float unit = __uint_as_float((uint32_t)(127 - sh) << 23);
     static_assert(G * OP * 4 <= Sh::kWarpRing, "a warp's outputs fit its ring");
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
@@ -901,7 +904,7 @@ __global__ void __launch_bounds__(Shape<HD>::kThreads, Shape<HD>::kCtas) k_attn(
       lsum[h] += __shfl_xor_sync(0xffffffffu, lsum[h], 16);
       if (j < G) {
         if (row8 == 0) {
-          sm.r[warp][j] = ref[h];
+          sm.r[warp][j] = mx[h];
           sm.l[warp][j] = lsum[h];
         }
 #pragma unroll
@@ -910,7 +913,7 @@ __global__ void __launch_bounds__(Shape<HD>::kThreads, Shape<HD>::kCtas) k_attn(
           for (int t = 0; t < 2; ++t) {
             const float* a = acc[c][t];
             *reinterpret_cast<float2*>(ow + j * OP + c * 32 + t * 16 + row8 * 2) =
-                G == 8 ? make_float2(a[h], a[2 + h]) : make_float2(a[0] + a[1], a[2] + a[3]);
+                G == 8 ? make_float2(a[h] * unit, a[2 + h] * unit) : make_float2((a[0] + a[1]) * unit, (a[2] + a[3]) * unit);
           }
       }
     }

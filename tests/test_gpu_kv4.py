@@ -10,13 +10,14 @@ gpu_util.attention_tolerance: with score errors delta_t and relative errors
 eps_t of the probabilities, |err| <= sum_t p_t (delta_t + eps_t) |V_t - o| +
 rel_sum sum_t p_t |V_t| + 16 u |o|.  Here (u = 2^-24; a tensor-core sum of n
 exact products is taken to err by at most 2 gamma(n), truncation included)
-  delta_t = scale sum_b s_tb sum_{i in b} |q_i| (79 * 2 gamma(40))   the block sums, whose codes enter as code + 24 or + 72
+  delta_t = scale sum_b s_tb sum_{i in b} |q_i| (8 * 2 gamma(40))    the block sums of |code| <= 8
           + (2^-21 + gamma(NB + 8)) scale sum_i |q_i K_ti|           q as two fp16 parts (2^-22 each way), FP32 over blocks
           + 6 u scale sum_i (|a_i| + |b_i|) |K_ti|                   RoPE and the score factor
           + 2^-33 scale max|q| sum_i |K_ti|                          fp16 spacing below the head's normalised range
   eps_t   = 2^-20 + 4 u (|s_t| + max |s| + 32)                       ex2.approx, its FP32 argument, p s_V as two fp16 parts
-            + 2^-40 / p_t-free: p s_V below fp16's normal range, at most 2^-25 of the 2^14 and more its largest value holds:
-            an absolute 2^-39 max_t(s_V) |code| <= 2^-36 max s_V, added to the bound
+          + npos 2^-35 max_t(s_V) in all                              p s_V below fp16's normal range: its two parts each err by
+            half the subnormal spacing, 2^-25, where the largest s_V counts 2^14 or more, so a row's term by at most
+            2 2^-25 / 2^14 max(s_V) |code| <= 2^-38 8 max(s_V); all npos rows may be such rows
   rel_sum = 2 gamma(36 (npos / 256 + 2) + 64)                        the per-warp tile sums and the joins."""
 import ctypes
 
@@ -99,13 +100,13 @@ def attend(q, K, V, Ks_blocks, yq):
         p /= p.sum()
         o[j] = p @ V
         aq = np.abs(q[j])
-        delta = scale * (np.abs(Ks_blocks) @ aq.reshape(NB, 32).sum(-1)) * 79 * 2 * gamma(40)
+        delta = scale * (np.abs(Ks_blocks) @ aq.reshape(NB, 32).sum(-1)) * 8 * 2 * gamma(40)
         delta += (2.0 ** -21 + gamma(NB + 8)) * scale * (aK @ aq) + 6 * U32 * scale * (aK @ rope_pair_abs(yq[j]))
         delta += 2.0 ** -33 * scale * aq.max() * aK.sum(-1)
         eps = 2.0 ** -20 + 4 * U32 * (np.abs(s) + np.abs(s).max() + 32)
         rel = 2 * gamma(36 * (npos // 256 + 2) + 64)
         tol[j] = ((delta + eps) * p) @ np.abs(V - o[j]) + rel * (p @ np.abs(V)) + 16 * U32 * np.abs(o[j])
-        tol[j] += 2.0 ** -36 * vs + 1e-30
+        tol[j] += npos * 2.0 ** -35 * vs + 1e-30
     return o, tol
 
 
