@@ -32,6 +32,11 @@
 //   R = max_i r_i,  o = sum_i 2^(r_i - R) o_i / sum_i 2^(r_i - R) l_i
 // without any CTA waiting: the last of each 24 sharers to arrive joins the 24,
 // and the last of those joins the rest.
+//
+// Measured (4 kv heads x 128, 16 query heads): 8 sequences of 120k-131k rows in
+// 112 us, 5190 GB/s, where widening (5 ALU operations for 8 codes, two issue
+// cycles each) and 32 MMAs a tile (eight each) fill four fifths of the issue
+// time; one of 4096 rows in 9.2 us, a chain of latencies.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -250,7 +255,8 @@ __device__ __forceinline__ void plan_work(const Params& p, Small& sm) {
   } else {
     if (items <= grid) {
       const int lo = max(W, (int)((unsigned)(total + grid - 1) / (unsigned)grid));
-      const int hi = max(lo, items < grid ? (int)((unsigned)(total + grid - items - 1) / (unsigned)(grid - items)) : total);
+      const int spare = grid - items;
+      const int hi = max(lo, spare ? (int)((unsigned)(total + spare - 1) / (unsigned)spare) : total);
       const unsigned mine = lane < 31 ? lo + (unsigned)(hi - lo) / 31u * lane : hi;
       unsigned ranges = 0;
 #pragma unroll 1
@@ -466,7 +472,8 @@ template <int HD, int G>
 __device__ __noinline__ void join_parts(const Params& p, Small& sm, uint8_t* smem, int first, int step, int n,
                                         bool final) {
   using Sh = Shape<HD>;
-  constexpr int NV = G * HD / 4, VT = (NV + Sh::kThreads - 1) / Sh::kThreads, NX = VT == 1 ? 8 : 12;  // vectors of a thread
+  constexpr int NV = G * HD / 4, VT = (NV + Sh::kThreads - 1) / Sh::kThreads;  // vectors; of a thread
+  constexpr int NX = VT == 1 ? 8 : 12;                                          // partials on their way at once
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c_lo = sm.c_lo, slot0 = sm.slot0;
   auto part_of = [&](int i) { return p.part + (2ll * (c_lo + i) + (i == 0 ? slot0 : 0)) * part_size(G, HD); };
@@ -913,7 +920,8 @@ __global__ void __launch_bounds__(Shape<HD>::kThreads, Shape<HD>::kCtas) k_attn(
           for (int t = 0; t < 2; ++t) {
             const float* a = acc[c][t];
             *reinterpret_cast<float2*>(ow + j * OP + c * 32 + t * 16 + row8 * 2) =
-                G == 8 ? make_float2(a[h] * unit, a[2 + h] * unit) : make_float2((a[0] + a[1]) * unit, (a[2] + a[3]) * unit);
+                G == 8 ? make_float2(a[h] * unit, a[2 + h] * unit)
+                       : make_float2((a[0] + a[1]) * unit, (a[2] + a[3]) * unit);
           }
       }
     }
