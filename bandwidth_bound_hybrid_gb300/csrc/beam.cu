@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_select(const SelectParams p
       const uint64_t w = lane < nb ? buf[lane] : 0, rest = buf[32 + lane];
       __syncwarp();
       buf[lane] = rest;
+      __syncwarp();
       nb = nb > 32 ? nb - 32 : 0;
       top = warp_join(top, __shfl_sync(0xffffffffu, (unsigned long long)warp_sort(w, lane), 31 - lane), lane);
     };

@@ -1735,6 +1735,7 @@ int move_states(hy_cache* c, const std::vector<int>& seqs, const int32_t* parent
   const hy_model* m = c->m;
   const hy_config& cf = m->cfg;
   const int n = (int)seqs.size(), hd = cf.head_dim, nkv = cf.attn_kv_heads;
+  if (2ll * m->n_attn * nkv > 65535) return fail(HY_ERR_UNSUPPORTED, "state move: above 65535 K and V heads");
   beam::ReorderParams p;
   auto run = [&](int segs) -> int {
     p.beams = n;
@@ -2509,9 +2510,14 @@ int hy_op_beam_reorder(void* state_dev, int64_t beam_stride, int32_t n_seg, int6
   if (!aligned16(state_dev) || !aligned(parent_dev) || groups <= 0 || beams <= 0 || n_seg <= 0 || seg_bytes < 0 ||
       beam_stride % 16 || seg_stride % 16 || seg_bytes % 16)
     return fail(HY_ERR_ARG, "bad beam reordering arguments (state, strides and segments in 16-byte pieces)");
-  if ((n_seg > 1 && seg_stride < seg_bytes) ||
-      ((long long)groups * beams > 1 &&
-       (beam_stride < seg_bytes || (n_seg > 1 && (beam_stride - seg_bytes) / (n_seg - 1) < seg_stride))))
+  // `count` pieces `pitch` apart, the last `last` bytes long, within `room`
+  auto fits = [](long long count, long long pitch, long long last, long long room) {
+    return room >= last && (count == 1 || (room - last) / (count - 1) >= pitch);
+  };
+  const long long states = (long long)groups * beams;
+  const bool apart = (n_seg == 1 || seg_stride >= seg_bytes) && (states == 1 || beam_stride >= seg_bytes);
+  if (!apart || (states > 1 && n_seg > 1 && !fits(n_seg, seg_stride, seg_bytes, beam_stride) &&
+                 !fits(states, beam_stride, seg_bytes, seg_stride)))
     return fail(HY_ERR_ARG, "beam reordering: segments or states overlap");
   if (beams > beam::kMaxBeams || groups > 65535 || n_seg > 65535)
     return fail(HY_ERR_UNSUPPORTED, "beam reordering: at most %d beams, 65535 groups and 65535 segments",

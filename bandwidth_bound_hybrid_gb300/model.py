@@ -199,6 +199,9 @@ class HybridModel:
         `first`, the prompt's length, on).  `beams`: a BeamState, updated in
         place."""
         n, V = len(seqs), self.shape.vocab
+        if tuple(beams.logits.shape) != (n, V):
+            raise ValueError(f"beam state of {beams.logits.shape[0]} beams x {beams.logits.shape[1]} tokens for {n} "
+                             f"sequences x {V} tokens")
         self.decode_batch(seqs, beams.tokens, beams.ids, beams.logits, stream)
         check(capi.lib().hy_op_beam_select(_ptr(beams.logits), V, 1, n, V, n, _ptr(beams.scores),
                                            _ptr(beams.done) if eos >= 0 else None, int(eos), _ptr(beams.scores),

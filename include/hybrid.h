@@ -419,8 +419,10 @@ int hy_op_beam_select(const float* logits_dev, int32_t ldl, int32_t groups, int3
  * (repeats allowed; states that keep themselves are not touched).  State j
  * starts at state_dev + j * beam_stride and consists of n_seg segments of
  * seg_bytes bytes, seg_stride bytes apart; bytes between the segments stay.
- * state_dev 16-byte aligned, strides and sizes (bytes) multiples of 16, and
- * neither segments nor states may overlap.  A parent outside [0, beams)
+ * state_dev 16-byte aligned, strides and sizes (bytes) multiples of 16.  The
+ * states lie one after the other (beam_stride holds all segments of a state),
+ * or segment after segment (seg_stride holds that segment of all states, as in
+ * a cache laid out [layer][beam][...]); nothing may overlap.  A parent outside [0, beams)
  * leaves its state as it is (HY_GUARD_BAD_INDEX). */
 int hy_op_beam_reorder(void* state_dev, int64_t beam_stride, int32_t n_seg, int64_t seg_stride, int64_t seg_bytes,
                        int32_t groups, int32_t beams, const int32_t* parent_dev, void* stream);

@@ -252,3 +252,22 @@ def test_reorder_refuses_bad_parents(L):
     assert L.hy_op_check_device(None, None) == capi.HY_ERR_DEVICE_GUARD
     np.testing.assert_array_equal(to_np(d), a[[1, 1, 2, 0]])
     assert L.hy_op_check_device(None, None) == 0
+
+
+@pytest.mark.parametrize("groups,beams,n_seg,seg,gap", [(1, 4, 3, 1040, 0), (3, 5, 7, 48, 32), (2, 16, 2, 65536, 16), (1, 2, 70, 16, 0)])
+def test_reorder_interleaved(L, groups, beams, n_seg, seg, gap):
+    """Layout [n_seg][groups * beams][seg (+ gap)], as [layer][beam][...] caches have it."""
+    torch = _torch()
+    rng = np.random.default_rng(beams * 10 + n_seg)
+    a = rng.integers(0, 256, (n_seg, groups, beams, seg + gap)).astype(np.uint8)
+    parent = rng.integers(0, beams, (groups, beams)).astype(np.int32)
+    want = a.copy()
+    for g in range(groups):
+        want[:, g, :, :seg] = a[:, g, parent[g], :seg]
+    d = torch.from_numpy(a).cuda()
+    p = torch.from_numpy(parent).cuda()
+    stride = seg + gap
+    # the last segment of the last state ends with the tensor, or `gap` before
+    assert L.hy_op_beam_reorder(d.data_ptr(), stride, n_seg, groups * beams * stride, seg, groups, beams, p.data_ptr(),
+                                torch.cuda.current_stream().cuda_stream) == 0, L.hy_last_error()
+    np.testing.assert_array_equal(to_np(d), want)

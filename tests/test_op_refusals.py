@@ -97,3 +97,23 @@ def test_beam_reorder_refusals(L):
         assert reorder(L, **over) == capi.HY_ERR_ARG, over
     for over in (dict(beams=17), dict(groups=65536), dict(n_seg=65536, pitch=512, stride=2 ** 40)):
         assert reorder(L, **over) == capi.HY_ERR_UNSUPPORTED, over
+
+
+def test_beam_reorder_of_interleaved_states(L):
+    """Segment after segment, each of all states: 8 states of 512 bytes need 4096."""
+    for over in (dict(stride=512, pitch=4080), dict(stride=496, pitch=4096), dict(stride=528, pitch=4096),
+                 dict(stride=512, pitch=2 ** 40, seg=528), dict(stride=2 ** 62, pitch=2 ** 62)):
+        assert reorder(L, **over) == capi.HY_ERR_ARG, over
+
+
+def test_beam_step_refuses_a_state_of_another_size(L):
+    from types import SimpleNamespace
+
+    from bandwidth_bound_hybrid_gb300.model import HybridModel
+    m = object.__new__(HybridModel)
+    m.shape = SimpleNamespace(vocab=1000)
+    m.c = m.m = None
+    for shape in ((3, 1000), (4, 999)):
+        beams = SimpleNamespace(logits=SimpleNamespace(shape=shape))
+        with pytest.raises(ValueError, match="beam state"):
+            m.beam_step(range(4), beams)
