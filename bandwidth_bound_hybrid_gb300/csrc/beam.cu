@@ -28,7 +28,9 @@
 // the states is kept, and a source is read once from memory whatever the
 // number of its children.  Bound by the bytes of the states that change (2 x 8
 // states of 25 MB, half of them moved: 52 us, 6.06 TB/s).
+#include <algorithm>
 #include <cfloat>
+#include <cmath>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -486,15 +488,22 @@ __global__ void __launch_bounds__(kThreads) k_reorder(const ReorderParams p) {
 
 int chunks(int vocab) { return (int)(((long long)vocab + kChunk - 1) / kChunk); }
 
-// Tiles of kChunk logits a CTA takes: the split of a row whose waves of CTAs
-// (kCtas an SM) take least, a CTA costing about three tiles besides its own.
+// The split of a row.  A CTA of t tiles (of kChunk logits) costs about what t +
+// 3.3 tiles take; a tile takes longer the more CTAs an SM holds, more steeply
+// from two on, where the memory is busy (measured, in us: 0.65, 0.83, 1.12 and
+// 1.41 for 1 to 4; rows of 38 tiles: 456 rows whole in 54 us, in four parts in
+// 63; 304 rows whole in 42.5, halved in 40.2; 8 rows in 19 parts in 14.6, in 38
+// in 17.2).  So: full waves of kCtas an SM and what the last one holds.
 void set_span(SelectParams* p, int groups, int nsm) {
   const long long rows = (long long)groups * p->beams, n = chunks(p->vocab), slots = (long long)nsm * kCtas;
-  long long best = -1;
+  auto tile = [](double k) { return std::max(0.47 + 0.18 * k, 0.25 + 0.29 * k); };
+  double best = 0;
   for (long long c = 1; c <= n && c <= 4096; ++c) {
     const long long t = (n + c - 1) / c, parts = (n + t - 1) / t;
-    const long long cost = (rows * parts + slots - 1) / slots * (t + 3);
-    if (best < 0 || cost < best) {
+    const long long waves = (rows * parts - 1) / slots;  // before the last
+    const double k = (double)(rows * parts - waves * slots) / nsm;
+    const double cost = ((double)t + 3.3) * ((double)waves * tile(kCtas) + (tile(k) + tile(std::ceil(k))) / 2);
+    if (c == 1 || cost < best) {
       best = cost;
       p->chunks = (int)parts;
       p->span = t * kChunk;
