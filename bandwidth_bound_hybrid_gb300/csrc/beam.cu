@@ -20,7 +20,7 @@
 // rest in FP64, as the scores are: candidates of different beams differ in
 // their last bits) and selects among the chunks' lists by the same kind of
 // bound, from the lists' heads.  Measured: 64 groups of 8 beams x 151936, 16
-// picks, in 59.7 us (4.8 TB/s), one group of 4 in 11.5 us.
+// picks, in 58.0 us (4.95 TB/s), one group of 4 in 10.0 us.
 //
 // Reordering.  State i of a group becomes what state parent[i] was, in place:
 // a thread owns one 16-byte column of all the group's states, reads the
@@ -87,21 +87,29 @@ __device__ __forceinline__ uint32_t warp_sort32(uint32_t v, int lane) {
   }
   return v;
 }
-// The n-th largest (n in 1..32) of all the CTA's keys: the warps' sorted lists merged (every warp by itself).
+// The n-th largest (n in 1..32) of all the CTA's keys: the warps' sorted lists merged, by every warp for itself (as a
+// tree, a chain of 15 exchanges: 0.4 us less than one list after the other).
 __device__ __forceinline__ uint32_t cta_nth(uint32_t (*sorted)[32], uint32_t v, int n, int lane, int warp) {
   sorted[warp][lane] = warp_sort32(v, lane);
   __syncthreads();
-  uint32_t best = sorted[0][lane];
+  // best 32 of lists 2 i and 2 i + 1, of those of two such, ...: the second of a pair the other way round
+  uint32_t best[kWarps / 2];
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) {
-    best = max(best, sorted[w][31 - lane]);
+  for (int i = 0; i < kWarps / 2; ++i) best[i] = max(sorted[2 * i][lane], sorted[2 * i + 1][31 - lane]);
+#pragma unroll
+  for (int w = kWarps / 2; w > 0; w >>= 1) {
 #pragma unroll
     for (int j = 16; j > 0; j >>= 1) {
-      const uint32_t o = __shfl_xor_sync(0xffffffffu, best, j);
-      best = (lane & j) == 0 ? max(best, o) : min(best, o);
+#pragma unroll
+      for (int i = 0; i < w; ++i) {
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, best[i], j);
+        best[i] = ((lane & j) == 0) == ((i & 1) == 0) ? max(best[i], o) : min(best[i], o);
+      }
     }
+#pragma unroll
+    for (int i = 0; i < w / 2; ++i) best[i] = max(best[2 * i], best[2 * i + 1]);
   }
-  return __shfl_sync(0xffffffffu, best, n - 1);
+  return __shfl_sync(0xffffffffu, best[0], n - 1);
 }
 
 // Sorted across the warp, largest in lane 0: a step of a bitonic network, the
@@ -304,17 +312,23 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_select(const SelectParams p
       float M = t0.x;
       for (int c = lane + 32; c < nch; c += 32) M = fmaxf(M, __ldcg(st + c).x);
       M = warp_max(M);
-      double S = lane < nch ? (double)(t0.y * carry(t0.x, M)) : 0.0;
+      // the sum as S + err, err the exact rest of every addition (FP64 ones are slow here)
+      float S = lane < nch ? __fmul_rn(t0.y, carry(t0.x, M)) : 0.f, err = 0.f;
+      auto add = [&](float b, float b_err) {
+        const float sum = S + b, of_b = sum - S;
+        err += b_err + ((S - (sum - of_b)) + (b - of_b));
+        S = sum;
+      };
       for (int c = lane + 32; c < nch; c += 32) {
         const float2 t = __ldcg(st + c);
-        S += (double)(t.y * carry(t.x, M));
+        add(__fmul_rn(t.y, carry(t.x, M)), 0.f);
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+      for (int o = 16; o > 0; o >>= 1)
+        if (o < nch) add(__shfl_xor_sync(0xffffffffu, S, o), __shfl_xor_sync(0xffffffffu, err, o));
       // log of S = 2^e f, f in [0.75, 1.5): the FP32 logarithm of f errs by 2^-25 at most, e log 2 is FP64
-      const float Sf = (float)S;
-      const int e = (int)((__float_as_uint(Sf) + 0x00400000u) >> 23) - 127;
-      const float f = __uint_as_float(__float_as_uint(Sf) - ((uint32_t)e << 23));
+      const int e = (int)((__float_as_uint(S) + 0x00400000u) >> 23) - 127;
+      const float f = __uint_as_float(__float_as_uint(S) - ((uint32_t)e << 23));
       const double log2 = 0.69314718055994530942;
       double top = (double)M;
       if (!large(M)) {
@@ -322,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_select(const SelectParams p
         // the mean of x (here: the largest)
         top = (double)__fmul_rn(M, kLog2e) * log2 + (1.0 - (double)kLog2e * log2) * (double)M;
       }
-      off -= top + (double)e * log2 + (double)(logf(f) + (float)(S - (double)Sf) / Sf);
+      off -= top + (double)e * log2 + (double)(logf(f) + err / S);
     }
     if (lane == 0) {
       sm.off[w] = off - off == 0.0 ? off : -INFINITY;
@@ -377,7 +391,20 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_select(const SelectParams p
   __syncthreads();
   const int nq = sm.nq;
   int n = sm.n;
-  if (nq <= kQual && n <= kBest) {
+  if (nq <= kQual && n <= kThreads / 4) {  // a quad counts the better ones of a candidate
+    const int a = tid / 4;
+    Cand c = {0, 0xffffffffu};
+    int rank = 0;
+    if (a < n) {
+      c = {sm.best.key[a], sm.best.i[a]};
+#pragma unroll 4
+      for (int b = tid % 4; b < n; b += 4) rank += better({sm.best.key[b], sm.best.i[b]}, c);
+    }
+    rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+    rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+    if (a < n && tid % 4 == 0 && rank < P) sm.sel[rank] = c;
+    if (n > P) n = P;
+  } else if (nq <= kQual && n <= kBest) {
     for (int a = tid; a < n; a += kThreads) {
       const Cand c = {sm.best.key[a], sm.best.i[a]};
       int rank = 0;
