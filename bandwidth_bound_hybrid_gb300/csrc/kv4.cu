@@ -259,8 +259,16 @@ __device__ __forceinline__ void plan_work(const Params& p, Small& sm) {
       const int hi = max(lo, spare ? (int)((unsigned)(total + spare - 1) / (unsigned)spare) : total);
       const unsigned mine = lane < 31 ? lo + (unsigned)(hi - lo) / 31u * lane : hi;
       unsigned ranges = 0;
-#pragma unroll 1
-      for (int b = 0; b < p.nb; ++b) ranges += ((unsigned)__shfl_sync(0xffffffffu, n, b) + mine - 1) / mine;
+      // ceil(x / mine) by FP32: off by less than 1 below 2^21, the larger quotients fit nowhere all the same
+      const float inv = 1.0f / (float)mine;
+#pragma unroll
+      for (int b = 0; b < kMaxB; ++b) {  // (n is 0 past the last sequence)
+        const unsigned x = __shfl_sync(0xffffffffu, n, b);
+        unsigned r = (unsigned)((float)x * inv);
+        r += r * mine < x;
+        r += r * mine < x;
+        ranges += r;
+      }
       const unsigned fits = __ballot_sync(0xffffffffu, p.nkv * (int)ranges <= grid);
       m = fits ? (int)__shfl_sync(0xffffffffu, mine, __ffs(fits) - 1) : 0;
       // a second range costs a CTA about what three tiles of every warp do
