@@ -23,11 +23,10 @@
 // picks, in 58.0 us (4.95 TB/s), one group of 4 in 10.0 us.
 //
 // Reordering.  State i of a group becomes what state parent[i] was, in place:
-// a thread owns one 16-byte column of all the group's states, reads the
-// sources of those that change, and only then writes.  So no second copy of
-// the states is kept, and a source is read once from memory whatever the
-// number of its children.  Bound by the bytes of the states that change (2 x 8
-// states of 25 MB, half of them moved: 52 us, 6.06 TB/s).
+// a thread owns 16-byte columns of all the group's states, reads the sources
+// of those that change, and only then writes.  So no second copy of the states
+// is kept.  Bound by the bytes of the states that change: 2 x 8 states of 25
+// MB, 4 of them moved, in 34.7 us (5.8 TB/s), 7 in 51.4 (6.4), 11 in 73.8 (6.5).
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -46,6 +45,7 @@ constexpr int kPer = 16;                 // logits of a lane at a time
 constexpr int kStep = kPer * 32;         // and of a warp
 constexpr int kFew = 4;                  // words of a thread in the final selection of few lists
 constexpr int kQual = 1024;              // lists looked into by the fast final selection
+constexpr int kMoves = 64;               // CTAs of the reordering per SM, at most
 constexpr int kBest = 2048;              // and their candidates
 
 // Sums of exponentials are held as S = sum 2^(x log2 e - c(M)) with the largest x
@@ -471,43 +471,75 @@ __global__ void __launch_bounds__(kThreads, kCtas) k_select(const SelectParams p
 }
 
 // ------------------------------------------------------------ reordering
-// Column x of segment y of group z (or, paged, of segment y % n_seg in page
-// first_page + y / n_seg).
+// The columns [x, end) (bytes, 16 each) of the n <= NM states that change, U
+// columns of a thread at a time, so that about 8 loads are on their way: all
+// are read before anything of these columns is written.
+template <int NM, int U>
+__device__ __forceinline__ void move(uint8_t* const* src, uint8_t* const* dst, int n, long long x, long long end) {
+  for (x += threadIdx.x * 16; x < end; x += (long long)U * kThreads * 16) {
+    uint4 v[U][NM];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < NM; ++i)
+        if (i < n && x + u * kThreads * 16 < end)
+          v[u][i] = *reinterpret_cast<const uint4*>(src[i] + x + u * kThreads * 16);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < NM; ++i)
+        if (i < n && x + u * kThreads * 16 < end) *reinterpret_cast<uint4*>(dst[i] + x + u * kThreads * 16) = v[u][i];
+  }
+}
+
+// A share of the columns of segment y of group z (or, paged, of segment y %
+// n_seg in page first_page + y / n_seg).  B: at least as many beams.
 template <int B>
 __global__ void __launch_bounds__(kThreads) k_reorder(const ReorderParams p) {
-  __shared__ int s_parent[B];
+  __shared__ uint8_t *s_src[B], *s_dst[B];
+  __shared__ int s_n;
   const int tid = threadIdx.x, z = blockIdx.z;
-  if (tid < p.beams) {
-    int q = p.parent ? p.parent[(long long)z * p.beams + tid] : 0;
-    if (q < 0 || q >= p.beams) {  // left as it is
-      if (blockIdx.x == 0 && blockIdx.y == 0) set_guard(p.guard, kGuardBadIndex);
-      q = tid;
-    }
-    s_parent[tid] = q;
-  }
-  __syncthreads();
-  long long lo = 0, bytes = p.seg_bytes;
+  long long lo = 0, end = p.seg_bytes;
   int seg = blockIdx.y, page = 0;
   if (p.page_bytes) {  // rows [first_row, end_row) of the sequence that lie in this page
     page = p.first_page + seg / p.n_seg;
     seg %= p.n_seg;
     const int r0 = max(p.first_row - page * p.page_rows, 0), r1 = min(p.end_row - page * p.page_rows, p.page_rows);
     lo = (long long)r0 * p.row_bytes;
-    bytes = (long long)r1 * p.row_bytes;
+    end = (long long)r1 * p.row_bytes;
   }
-  const long long hop = (long long)gridDim.x * kThreads * 16;
-  for (long long x = lo + ((long long)blockIdx.x * kThreads + tid) * 16; x < bytes; x += hop) {
-    auto at = [&](int i) {
-      uint8_t* b = p.base[i] + z * p.group_stride + seg * p.seg_stride[i] + x;
-      return reinterpret_cast<uint4*>(p.page_bytes ? b + p.pages[i][page] * p.page_bytes : b);
-    };
-    uint4 v[B];
-#pragma unroll
-    for (int i = 0; i < B; ++i)
-      if (i < p.beams && s_parent[i] != i) v[i] = *at(s_parent[i]);
-#pragma unroll
-    for (int i = 0; i < B; ++i)
-      if (i < p.beams && s_parent[i] != i) *at(i) = v[i];
+  if (tid < 32) {  // the states that change
+    int q = tid;
+    if (tid < p.beams) {
+      q = p.parent ? p.parent[(long long)z * p.beams + tid] : 0;
+      if (q < 0 || q >= p.beams) {  // left as it is
+        if (blockIdx.x == 0 && blockIdx.y == 0) set_guard(p.guard, kGuardBadIndex);
+        q = tid;
+      }
+    }
+    const unsigned moved = __ballot_sync(0xffffffffu, q != tid);
+    if (q != tid) {
+      auto at = [&](int i) {
+        uint8_t* b = p.base[i] + z * p.group_stride + seg * p.seg_stride[i];
+        return p.page_bytes ? b + p.pages[i][page] * p.page_bytes : b;
+      };
+      const int to = __popc(moved & ((1u << tid) - 1));
+      s_src[to] = at(q);
+      s_dst[to] = at(tid);
+    }
+    if (tid == 0) s_n = __popc(moved);
+  }
+  __syncthreads();
+  const int n = s_n;
+  const long long x = lo + blockIdx.x * p.share, x_end = min(x + p.share, end);
+  if (n <= 2) {
+    if (n) move<2, 4>(s_src, s_dst, n, x, x_end);
+  } else if (B == 4 || n <= 4) {
+    move<4, 2>(s_src, s_dst, n, x, x_end);
+  } else if (B == 8 || n <= 8) {
+    move<8, 1>(s_src, s_dst, n, x, x_end);
+  } else {
+    move<16, 1>(s_src, s_dst, n, x, x_end);
   }
 }
 
@@ -547,19 +579,27 @@ cudaError_t select(const SelectParams& p, int groups, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-cudaError_t reorder(const ReorderParams& p, int groups, int segs, cudaStream_t st) {
+// A CTA takes one or two rows of kThreads columns, or a multiple of four (whole
+// turns of every move<>) where that is more than kMoves CTAs an SM: one row
+// each takes 41.5 us for the 4 moved states above, 12 CTAs an SM 81.5 for the 11.
+cudaError_t reorder(const ReorderParams& p, int groups, int segs, int nsm, cudaStream_t st) {
   const long long most = p.page_bytes ? (long long)p.page_rows * p.row_bytes : p.seg_bytes;
   if (groups <= 0 || segs <= 0 || most <= 0) return cudaSuccess;
   if (groups > 65535 || segs > 65535 || p.beams < 1 || p.beams > kMaxBeams) return cudaErrorInvalidValue;
-  long long x = (most / 16 + kThreads - 1) / kThreads;
-  if (x > 4096) x = 4096;
+  const long long all = (most / 16 + kThreads - 1) / kThreads;  // rows of columns
+  const long long fair = std::max((long long)nsm * kMoves / ((long long)groups * segs), 1ll);
+  long long per = (all + fair - 1) / fair;
+  if (per > 2) per = (per + 3) / 4 * 4;
+  ReorderParams q = p;
+  q.share = per * kThreads * 16;
+  const long long x = (all + per - 1) / per;
   const dim3 grid((unsigned)x, (unsigned)segs, (unsigned)groups);
   if (p.beams <= 4)
-    k_reorder<4><<<grid, kThreads, 0, st>>>(p);
+    k_reorder<4><<<grid, kThreads, 0, st>>>(q);
   else if (p.beams <= 8)
-    k_reorder<8><<<grid, kThreads, 0, st>>>(p);
+    k_reorder<8><<<grid, kThreads, 0, st>>>(q);
   else
-    k_reorder<16><<<grid, kThreads, 0, st>>>(p);
+    k_reorder<16><<<grid, kThreads, 0, st>>>(q);
   return cudaGetLastError();
 }
 

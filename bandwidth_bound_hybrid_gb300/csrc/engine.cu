@@ -1741,7 +1741,7 @@ int move_states(hy_cache* c, const std::vector<int>& seqs, const int32_t* parent
     p.beams = n;
     p.parent = parent;
     p.guard = c->guard;
-    cudaError_t e = beam::reorder(p, 1, segs, st);
+    cudaError_t e = beam::reorder(p, 1, segs, m->nsm, st);
     if (e != cudaSuccess) return fail(HY_ERR_CUDA, "state move launch: %s", cudaGetErrorString(e));
     return HY_OK;
   };
@@ -2537,7 +2537,7 @@ int hy_op_beam_reorder(void* state_dev, int64_t beam_stride, int32_t n_seg, int6
   p.n_seg = n_seg;
   p.parent = parent_dev;
   p.guard = guard;
-  cudaError_t e = beam::reorder(p, groups, n_seg, (cudaStream_t)stream);
+  cudaError_t e = beam::reorder(p, groups, n_seg, op_nsm(), (cudaStream_t)stream);
   if (e != cudaSuccess) return fail(HY_ERR_CUDA, "beam reordering launch: %s", cudaGetErrorString(e));
   return HY_OK;
 }

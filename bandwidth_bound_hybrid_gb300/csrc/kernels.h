@@ -284,8 +284,9 @@ struct ReorderParams {
   const int* pages[kMaxBeams];
   long long page_bytes;
   int page_rows, row_bytes, first_row, end_row, first_page;
+  long long share;               // bytes of a segment that a CTA moves (set by the launch)
 };
-cudaError_t reorder(const ReorderParams& p, int groups, int segs, cudaStream_t st);
+cudaError_t reorder(const ReorderParams& p, int groups, int segs, int nsm, cudaStream_t st);
 }  // namespace beam
 
 // ---------------------------------------------------------------- batched GEMV
