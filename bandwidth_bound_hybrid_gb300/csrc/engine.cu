@@ -63,8 +63,18 @@ int ensure_init(int dev) {
   HY_CK(bgemv::init());
   HY_CK(gemm::init());
   HY_CK(prefill::init());
-  HY_CK(kv4::init());
   g_inited[dev] = true;
+  return HY_OK;
+}
+
+// The 4-bit cache's kernels, apart: a program without one does not load them.
+int ensure_kv4(int dev) {
+  static std::map<int, bool> done;
+  std::lock_guard<std::mutex> lk(g_init_mu);
+  if (done[dev]) return HY_OK;
+  HY_CK(kv4::init());
+  HY_CK(prefill::init_kv4());
+  done[dev] = true;
   return HY_OK;
 }
 
@@ -1440,7 +1450,8 @@ int hy_model_create(const hy_config* cfg, const hy_weights* w, hy_model** out) {
     delete m;
     return rc;
   }
-  if ((rc = current_device(&m->device, &m->nsm)) != HY_OK || (rc = ensure_init(m->device)) != HY_OK) {
+  if ((rc = current_device(&m->device, &m->nsm)) != HY_OK || (rc = ensure_init(m->device)) != HY_OK ||
+      (m->cfg.kv_format == 2 && (rc = ensure_kv4(m->device)) != HY_OK)) {
     delete m;
     return rc;
   }
@@ -2390,7 +2401,9 @@ int hy_op_attention_q4(const float* y_dev, int32_t ldy, int32_t batch, void* Kq_
     return fail(HY_ERR_ARG, "bad 4-bit attention arguments (batch 1..%d, ldy >= (nq + 2 nkv) hd, ldo >= nq hd)",
                 kv4::kMaxB);
   unsigned* guard = nullptr;
-  if ((rc = op_guard(&guard)) != HY_OK) return rc;
+  int dev = 0, nsm = 0;
+  if ((rc = op_guard(&guard)) != HY_OK || (rc = current_device(&dev, &nsm)) != HY_OK || (rc = ensure_kv4(dev)) != HY_OK)
+    return rc;
   kv4::Params a;
   memset(&a, 0, sizeof(a));
   a.y = y_dev;
@@ -2415,7 +2428,7 @@ int hy_op_attention_q4(const float* y_dev, int32_t ldy, int32_t batch, void* Kq_
     a.len[b] = len_dev + b;
     a.cap[b] = cap;
   }
-  cudaError_t e = kv4::launch(a, hd, op_nsm(), (cudaStream_t)stream, false);
+  cudaError_t e = kv4::launch(a, hd, nsm, (cudaStream_t)stream, false);
   if (e != cudaSuccess) return fail(HY_ERR_CUDA, "4-bit attention launch: %s", cudaGetErrorString(e));
   return HY_OK;
 }

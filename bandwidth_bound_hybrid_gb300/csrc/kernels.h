@@ -474,6 +474,7 @@ struct AttnArgs {
   float scale;
 };
 cudaError_t init();
+cudaError_t init_kv4();           // for the 4-bit cache
 cudaError_t embed_rows(const uint16_t* embed, const int* tok, int n, int H, int vocab, float* X, unsigned* guard,
                        cudaStream_t st);
 cudaError_t gdn(const GdnArgs& a, cudaStream_t st);

@@ -505,28 +505,31 @@ cudaError_t launch_causal(const AttnArgs& a, cudaStream_t st) {
   return launch_k(k_attn_causal<HD, false>, grid, dim3(kCausalThreads), CausalSmem<HD, false>::total, st, false, a);
 }
 
-template <int HD>
+template <int HD, bool KV4>
 cudaError_t init_causal() {
-  cudaError_t e = cudaFuncSetAttribute(k_attn_causal<HD, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)CausalSmem<HD, false>::total);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k_attn_causal<HD, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)CausalSmem<HD, true>::total);
-  return e;
+  return cudaFuncSetAttribute(k_attn_causal<HD, KV4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)CausalSmem<HD, KV4>::total);
 }
 
 }  // namespace
 
 cudaError_t init() {
-  cudaError_t e = init_causal<64>();
-  if (e == cudaSuccess) e = init_causal<128>();
-  if (e == cudaSuccess) e = init_causal<256>();
+  cudaError_t e = init_causal<64, false>();
+  if (e == cudaSuccess) e = init_causal<128, false>();
+  if (e == cudaSuccess) e = init_causal<256, false>();
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(k_gdn_scan<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)scan_smem(64));
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(k_gdn_scan<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)scan_smem(128));
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(k_gdn_scan<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)scan_smem(256));
+  return e;
+}
+
+cudaError_t init_kv4() {
+  cudaError_t e = init_causal<64, true>();
+  if (e == cudaSuccess) e = init_causal<128, true>();
+  if (e == cudaSuccess) e = init_causal<256, true>();
   return e;
 }
 
