@@ -946,14 +946,15 @@ __global__ void __launch_bounds__(Shape<HD>::kThreads, Shape<HD>::kCtas) k_attn(
 
 // ------------------------------------------------------------ append
 // Rows of n tokens at positions T .. T + n - 1 of one sequence; blockIdx.y is
-// the kv head of k, then of v.  A lane holds 4 adjacent values (hd 256: two such
-// groups, which are the halves of its rotate-half pairs; else the other half
-// is hd / 8 lanes away), 8 lanes a block, a warp the vectors of two tokens (hd
-// 64) or one; the loads of kUnits of them are on their way together.  Bound by
-// its bytes: one pass, 16-byte accesses.  VEC: y, the table and kv_new are
-// 16-byte aligned with rows of whole 16 bytes (8192 rows of 8 heads x 256: 49.5
-// us so, 60.2 us in 4-byte loads and stores, against 44.2 us for the bytes).
-constexpr int kUnits = 2;
+// the kv head of k, then of v.  A lane holds the 4 + 4 adjacent values that are
+// rotate-half pairs of each other, 8 lanes a block, a warp the vectors of 256 /
+// hd tokens; the loads of units(hd) of them are on their way together (8192
+// rows of 8 heads x 256: 49.5 us with two, 52.8 with one; x 64: 17.9 and 15.9;
+// 2048 rows of 4 x 128: 5.4 and 4.65).  Bound by its bytes: one pass, 16-byte
+// accesses.  VEC: y, the table and kv_new are 16-byte aligned with rows of
+// whole 16 bytes (8192 rows of 8 heads x 256: 49.5 us so, 60.2 us in 4-byte
+// loads and stores, against 44.2 us for the bytes).
+__host__ __device__ constexpr int units(int hd) { return hd == 256 ? 2 : 1; }
 
 template <bool VEC>
 __device__ __forceinline__ float4 load4(const float* p) {
@@ -962,8 +963,8 @@ __device__ __forceinline__ float4 load4(const float* p) {
 
 template <int HD, bool VEC>
 __global__ void __launch_bounds__(256) k_append(const AppendParams p) {
-  constexpr int NB = HD / 32, NH = HD == 256 ? 2 : 1;  // groups of 4 values of a lane
-  constexpr int VW = HD == 64 ? 2 : 1, LV = 32 / VW;     // tokens of a warp, lanes of a vector
+  constexpr int NB = HD / 32, VW = 256 / HD, LV = 32 / VW;  // blocks; tokens of a warp, lanes of a vector
+  constexpr int kUnits = units(HD);
   const int lane = threadIdx.x & 31;
   const int T = p.len ? *p.len : p.t0;
   if (T < 0 || (long long)T + p.n > p.cap) {
@@ -971,21 +972,21 @@ __global__ void __launch_bounds__(256) k_append(const AppendParams p) {
     return;
   }
   const int kg = blockIdx.y, kv = kg >= p.nkv, g = kv ? kg - p.nkv : kg;
-  const int e = (lane % LV) * 4;  // the lane's first element
+  const int e = (lane % LV) * 4;  // the lane's first element, of the first half
   const float* y0 = p.y + (long long)(p.nq + kg) * HD + e;
-  const float* rope0 = reinterpret_cast<const float*>(p.rope + (long long)T * (HD / 2) + e % (HD / 2));
+  const float* rope0 = reinterpret_cast<const float*>(p.rope + (long long)T * (HD / 2) + e);
   const long long row0 = (long long)g * p.cap + T, row0_s = (long long)g * (((long long)p.cap + 3) & ~3ll) + T;
   uint8_t* codes0 = (kv ? p.V : p.K) + row0 * (HD / 2);
   uint16_t* scales0 = (kv ? p.Vs : p.Ks) + row0_s * NB;
   const long long step = (long long)gridDim.x * (blockDim.x >> 5) * VW;
   for (long long i0 = (blockIdx.x * (long long)(blockDim.x >> 5) + (threadIdx.x >> 5)) * VW; i0 < p.n;
        i0 += step * kUnits) {
-    float4 x[kUnits][NH], c0[kUnits], c1[kUnits];
+    float4 x[kUnits][2], c0[kUnits], c1[kUnits];
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {  // (a lane past the last token reads the first one's)
       const long long at = i0 + u * step + lane / LV, i = at < p.n ? at : 0;
 #pragma unroll
-      for (int h = 0; h < NH; ++h) x[u][h] = load4<VEC>(y0 + i * p.ld_y + h * (HD / 2));
+      for (int h = 0; h < 2; ++h) x[u][h] = load4<VEC>(y0 + i * p.ld_y + h * (HD / 2));
       if (!kv) {
         c0[u] = load4<VEC>(rope0 + i * HD);
         c1[u] = load4<VEC>(rope0 + i * HD + 4);
@@ -996,9 +997,9 @@ __global__ void __launch_bounds__(256) k_append(const AppendParams p) {
       if (i0 + u * step >= p.n) break;  // the whole warp
       const long long i = i0 + u * step + lane / LV;
       const bool in = i < p.n;
-      float f[NH][4];
+      float f[2][4];
 #pragma unroll
-      for (int h = 0; h < NH; ++h) {
+      for (int h = 0; h < 2; ++h) {
         f[h][0] = x[u][h].x;
         f[h][1] = x[u][h].y;
         f[h][2] = x[u][h].z;
@@ -1007,20 +1008,10 @@ __global__ void __launch_bounds__(256) k_append(const AppendParams p) {
       if (!kv) {
         const float2 cs[4] = {{c0[u].x, c0[u].y}, {c0[u].z, c0[u].w}, {c1[u].x, c1[u].y}, {c1[u].z, c1[u].w}};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (NH == 2) {
-            rotate(f[0][k], f[NH - 1][k], cs[k], &f[0][k], &f[NH - 1][k]);
-          } else {
-            const float o = __shfl_xor_sync(0xffffffffu, f[0][k], LV / 2);
-            const bool second = e >= HD / 2;
-            float r0, r1;
-            rotate(second ? o : f[0][k], second ? f[0][k] : o, cs[k], &r0, &r1);
-            f[0][k] = second ? r1 : r0;
-          }
-        }
+        for (int k = 0; k < 4; ++k) rotate(f[0][k], f[1][k], cs[k], &f[0][k], &f[1][k]);
       }
 #pragma unroll
-      for (int h = 0; h < NH; ++h) {
+      for (int h = 0; h < 2; ++h) {
         const int el = e + h * (HD / 2), blk = el / 32;
         uint32_t a = 0;
 #pragma unroll
@@ -1112,7 +1103,8 @@ cudaError_t launch(const Params& p, int hd, int nsm, cudaStream_t st, bool pdl) 
 
 cudaError_t append(const AppendParams& p, int hd, cudaStream_t st) {
   if (p.n <= 0) return cudaSuccess;
-  const int per_block = 8 * (hd == 64 ? 2 : 1) * kUnits;  // tokens
+  if (hd != 64 && hd != 128 && hd != 256) return cudaErrorInvalidValue;
+  const int per_block = 8 * (256 / hd) * units(hd);  // tokens
   const dim3 blocks((unsigned)((p.n + (long long)per_block - 1) / per_block), (unsigned)(2 * p.nkv));
   auto ok = [](const void* q) { return ((uintptr_t)q & 15) == 0; };
   const bool vec = ok(p.y) && p.ld_y % 4 == 0 && ok(p.rope) && ok(p.kv_new);
