@@ -2494,6 +2494,9 @@ int hy_op_beam_select(const float* logits_dev, int32_t ldl, int32_t groups, int3
       (long long)groups * lists > 0x7fffffffll || (long long)beams * vocab > 0xffffffffll)
     return fail(HY_ERR_UNSUPPORTED, "beam selection: at most %d beams, %d picks, %d beams x chunks of %d tokens",
                 beam::kMaxBeams, beam::kMaxPicks, beam::kMaxLists, beam::kChunk);
+  int dev = 0, nsm = 0;
+  const int rc = current_device(&dev, &nsm);
+  if (rc != HY_OK) return rc;
   uint8_t* ws = (uint8_t*)workspace_dev;
   beam::SelectParams p;
   memset(&p, 0, sizeof(p));
@@ -2502,7 +2505,7 @@ int hy_op_beam_select(const float* logits_dev, int32_t ldl, int32_t groups, int3
   p.vocab = vocab;
   p.beams = beams;
   p.picks = picks;
-  beam::set_span(&p, groups, op_nsm());
+  beam::set_span(&p, groups, nsm);
   p.score = score_dev;
   p.done = done_dev;
   p.eos = eos;

@@ -1,9 +1,14 @@
 """Argument checks of the 4-bit cache and beam search operators: refused on the
 host, before any device call (CPU only)."""
+import os
+import subprocess
+import sys
+
 import pytest
 
 from bandwidth_bound_hybrid_gb300 import capi
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 A = 4096  # a 16-byte aligned stand-in address: never read, the calls are refused
 
 
@@ -117,3 +122,22 @@ def test_beam_step_refuses_a_state_of_another_size(L):
         beams = SimpleNamespace(logits=SimpleNamespace(shape=shape))
         with pytest.raises(ValueError, match="beam state"):
             m.beam_step(range(4), beams)
+
+
+def without_a_gpu(code):
+    """Run Python code (with L, the library, and A) in a process that sees no GPU."""
+    env = dict(os.environ, CUDA_VISIBLE_DEVICES="", PYTHONPATH=ROOT)
+    pre = f"from bandwidth_bound_hybrid_gb300 import capi\nL = capi.lib()\nA = {A}\n"
+    return subprocess.run([sys.executable, "-c", pre + code], cwd=ROOT, env=env, capture_output=True, text=True)
+
+
+@pytest.mark.parametrize("call", [
+    "L.hy_op_beam_select(A, 1000, 1, 4, 1000, 4, A, None, -1, A, A, A, None, A, None)",
+    "L.hy_op_beam_reorder(A, 64, 1, 64, 64, 1, 4, A, None)",
+    "L.hy_op_attention_q4(A, 768, 1, A, A, A, A, 100, 8, 2, 64, A, A, A, 512, None, A, None)",
+    "L.hy_op_kv_append_q4(A, 768, 5, A, A, A, A, 100, 8, 2, 64, A, A, None, None)"])
+def test_calls_without_a_gpu_return_an_error(L, call):
+    """Good arguments on a machine without a usable GPU: an error code and a message, the process lives."""
+    r = without_a_gpu(f"print({call}, bool(L.hy_last_error()))")
+    assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
+    assert r.stdout.split() == [str(capi.HY_ERR_CUDA), "True"]
