@@ -2386,7 +2386,9 @@ static int check_q4_cache(const void* K, const void* Ks, const void* V, const vo
 size_t hy_op_attention_q4_workspace(int32_t batch, int32_t nq, int32_t nkv, int32_t hd) {
   if (batch < 1 || batch > kv4::kMaxB || nkv <= 0 || nq <= 0 || nq % nkv || hd <= 0) return 0;
   if ((hd != 64 && hd != 128 && hd != 256) || nq / nkv > 8 || ((nq / nkv) & (nq / nkv - 1))) return 0;
-  return (kv4::counters(kv4::kMaxB, nkv) * 4 + 255) / 256 * 256 + kv4::part_floats(nq, nkv, hd, op_nsm()) * 4;
+  const int nsm = op_nsm();  // 0 without a device: a size of the counters alone would be too small for a later call
+  if (nsm <= 0) return 0;
+  return (kv4::counters(kv4::kMaxB, nkv) * 4 + 255) / 256 * 256 + kv4::part_floats(nq, nkv, hd, nsm) * 4;
 }
 
 int hy_op_attention_q4(const float* y_dev, int32_t ldy, int32_t batch, void* Kq_dev, void* Ks_dev, void* Vq_dev,

@@ -487,9 +487,10 @@ int hy_op_attention_i8(const float* y_dev, void* Kq_dev, float* Ks_dev, void* Vq
  * o and kv_new unwritten (HY_GUARD_BAD_POSITION); the others run.
  * rope_table_dev has at least cap rows.  The work is shared over the GPU by
  * cached rows whatever the mix of lengths.  workspace_dev:
- * hy_op_attention_q4_workspace() bytes (the same for every batch), zeroed
- * before its first use and then passed unmodified to later calls of the same
- * nq, nkv and hd; calls that can overlap on the GPU need a workspace each. */
+ * hy_op_attention_q4_workspace() bytes (the same for every batch; 0 for bad
+ * shapes or without a usable GPU), zeroed before its first use and then passed
+ * unmodified to later calls of the same nq, nkv and hd; calls that can overlap
+ * on the GPU need a workspace each. */
 size_t hy_op_attention_q4_workspace(int32_t batch, int32_t nq, int32_t nkv, int32_t hd);
 int hy_op_attention_q4(const float* y_dev, int32_t ldy, int32_t batch, void* Kq_dev, void* Ks_dev, void* Vq_dev,
                        void* Vs_dev, int32_t cap, int32_t nq, int32_t nkv, int32_t hd, const int32_t* len_dev,

@@ -141,3 +141,9 @@ def test_calls_without_a_gpu_return_an_error(L, call):
     r = without_a_gpu(f"print({call}, bool(L.hy_last_error()))")
     assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
     assert r.stdout.split() == [str(capi.HY_ERR_CUDA), "True"]
+
+
+def test_attention_q4_workspace_without_a_gpu(L):
+    """The partials' size needs the GPU's SM count: 0, not the counters' size alone."""
+    r = without_a_gpu("print(L.hy_op_attention_q4_workspace(1, 8, 2, 64))")
+    assert r.returncode == 0 and r.stdout.split() == ["0"], (r.stdout, r.stderr[-2000:])
