@@ -531,7 +531,20 @@ __global__ void __launch_bounds__(kThreads) k_reorder(const ReorderParams p) {
   }
   __syncthreads();
   const int n = s_n;
-  const long long x = lo + blockIdx.x * p.share, x_end = min(x + p.share, end);
+  long long x = lo + blockIdx.x * p.share;
+  const long long x_end = min(x + p.share, end);
+  if (p.skip && blockIdx.x == 0) {  // the first piece: its last words, a thread each
+    if (tid < 4 && tid * 4 >= p.skip) {
+      uint32_t v[B];
+#pragma unroll
+      for (int i = 0; i < B; ++i)
+        if (i < n) v[i] = *reinterpret_cast<const uint32_t*>(s_src[i] + x + tid * 4);
+#pragma unroll
+      for (int i = 0; i < B; ++i)
+        if (i < n) *reinterpret_cast<uint32_t*>(s_dst[i] + x + tid * 4) = v[i];
+    }
+    x += 16;
+  }
   if (n <= 2) {
     if (n) move<2, 4>(s_src, s_dst, n, x, x_end);
   } else if (B == 4 || n <= 4) {

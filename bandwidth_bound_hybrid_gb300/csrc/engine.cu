@@ -1756,7 +1756,7 @@ int move_states(hy_cache* c, const std::vector<int>& seqs, const int32_t* parent
     if (e != cudaSuccess) return fail(HY_ERR_CUDA, "state move launch: %s", cudaGetErrorString(e));
     return HY_OK;
   };
-  auto region = [&](auto base, long long bytes, int segs, auto pitch) -> int {
+  auto region = [&](auto base, long long bytes, int segs, auto pitch, int skip = 0) -> int {
     if (bytes <= 0 || segs <= 0) return HY_OK;
     memset(&p, 0, sizeof(p));
     for (int i = 0; i < n; ++i) {
@@ -1765,6 +1765,7 @@ int move_states(hy_cache* c, const std::vector<int>& seqs, const int32_t* parent
     }
     p.n_seg = segs;
     p.seg_bytes = bytes;
+    p.skip = skip;
     return run(segs);
   };
   auto none = [](int) { return 0ll; };
@@ -1803,15 +1804,18 @@ int move_states(hy_cache* c, const std::vector<int>& seqs, const int32_t* parent
   rc = region([&](int s) { return reinterpret_cast<uint8_t*>(kv_cache(c, s, 0, 0)) + (long long)first * row; },
               (long long)(len - first) * row, segs, [&](int s) { return (long long)c->cap[s] * row; });
   if (rc != HY_OK || cf.kv_format == 0) return rc;
-  // scales, from a multiple of 8 rows on (16-byte pieces; the rows before are alike) to one of 4 within the padding
-  const int r0 = first & ~7, r1 = cap_scales(len), sb = cf.kv_format == 1 ? 4 : hd / 16;
+  // scales: the 16-byte pieces from the one that holds row `first` on (what lies in it before that row stays) to a
+  // multiple of 4 rows within the padding
+  const int sb = cf.kv_format == 1 ? 4 : hd / 16;  // bytes of a row's: 4, 8 or 16
+  const long long from = (long long)first * sb & ~15ll;
   return region(
       [&](int s) {
         uint8_t* base = cf.kv_format == 1 ? reinterpret_cast<uint8_t*>(kv_scales(c, s, 0, 0))
                                           : reinterpret_cast<uint8_t*>(kv4_scales(c, s, 0, 0));
-        return base + (long long)r0 * sb;
+        return base + from;
       },
-      (long long)(r1 - r0) * sb, segs, [&](int s) { return (long long)cap_scales(c->cap[s]) * sb; });
+      (long long)cap_scales(len) * sb - from, segs, [&](int s) { return (long long)cap_scales(c->cap[s]) * sb; },
+      (int)((long long)first * sb - from));
 }
 }  // namespace
 

@@ -271,13 +271,15 @@ void set_span(SelectParams* p, int groups, int nsm);
 cudaError_t select(const SelectParams& p, int groups, cudaStream_t st);
 
 // Segment s of state i of group z: seg_bytes bytes at base[i] + z * group_stride
-// + s * seg_stride[i] (all multiples of 16).  Paged (page_bytes > 0): rows
+// + s * seg_stride[i] (all multiples of 16), the first `skip` bytes left as they
+// are (0, 4, 8 or 12).  Paged (page_bytes > 0): rows
 // [first_row, end_row) of row_bytes bytes, row r of the segment in page
 // pages[i][r / page_rows], at base[i] + page * page_bytes + s * seg_stride[i].
 struct ReorderParams {
   uint8_t* base[kMaxBeams];
   long long seg_stride[kMaxBeams];
   long long group_stride, seg_bytes;
+  int skip;
   int beams, n_seg;
   const int* parent;             // [groups * beams]; null: every state becomes state 0
   unsigned* guard;

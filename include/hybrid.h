@@ -209,11 +209,11 @@ int hy_seq_copy(hy_cache* c, int32_t src, int32_t dst, void* stream);
 /* Reorder the states of the n (1..16) distinct sequences seqs_host, all of the
  * same length, in place: sequence i takes what sequence parent_dev[i] (an index
  * into seqs_host, on the device: a selection's result) held, repeats allowed.
- * Only KV rows from position `first` on are moved (rows before it are taken to
- * be alike in all of them, as a common prompt's are: 0 moves every row); the
- * DeltaNet states and conv rings are moved whole.  A parent outside [0, n)
- * leaves its sequence as it is (HY_GUARD_BAD_INDEX, see hy_check_device).
- * Every KV format, paged or not.  Stream-ordered.  "hanzo-engine: A Portable
+ * Only KV rows from position `first` on are moved (0: every row); the rows
+ * before it stay as they are, in every format (a common prompt's are alike in
+ * all of the sequences and need no move).  The DeltaNet states and conv rings
+ * are moved whole.  A parent outside [0, n) leaves its sequence as it is
+ * (HY_GUARD_BAD_INDEX, see hy_check_device).  Paged or not.  Stream-ordered.  "hanzo-engine: A Portable
  * Single-Binary LLM Inference Engine...", section "System Architecture"
  * (sequences that share and leave a batch between steps). */
 int hy_seq_reorder(hy_cache* c, const int32_t* seqs_host, int32_t n, const int32_t* parent_dev, int32_t first,

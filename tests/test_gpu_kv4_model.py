@@ -271,3 +271,29 @@ def test_beam_search_with_an_end_token(built):
         d, sc, tk = to_np(beams.done), to_np(beams.scores), to_np(beams.tokens)
         assert ended in sc[d == 1].tolist() and (tk[d == 1] == eos).all()
     assert torch.isfinite(beams.scores).all()
+
+
+@pytest.mark.parametrize("kind,hd", [("bf16", 64), ("int8", 64), ("paged", 64), ("4-bit", 64), ("4-bit", 128), ("4-bit", 256)])
+def test_reorder_leaves_the_rows_before_first(built, kind, hd):
+    """Unlike sequences reordered from a row inside a 16-byte piece of the scales: every row before it stays the sequence's own,
+    every later one is the parent's.  In a one-layer model the rows of a position depend on its token alone, so the
+    sequence goes on exactly as one does that was prompted with its own tokens up to `first` and its parent's from there."""
+    torch = _torch()
+    from bandwidth_bound_hybrid_gb300.model import HybridModel
+    shape = dataclasses.replace(SHAPES[kind], name=f"{kind}-{hd}", n_layers=1, attn_layers=(0,), head_dim=hd, attn_q_heads=8,
+                                attn_kv_heads=2)
+    m = HybridModel(shape, workloads.device_weights(shape), [24, 30, 24, 30], pages=(128, 4) if kind == "paged" else None)
+    rng = np.random.default_rng(hd)
+    for n in (13, 16):
+        for first in (0, 1, 2, 3, 5, 7, 8, 11, n - 1, n):
+            prompts = rng.integers(0, shape.vocab, (2, n)).astype(np.int32)
+            for s in range(4):
+                m.reset(s)
+            for s in range(2):
+                m.prefill(s, torch.from_numpy(prompts[s]).cuda())
+                mixed = np.concatenate([prompts[s, :first], prompts[1 - s, first:]])
+                m.prefill(2 + s, torch.from_numpy(mixed).cuda())
+            m.reorder([0, 1], ints(1, 0), first=first)
+            got = next_logits(m, [0, 1, 2, 3])
+            np.testing.assert_array_equal(got[:2], got[2:], err_msg=f"{n} rows from {first} on")
+    assert m.check_device() == 0
