@@ -50,11 +50,14 @@ def make_config(shape, splits: int = 0, flags: int = 0) -> hy_config:
 class BeamState:
     """What HybridModel.beam_step keeps of n beams (CUDA tensors): the tokens
     to decode next, the scores (log probabilities so far), which beams have
-    ended, and each beam's parent in the last step.  All beams start alike, so
-    only the first counts in the first step (the others' scores are
+    ended, and each beam's parent in the last step.  n is 1..8, the sequences
+    of one hy_decode_step (a MoE model's step may take fewer).  All beams start
+    alike, so only the first counts in the first step (the others' scores are
     -infinity)."""
 
     def __init__(self, n: int, vocab: int, token: int):
+        if not 1 <= n <= 8:
+            raise ValueError(f"{n} beams: a decode step takes 1..8 sequences")
         import torch
         i32 = dict(dtype=torch.int32, device="cuda")
         self.tokens = torch.full((n,), int(token), **i32)
@@ -197,11 +200,20 @@ class HybridModel:
         decodes beams.tokens, selects the best continuations of all beams, and
         moves every sequence to its parent's state (KV rows from position
         `first`, the prompt's length, on).  `beams`: a BeamState, updated in
-        place."""
+        place.  eos < 0: no token ends a beam.  Refused calls (ValueError, or
+        HybridError from the decode step: too many sequences, one of them full
+        or twice) leave sequences and beams as they were."""
+        seqs = [int(s) for s in seqs]
         n, V = len(seqs), self.shape.vocab
         if tuple(beams.logits.shape) != (n, V):
             raise ValueError(f"beam state of {beams.logits.shape[0]} beams x {beams.logits.shape[1]} tokens for {n} "
                              f"sequences x {V} tokens")
+        # what the selection and the reordering would refuse, once the sequences have gone on
+        if eos >= V or first < 0:
+            raise ValueError(f"end token {eos} (below {V}), first position {first} (from 0)")
+        lens = [self.seq_len(s) for s in seqs]
+        if len(set(lens)) > 1:
+            raise ValueError(f"beams of different lengths: {lens}")
         self.decode_batch(seqs, beams.tokens, beams.ids, beams.logits, stream)
         check(capi.lib().hy_op_beam_select(_ptr(beams.logits), V, 1, n, V, n, _ptr(beams.scores),
                                            _ptr(beams.done) if eos >= 0 else None, int(eos), _ptr(beams.scores),
