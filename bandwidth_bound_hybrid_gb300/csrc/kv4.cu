@@ -24,10 +24,11 @@
 // and in a CTA each warp takes every W-th tile of the CTA's range through its
 // own cp.async ring and keeps its own running maximum, sum and outputs (no
 // block barrier inside a range).  A CTA gets one range of at most m tiles of
-// one (sequence, head), m the least for which the CTAs suffice; where that
+// one (sequence, head), m about the least for which the CTAs suffice (the
+// least, where the bounds of the search are at most 31 apart); where that
 // leaves much more than an equal share (more heads than CTAs, a few long
-// contexts each), all tiles form one list instead and every CTA takes an
-// equal span of it, its ends moved to a nearby border between heads.
+// contexts each), all tiles form one list instead and every CTA takes an equal
+// span of it, its ends moved to a nearby border between heads.
 // An (sequence, head) that several CTAs share is joined from their partials
 //   R = max_i r_i,  o = sum_i 2^(r_i - R) o_i / sum_i 2^(r_i - R) l_i
 // without any CTA waiting: the last of each 24 sharers to arrive joins the 24,
@@ -42,6 +43,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "kv4_dev.cuh"
+#include "kv4_plan.h"
 
 namespace hy {
 namespace kv4 {
@@ -247,28 +249,20 @@ __device__ __forceinline__ void plan_work(const Params& p, Small& sm) {
   const int total = p.nkv * (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
   const int items = p.nkv * __popc(__ballot_sync(0xffffffffu, n > 0));
   const int grid = gridDim.x;
-  // least m: a tile per warp if the CTAs suffice, else 32 candidates, a lane
-  // each, from an equal share up to total / (grid - items), which always does
+  // m: a tile per warp if the CTAs suffice, else the least of 32 candidates that fits, a lane each
   int m = 0, per = (n + W - 1) / W;
   if (p.nkv * (int)__reduce_add_sync(0xffffffffu, (unsigned)per) <= grid) {
     m = W;
   } else {
     if (items <= grid) {
-      const int lo = max(W, (int)((unsigned)(total + grid - 1) / (unsigned)grid));
-      const int spare = grid - items;
-      const int hi = max(lo, spare ? (int)((unsigned)(total + spare - 1) / (unsigned)spare) : total);
-      const unsigned mine = lane < 31 ? lo + (unsigned)(hi - lo) / 31u * lane : hi;
+      const int lo = (int)shortest_range(total, grid, W);
+      const int hi = (int)longest_range(total, grid, items, lo);
+      const unsigned mine = range_length(lo, hi, lane);
       unsigned ranges = 0;
-      // ceil(x / mine) by FP32: off by less than 1 below 2^21, the larger quotients fit nowhere all the same
       const float inv = 1.0f / (float)mine;
 #pragma unroll
-      for (int b = 0; b < kMaxB; ++b) {  // (n is 0 past the last sequence)
-        const unsigned x = __shfl_sync(0xffffffffu, n, b);
-        unsigned r = (unsigned)((float)x * inv);
-        r += r * mine < x;
-        r += r * mine < x;
-        ranges += r;
-      }
+      for (int b = 0; b < kMaxB; ++b)  // (n is 0 past the last sequence)
+        ranges += ranges_of(__shfl_sync(0xffffffffu, n, b), mine, inv);
       const unsigned fits = __ballot_sync(0xffffffffu, p.nkv * (int)ranges <= grid);
       m = fits ? (int)__shfl_sync(0xffffffffu, mine, __ffs(fits) - 1) : 0;
       // a second range costs a CTA about what three tiles of every warp do
