@@ -395,7 +395,11 @@ int hy_op_gemv_argmax(const void* W_dev, int32_t rows, int32_t cols, const float
  * each group's best `picks` (1..32, at most beams * vocab) candidates are
  * written in order, best first: score_out_dev, parent_out_dev (beam w of the
  * group) and token_out_dev (v), all [groups][picks].  Ties go to the lowest w *
- * vocab + v; scores are compared in FP64 and written as FP32.  A beam with
+ * vocab + v.  Scores are added and compared in FP64 and written as FP32; the
+ * log sum exp in them comes from FP32 sums and errs by at most 2^-17 + 2^-21
+ * ceil(vocab / 4096) (below 1e-6 for usual logits), so candidates of different
+ * beams that are closer than twice that may come in either order, unless their
+ * beams are alike in scores and logits: those have equal sums.  A beam with
  * done_dev[w] != 0 (nullable: none) is not read and has one candidate, (w,
  * eos) with its score unchanged; done_out_dev (nullable) tells which picks
  * have ended (a done parent, or the token eos; eos < 0: no token ends a beam,

@@ -213,6 +213,39 @@ def test_select_again_and_concurrently(L):
     check([to_np(t) for t in outs[0][1]], logits, score2, None, 1, 3, 4, 4)
 
 
+@pytest.mark.parametrize("groups,beams,V", [(6, 1, 151936), (640, 1, 262144), (6, 1, 1000003), (2, 3, 151936)])
+def test_select_score_error(L, groups, beams, V):
+    """The bound that include/hybrid.h states for the log-sum-exp, 2^-17 + 2^-21 ceil(V / 4096): logits of a lane that grow
+    step after step (every step a new maximum), fall, are flat, a peak over a flat tail, normal, or far below zero.
+
+    Per step of 4096 logits a lane's sum takes two roundings (2 2^-24) and an ex2.approx (2^-22) whose rounded argument
+    counts 2^-24 ln 2 d 2^-d at most, d octaves apart: below 2^-21.  Apart from that 16 terms are summed (15 2^-24), each
+    an ex2.approx (2^-22) of a rounded argument (2^-24 ln 2 times its octaves, whose mean weighted by the terms is at most
+    log2 V <= 27: 19 2^-24), then the lanes (ex2, 6 2^-24), the warps (ex2, 9 2^-24) and the chunks (ex2, 2^-24); FP32's
+    log2 e is 2^-26 off, times as many octaves (5 2^-24), and the logarithm errs by 2^-25: 73 2^-24 < 2^-17.  (One
+    beam a group: every row's log-sum-exp shows.)"""
+    torch = _torch()
+    rows, dev = groups * beams, dict(device="cuda")
+    g = torch.Generator(**dev)
+    g.manual_seed(V)
+    up = torch.arange(V, **dev).float() * (24.0 / V)
+    kinds = [up, up.flip(0), torch.full((V,), 3.75, **dev), torch.where(torch.arange(V, **dev) == V // 3, 12.0, 0.25), up * 4 - 70]
+    x = torch.empty((rows, V), **dev)
+    for r in range(rows):
+        x[r] = torch.randn(V, generator=g, **dev) * 2.5 if r % 6 == 5 else kinds[r % 6]
+    score = torch.full((rows,), -2.0, **dev)
+    ws = torch.zeros(L.hy_op_beam_select_workspace(groups, beams, V), dtype=torch.uint8, device="cuda")
+    so = torch.empty((groups, beams), **dev)
+    po, to = (torch.empty((groups, beams), dtype=torch.int32, **dev) for _ in range(2))
+    assert L.hy_op_beam_select(x.data_ptr(), V, groups, beams, V, beams, score.data_ptr(), None, -1, so.data_ptr(), po.data_ptr(),
+                               to.data_ptr(), None, ws.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
+    row = (po.long() + torch.arange(groups, **dev)[:, None] * beams).view(-1)
+    lse = torch.cat([torch.logsumexp(x[i:i + 32].double(), -1) for i in range(0, rows, 32)])
+    want = -2.0 + x[row, to.long().view(-1)].double() - lse[row]
+    err = (so.double().view(-1) - want).abs() - 2.0 ** -24 * want.abs()
+    assert (err <= 2.0 ** -17 + 2.0 ** -21 * -(-V // 4096)).all()
+
+
 # ------------------------------------------------------------------ reordering
 @pytest.mark.parametrize("groups,beams,n_seg,seg,pitch,pad", [
     (1, 1, 1, 16, 16, 0), (1, 2, 1, 65536, 65536, 0), (3, 4, 5, 48, 80, 32), (2, 8, 7, 4112, 4112, 16), (1, 16, 3, 100000, 100016, 0),
