@@ -13,8 +13,11 @@
 // so both products run on the tensor cores on the codes themselves, which
 // fp16 holds exactly, and the scales stay FP32 factors outside: of a block's
 // partial score, and of the probability that meets a block of V.  q and
-// p sV are split into two fp16 parts (relative error 2^-22), which a
-// row-by-8-heads (or hi-and-lo-of-4-heads) operand carries in one MMA.
+// p sV are split into two fp16 parts, which err by 2^-22 of the value, or where
+// that is below fp16's subnormals by 2^-34 of the head's largest |q| and 2^-38
+// of the largest sV that the warp has met.  (So a block of V far below others
+// has fewer bits: 2^-16 of a row at a ratio of 2^22.)  A row-by-8-heads (or
+// hi-and-lo-of-4-heads) operand carries them in one MMA.
 // A batch of small queries against a cache that is read once fills 8 of the
 // 128 rows of a tcgen05 tile and would still need the codes widened into
 // shared memory, so this uses mma.sync, whose operands are widened in

@@ -489,8 +489,12 @@ int hy_op_attention_i8(const float* y_dev, void* Kq_dev, float* Ks_dev, void* Vq
  * values that the appended rows stand for, FP32 [batch][2][nkv][hd] (k, then
  * v).  A sequence whose T is negative or at or past cap is left as it was, its
  * o and kv_new unwritten (HY_GUARD_BAD_POSITION); the others run.
- * rope_table_dev has at least cap rows.  The work is shared over the GPU by
- * cached rows whatever the mix of lengths.  workspace_dev:
+ * rope_table_dev has at least cap rows.  Sums and softmax are FP32; queries and
+ * weighted V scales enter the products with 22 bits, and with an absolute error
+ * of 2^-34 of the head's largest |q| and 2^-38 of the largest V scale (so
+ * blocks of V whose scales lie 2^16 or more below others' lose low bits).  The
+ * work is shared over the GPU by cached rows whatever the mix of lengths.
+ * workspace_dev:
  * hy_op_attention_q4_workspace() bytes (the same for every batch; 0 for bad
  * shapes or without a usable GPU), zeroed before its first use and then passed
  * unmodified to later calls of the same nq, nkv and hd; calls that can overlap

@@ -192,3 +192,26 @@ def test_norms_against_64_bits(L, nkv, G, hd, lens):
             want = t.softmax(q @ K.T / math.sqrt(hd), -1) @ V
             rel = (o[b, kv] - want).norm(dim=-1) / want.norm(dim=-1)
             assert (rel <= 2.0 ** -19).all(), (b, T, kv, rel.tolist())
+
+
+@pytest.mark.parametrize("nkv,G,hd", [(2, 8, 256), (4, 4, 128), (3, 1, 64)])
+@pytest.mark.parametrize("ratio", [2.0 ** -10, 2.0 ** -20])
+def test_blocks_far_below_others(L, nkv, G, hd, ratio):
+    """One block of V large, the others small: a row's weighted scale errs by 2^-22 of itself or 2^-38 of the largest, times
+    |code| <= 7.  Weights relative to the largest, 1 / max p in all; 2^-19 covers what the norms above allow a row."""
+    c = Cache(L, nkv, G, hd, [5000, 321], 5, powers_of_two)
+    t = c.torch
+    c.q["Vs"] *= ratio
+    c.q["Vs"][..., 0] = 1.0
+    c.q["Ks"] *= 0.125
+    c.y.normal_(generator=c.g)
+    c.y.view(c.B, -1, hd)[:, c.nq + nkv:] *= ratio
+    o = c.call()
+    for b, T in enumerate(c.lens):
+        for kv in range(nkv):
+            K, V = c.values("K", b, kv), c.values("V", b, kv)
+            q = c.y[b].view(-1, hd)[kv * G:(kv + 1) * G].double()
+            p = t.softmax(q @ K.T / math.sqrt(hd), -1)
+            tol = 2.0 ** -19 * (p @ V.abs()) + (T + 1) * p.amax(-1, keepdim=True) * 7 * 2.0 ** -38
+            err = (o[b, kv] - p @ V).abs()
+            assert (err <= tol).all(), (b, kv, float((err / tol).max()))
