@@ -297,3 +297,41 @@ def test_reorder_leaves_the_rows_before_first(built, kind, hd):
             got = next_logits(m, [0, 1, 2, 3])
             np.testing.assert_array_equal(got[:2], got[2:], err_msg=f"{n} rows from {first} on")
     assert m.check_device() == 0
+
+
+@pytest.mark.parametrize("kind", list(SHAPES))
+def test_copy_over_longer_and_shorter_sequences(built, kind):
+    """What the destination held before, longer or shorter or nothing, does not show; the source stays as it is."""
+    m = make(kind, [300, 310, 290, 300])
+    m.fill_synthetic(0, 150, seed=1)
+    m.fill_synthetic(1, 280, seed=2)
+    m.fill_synthetic(2, 3, seed=3)
+    for s in (1, 2, 3):
+        m.copy(0, s)
+        assert m.seq_len(s) == 150
+    got = [next_logits(m, [s])[0] for s in range(4)]
+    for s in (1, 2, 3):
+        assert rel_l2(got[s], got[0]) < 1e-5
+    m.reset(3)
+    m.copy(3, 1)  # an empty sequence
+    assert m.seq_len(1) == 0 and m.seq_len(0) == 151
+    assert rel_l2(next_logits(m, [1])[0], next_logits(m, [3])[0]) < 1e-5
+    assert m.check_device() == 0
+
+
+@pytest.mark.parametrize("kind", list(SHAPES))
+def test_one_beam_is_the_greedy_search(built, kind):
+    torch = _torch()
+    from bandwidth_bound_hybrid_gb300.model import BeamState
+    m = make(kind, [100, 100])
+    prompt = torch.from_numpy(workloads.prompt_ids(workloads.WORKLOADS["tiny"], n=40)).cuda()
+    m.prefill(0, prompt[:-1])
+    m.copy(0, 1)
+    beams = BeamState(1, m.shape.vocab, int(prompt[-1]))
+    tok, ids = prompt[-1:].clone(), ints(0)
+    for _ in range(8):
+        m.beam_step([0], beams, first=39)
+        m.decode_step(1, tok, ids)
+        tok.copy_(ids)
+        assert beams.tokens.tolist() == ids.tolist() and beams.parent.tolist() == [0]
+    assert m.check_device() == 0
