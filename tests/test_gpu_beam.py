@@ -246,6 +246,26 @@ def test_select_score_error(L, groups, beams, V):
     assert (err <= 2.0 ** -17 + 2.0 ** -21 * -(-V // 4096)).all()
 
 
+def test_select_offsets_past_32_bits(L):
+    """2.2e9 logits: the last groups' rows lie past 2^31 elements."""
+    torch = _torch()
+    groups, beams, V = 900, 16, 151936
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    x = torch.empty((groups * beams, V), device="cuda")
+    assert x.numel() > 2 ** 31
+    x.normal_(0, 2.5, generator=g)
+    score = -20 * torch.rand(groups * beams, generator=g, device="cuda") - 1
+    ws = torch.zeros(L.hy_op_beam_select_workspace(groups, beams, V), dtype=torch.uint8, device="cuda")
+    out = torch.empty((groups, 4), device="cuda"), *(torch.empty((groups, 4), dtype=torch.int32, device="cuda") for _ in range(3))
+    assert L.hy_op_beam_select(x.data_ptr(), V, groups, beams, V, 4, score.data_ptr(), None, 2, out[0].data_ptr(), out[1].data_ptr(),
+                               out[2].data_ptr(), out[3].data_ptr(), ws.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
+    for q in (0, 1, 700, groups - 2, groups - 1):
+        rows = slice(q * beams, (q + 1) * beams)
+        one = to_np(x[rows]), to_np(score[rows])
+        check([to_np(t[q:q + 1]) for t in out], one[0], one[1], None, 2, 1, beams, 4)
+
+
 # ------------------------------------------------------------------ reordering
 @pytest.mark.parametrize("groups,beams,n_seg,seg,pitch,pad", [
     (1, 1, 1, 16, 16, 0), (1, 2, 1, 65536, 65536, 0), (3, 4, 5, 48, 80, 32), (2, 8, 7, 4112, 4112, 16), (1, 16, 3, 100000, 100016, 0),
@@ -304,3 +324,21 @@ def test_reorder_interleaved(L, groups, beams, n_seg, seg, gap):
     assert L.hy_op_beam_reorder(d.data_ptr(), stride, n_seg, groups * beams * stride, seg, groups, beams, p.data_ptr(),
                                 torch.cuda.current_stream().cuda_stream) == 0, L.hy_last_error()
     np.testing.assert_array_equal(to_np(d), want)
+
+
+def test_reorder_offsets_past_32_bits(L):
+    """States of 4.3 GB each, exchanged, in one segment and in segments far apart."""
+    torch = _torch()
+    n = 2 ** 29 + 2 ** 20 + 4  # values of 8 bytes
+    a = torch.arange(2 * n, dtype=torch.int64, device="cuda").view(2, n)
+    p = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    st = torch.cuda.current_stream().cuda_stream
+    assert L.hy_op_beam_reorder(a.data_ptr(), n * 8, 1, n * 8, n * 8, 1, 2, p.data_ptr(), st) == 0, L.hy_last_error()
+    want = torch.arange(n, dtype=torch.int64, device="cuda")
+    assert torch.equal(a[0], want + n) and torch.equal(a[1], want)
+    # two segments of two states, [segment][beam][...]
+    b = a.view(2, 2, n // 2)
+    assert L.hy_op_beam_reorder(b.data_ptr(), n // 2 * 8, 2, n * 8, n // 2 * 8, 1, 2, p.data_ptr(), st) == 0, L.hy_last_error()
+    h = n // 2
+    assert torch.equal(a[0, :h], want[h:] + n) and torch.equal(a[0, h:], want[:h] + n)
+    assert torch.equal(a[1, :h], want[h:]) and torch.equal(a[1, h:], want[:h])

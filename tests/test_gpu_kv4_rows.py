@@ -215,3 +215,22 @@ def test_blocks_far_below_others(L, nkv, G, hd, ratio):
             tol = 2.0 ** -19 * (p @ V.abs()) + (T + 1) * p.amax(-1, keepdim=True) * 7 * 2.0 ** -38
             err = (o[b, kv] - p @ V).abs()
             assert (err <= tol).all(), (b, kv, float((err / tol).max()))
+
+
+def test_offsets_past_32_bits(L):
+    """Codes of 4.6 GB each: a long last sequence behind short ones, its last heads past 2^32 bytes."""
+    lens = [3, 0, 17, 40, 5, 33, 1, 69998]
+    c = Cache(L, 64, 1, 256, lens, 6, powers_of_two)
+    assert c.q["K"].numel() > 2 ** 32
+    c.new_row()
+    kept = {n: c.q[n][:, :, -1].clone() for n in ("K", "V")}  # the row behind the longest sequence's last
+    o = c.call()
+    for b, T in enumerate(lens):
+        for kv in range(0, 64, 7):
+            want = c.values("V", b, kv).sum(0) / (T + 1)
+            err = (o[b, kv] - want).abs()
+            assert (err <= 2.0 ** -23 * (1 + 2.0 ** -20) * want.abs()).all(), (b, T, kv)
+            codes, _ = quant(c.y[b].view(-1, 256)[64 + kv].cpu().numpy())
+            assert (c.q["K"][b, kv, T].cpu().numpy() == pack(codes)).all()
+    for n in ("K", "V"):
+        assert c.torch.equal(c.q[n][:-1, :, -1], kept[n][:-1])
