@@ -399,7 +399,8 @@ int hy_op_gemv_argmax(const void* W_dev, int32_t rows, int32_t cols, const float
  * log sum exp in them comes from FP32 sums and errs by at most 2^-17 + 2^-21
  * ceil(vocab / 4096) (below 1e-6 for usual logits), so candidates of different
  * beams that are closer than twice that may come in either order, unless their
- * beams are alike in scores and logits: those have equal sums.  A beam with
+ * beams are alike in scores and logits: those have equal sums.  (Unequal logits
+ * of one beam may too where FP64 scores do not tell them apart.)  A beam with
  * done_dev[w] != 0 (nullable: none) is not read and has one candidate, (w,
  * eos) with its score unchanged; done_out_dev (nullable) tells which picks
  * have ended (a done parent, or the token eos; eos < 0: no token ends a beam,
