@@ -58,6 +58,11 @@ class hy_weights(ctypes.Structure):
     _fields_ = [("embed", vp), ("final_norm", vp), ("lm_head", hy_tensor), ("layers", P(hy_layer_weights))]
 
 
+class hy_kv_p8(ctypes.Structure):
+    _fields_ = [("k_codes", vp), ("v_codes", vp), ("k_scales", vp), ("v_scales", vp), ("page_stride", i64), ("scale_stride", i64),
+                ("page_tokens", i32), ("pool_pages", i32), ("tail", vp), ("tail_stride", i64), ("table", vp), ("max_pages", i32)]
+
+
 # name -> (restype, argtypes), exactly the functions declared in include/hybrid.h
 SIGNATURES = {
     "hy_last_error": (ctypes.c_char_p, []),
@@ -102,6 +107,12 @@ SIGNATURES = {
     "hy_op_attention_q4_workspace": (sz, [i32, i32, i32, i32]),
     "hy_op_attention_q4": (ctypes.c_int, [vp, i32, i32, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, i32, vp, vp, vp]),
     "hy_op_kv_append_q4": (ctypes.c_int, [vp, i32, i32, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp]),
+    "hy_op_kv_append_p8": (ctypes.c_int, [vp, i32, i32, i32, vp, P(hy_kv_p8), i32, i32, i32, vp, vp, vp, vp]),
+    "hy_op_attention_p8_workspace": (sz, [i32, i32, i32, i32]),
+    "hy_op_attention_p8": (ctypes.c_int, [vp, i32, i32, P(hy_kv_p8), i32, i32, i32, i32, i32, vp, vp, vp, i32, vp, vp, vp]),
+    "hy_op_attention_p8_prompt_workspace": (sz, [i32, i32, i32, i32, i32]),
+    "hy_op_attention_p8_prompt": (ctypes.c_int, [vp, i32, i32, i32, vp, P(hy_kv_p8), i32, i32, i32, i32, i32, vp, vp, vp, i32, vp,
+                                                 vp]),
     "hy_op_beam_select_workspace": (sz, [i32, i32, i32]),
     "hy_op_beam_select": (ctypes.c_int, [vp, i32, i32, i32, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp]),
     "hy_op_beam_reorder": (ctypes.c_int, [vp, i64, i32, i64, i64, i32, i32, vp, vp]),

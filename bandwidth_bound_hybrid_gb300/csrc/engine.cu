@@ -2473,6 +2473,154 @@ int hy_op_kv_append_q4(const float* y_dev, int32_t ldy, int32_t n, void* Kq_dev,
   return HY_OK;
 }
 
+// The paged 8-bit cache's kernels, set up by the calls that use them (as the
+// 4-bit cache's: loaded with the others they would move those in the GPU's
+// code memory).
+static int ensure_p8(int dev) {
+  static std::map<int, bool> done;
+  std::lock_guard<std::mutex> lk(g_init_mu);
+  if (done[dev]) return HY_OK;
+  HY_CK(p8::init());
+  HY_CK(p8::init_prompt());
+  done[dev] = true;
+  return HY_OK;
+}
+
+static bool p8_shape(int32_t nq, int32_t nkv, int32_t hd) {
+  return nkv > 0 && nkv <= 1024 && nq > 0 && nq % nkv == 0 && (hd == 64 || hd == 128 || hd == 256) &&
+         (nq / nkv == 1 || nq / nkv == 2 || nq / nkv == 4 || nq / nkv == 8);
+}
+
+// Checks that the calls on a paged 8-bit cache share; fills in p.
+static int p8_params(const float* y, int32_t ldy, int32_t n, int32_t batch, const hy_kv_p8* kv, int32_t nq,
+                     int32_t nkv, int32_t hd, const int32_t* len, const float* rope, p8::Params* p) {
+  if (!kv || !aligned16(kv->k_codes) || !aligned16(kv->v_codes) || !aligned(kv->k_scales) || !aligned(kv->v_scales) ||
+      !aligned16(kv->tail) || !aligned(kv->table) || !aligned(y) || !aligned(len) || !aligned(rope, 8))
+    return fail(HY_ERR_ARG, "8-bit paged cache: a null or misaligned pointer");
+  if (nq <= 0 || nkv <= 0 || nq % nkv || hd <= 0 || n < 0 || batch < 1 ||
+      (long long)ldy < ((long long)nq + 2 * nkv) * hd)
+    return fail(HY_ERR_ARG, "8-bit paged cache: bad sizes (ldy >= (nq + 2 nkv) hd, batch >= 1)");
+  if (!p8_shape(nq, nkv, hd) || batch > p8::kMaxB)
+    return fail(HY_ERR_UNSUPPORTED, "8-bit paged cache: head_dim 64/128/256, nq/nkv in {1,2,4,8}, nkv <= 1024, batch <= %d",
+                p8::kMaxB);
+  if (kv->page_tokens <= 0 || kv->page_tokens % p8::kBlock || kv->pool_pages <= 0 || kv->max_pages <= 0)
+    return fail(HY_ERR_ARG, "8-bit paged cache: page_tokens a positive multiple of %d, pool_pages and max_pages positive",
+                p8::kBlock);
+  if (kv->page_tokens > 65536 || (long long)kv->page_tokens * kv->max_pages > 0x7fffffffll)
+    return fail(HY_ERR_UNSUPPORTED, "8-bit paged cache: page_tokens at most 65536, a capacity below 2^31");
+  if (kv->page_stride % 16 || kv->page_stride < (long long)nkv * kv->page_tokens * hd || kv->tail_stride % 16 ||
+      kv->tail_stride < 64ll * nkv * hd || kv->scale_stride < (long long)nkv * (kv->page_tokens / p8::kBlock))
+    return fail(HY_ERR_ARG, "8-bit paged cache: strides too short or not multiples of 16 bytes");
+  memset(p, 0, sizeof(*p));
+  p->c.K = (int8_t*)kv->k_codes;
+  p->c.V = (int8_t*)kv->v_codes;
+  p->c.Ks = kv->k_scales;
+  p->c.Vs = kv->v_scales;
+  p->c.page_stride = kv->page_stride;
+  p->c.scale_stride = kv->scale_stride;
+  p->c.page_tokens = kv->page_tokens;
+  p->c.bpp = kv->page_tokens / p8::kBlock;
+  p->c.pool_pages = kv->pool_pages;
+  p->c.max_pages = kv->max_pages;
+  p->c.tail = (uint16_t*)kv->tail;
+  p->c.tail_stride = kv->tail_stride / 2;
+  p->c.table = kv->table;
+  p->y = y;
+  p->ld_y = ldy;
+  p->n = n;
+  p->nb = batch;
+  p->nq = nq;
+  p->nkv = nkv;
+  p->len = len;
+  p->rope = (const float2*)rope;
+  p->scale_log2e = kv4_scale(hd);
+  return HY_OK;
+}
+
+int hy_op_kv_append_p8(const float* y_dev, int32_t ldy, int32_t n, int32_t batch, const int32_t* row_start_dev,
+                       const hy_kv_p8* kv, int32_t nq, int32_t nkv, int32_t hd, const int32_t* len_dev,
+                       const float* rope_table_dev, float* kv_new_dev, void* stream) {
+  p8::Params p;
+  if (n == 0 && !y_dev) y_dev = rope_table_dev;  // no row is read
+  int rc = p8_params(y_dev, ldy, n, batch, kv, nq, nkv, hd, len_dev, rope_table_dev, &p);
+  if (rc != HY_OK) return rc;
+  if (!aligned(row_start_dev) || !null_or_aligned(kv_new_dev))
+    return fail(HY_ERR_ARG, "8-bit paged append: bad row_start or kv_new pointer");
+  if (n == 0) return HY_OK;
+  if ((rc = op_guard(&p.guard)) != HY_OK) return rc;
+  p.row_start = row_start_dev;
+  p.kv_new = kv_new_dev;
+  cudaError_t e = p8::append(p, hd, (cudaStream_t)stream);
+  if (e != cudaSuccess) return fail(HY_ERR_CUDA, "8-bit paged append launch: %s", cudaGetErrorString(e));
+  return HY_OK;
+}
+
+size_t hy_op_attention_p8_workspace(int32_t batch, int32_t nq, int32_t nkv, int32_t hd) {
+  if (batch < 1 || batch > p8::kMaxB || !p8_shape(nq, nkv, hd)) return 0;
+  const int nsm = op_nsm();
+  if (nsm <= 0) return 0;
+  return (p8::counters(batch, nkv) * 4 + 255) / 256 * 256 + p8::part_floats(nq, nkv, hd, nsm) * 4;
+}
+
+int hy_op_attention_p8(const float* y_dev, int32_t ldy, int32_t batch, const hy_kv_p8* kv, int32_t nq, int32_t nkv,
+                       int32_t hd, int32_t window, int32_t sinks, const int32_t* len_dev, const float* rope_table_dev,
+                       float* o_dev, int32_t ldo, float* kv_new_dev, void* workspace_dev, void* stream) {
+  p8::Params p;
+  int rc = p8_params(y_dev, ldy, batch, batch, kv, nq, nkv, hd, len_dev, rope_table_dev, &p);
+  if (rc != HY_OK) return rc;
+  if (!aligned(o_dev) || !null_or_aligned(kv_new_dev) || !aligned16(workspace_dev) || window < 0 || sinks < 0 ||
+      (long long)ldo < (long long)nq * hd)
+    return fail(HY_ERR_ARG, "bad 8-bit paged attention arguments (ldo >= nq hd, window and sinks not negative)");
+  if ((long long)batch * nkv * p.c.max_pages * p.c.bpp > (1 << 30))  // the list of tiles
+    return fail(HY_ERR_UNSUPPORTED, "8-bit paged cache: batch x nkv x capacity above 2^34 rows");
+  int dev = 0, nsm = 0;
+  if ((rc = op_guard(&p.guard)) != HY_OK || (rc = current_device(&dev, &nsm)) != HY_OK || (rc = ensure_p8(dev)) != HY_OK)
+    return rc;
+  p.o = o_dev;
+  p.ld_o = ldo;
+  p.kv_new = kv_new_dev;
+  p.window = window;
+  p.sinks = sinks;
+  p.counter = (unsigned*)workspace_dev;
+  p.part = (float*)((uint8_t*)workspace_dev + (p8::counters(batch, nkv) * 4 + 255) / 256 * 256);
+  cudaError_t e = p8::attention(p, hd, nsm, (cudaStream_t)stream);
+  if (e != cudaSuccess) return fail(HY_ERR_CUDA, "8-bit paged attention launch: %s", cudaGetErrorString(e));
+  return HY_OK;
+}
+
+size_t hy_op_attention_p8_prompt_workspace(int32_t n, int32_t batch, int32_t nq, int32_t nkv, int32_t hd) {
+  if (n < 0 || batch < 1 || batch > p8::kMaxB || !p8_shape(nq, nkv, hd)) return 0;
+  const int nsm = op_nsm();
+  if (nsm <= 0) return 0;
+  return p8::prompt_workspace(n, batch, nq, nkv, hd, nsm);
+}
+
+int hy_op_attention_p8_prompt(const float* y_dev, int32_t ldy, int32_t n, int32_t batch, const int32_t* row_start_dev,
+                              const hy_kv_p8* kv, int32_t nq, int32_t nkv, int32_t hd, int32_t window, int32_t sinks,
+                              const int32_t* len_dev, const float* rope_table_dev, float* o_dev, int32_t ldo,
+                              void* workspace_dev, void* stream) {
+  p8::Params p;
+  if (n == 0 && !y_dev) y_dev = rope_table_dev;  // no row is read
+  int rc = p8_params(y_dev, ldy, n, batch, kv, nq, nkv, hd, len_dev, rope_table_dev, &p);
+  if (rc != HY_OK) return rc;
+  if (!aligned(row_start_dev) || (n > 0 && !aligned(o_dev)) || !aligned16(workspace_dev) || window < 0 || sinks < 0 ||
+      (long long)ldo < (long long)nq * hd)
+    return fail(HY_ERR_ARG, "bad 8-bit paged prompt attention arguments (ldo >= nq hd, window and sinks not negative)");
+  if (n == 0) return HY_OK;
+  int dev = 0, nsm = 0;
+  if ((rc = op_guard(&p.guard)) != HY_OK || (rc = current_device(&dev, &nsm)) != HY_OK || (rc = ensure_p8(dev)) != HY_OK)
+    return rc;
+  p.row_start = row_start_dev;
+  p.o = o_dev;
+  p.ld_o = ldo;
+  p.window = window;
+  p.sinks = sinks;
+  p.part = (float*)workspace_dev;
+  cudaError_t e = p8::prompt(p, hd, nsm, (cudaStream_t)stream);
+  if (e != cudaSuccess) return fail(HY_ERR_CUDA, "8-bit paged prompt attention launch: %s", cudaGetErrorString(e));
+  return HY_OK;
+}
+
 static size_t beam_counters(int32_t groups) { return ((size_t)groups * 4 + 255) / 256 * 256; }
 static size_t beam_stats(int32_t groups, int32_t beams, int32_t vocab) {
   return ((size_t)groups * beams * beam::chunks(vocab) * 8 + 255) / 256 * 256;

@@ -241,6 +241,51 @@ cudaError_t launch(const Params& p, int hd, int nsm, cudaStream_t st, bool pdl);
 cudaError_t append(const AppendParams& p, int hd, cudaStream_t st);
 }  // namespace kv4
 
+// ---------------------------------------------------------------- paged 8-bit KV cache
+// 16 positions of a kv head are a block with one FP32 scale; the rows of a
+// sequence's open block are bf16 in its tail (p8.cu, p8_prompt.cu).
+namespace p8 {
+constexpr int kBlock = 16;      // rows of a block
+constexpr int kMaxB = 256;      // sequences of a call
+struct Cache {
+  int8_t* K;                    // page p, kv head h, row r: + p * page_stride + (h * page_tokens + r) * hd
+  int8_t* V;
+  float* Ks;                    // + p * scale_stride + h * bpp + r / kBlock
+  float* Vs;
+  long long page_stride, scale_stride;
+  int page_tokens, bpp;         // bpp = page_tokens / kBlock
+  int pool_pages, max_pages;
+  uint16_t* tail;               // sequence b: + b * tail_stride, [2][nkv][kBlock][hd]
+  long long tail_stride;        // elements
+  const int* table;             // [nb][max_pages]
+};
+struct Params {
+  Cache c;
+  const float* y;               // projection rows q|k|v
+  long long ld_y;
+  float* o;
+  long long ld_o;
+  float* kv_new;                // values of the new rows [n][2][nkv][hd] (nullable)
+  const float2* rope;           // (cos, sin) [>= capacity][hd/2]
+  const int* len;               // [nb] positions before the new rows
+  const int* row_start;         // [nb + 1] (append, prompt)
+  int n, nb, nq, nkv;           // n: rows of y (append, prompt)
+  int window, sinks;            // window 0: every position up to the query's
+  float scale_log2e;            // log2(e) / sqrt(hd)
+  float* part;
+  unsigned* counter;            // zero between launches
+  unsigned* guard;
+};
+size_t part_floats(int nq, int nkv, int hd, int nsm);
+size_t counters(int nb, int nkv);
+cudaError_t init();
+cudaError_t append(const Params& p, int hd, cudaStream_t st);
+cudaError_t attention(const Params& p, int hd, int nsm, cudaStream_t st);
+size_t prompt_workspace(int n, int nb, int nq, int nkv, int hd, int nsm);  // bytes
+cudaError_t init_prompt();
+cudaError_t prompt(const Params& p, int hd, int nsm, cudaStream_t st);
+}  // namespace p8
+
 // ---------------------------------------------------------------- beam search
 // Selection over beams and vocabulary, and in-place reordering of the beams'
 // states (beam.cu).

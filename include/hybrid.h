@@ -515,6 +515,96 @@ int hy_op_kv_append_q4(const float* y_dev, int32_t ldy, int32_t n, void* Kq_dev,
                        void* Vs_dev, int32_t cap, int32_t nq, int32_t nkv, int32_t hd, const int32_t* len_dev,
                        const float* rope_table_dev, float* kv_new_dev, void* stream);
 
+/* A paged 8-bit KV cache of one layer ("hanzo-engine: A Portable Single-Binary
+ * LLM Inference Engine...", section "System Architecture": paged KV, int8 KV).
+ * Rows are positions of a sequence.  A row (k after RoPE, v as projected) is
+ * rounded to bf16; what is not finite then is stored as NaN.  16 rows of a kv
+ * head that start at a multiple of 16 are a block.  Once all 16 are there the
+ * block is closed: int8 codes c and, for K and for V, one FP32 scale s, value
+ * = s c.  The rule, in FP32 with each operation rounded on its own: a = max
+ * |x| over the block's 16 hd values, s = a / 127, c = round-half-even(x * (127
+ * / a)) clamped to [-127, 127]; a < 2^-100: s = 0 and c = 0; a NaN in the block:
+ * s = NaN and c = 0.  The rows of a sequence's last, open block stay bf16 in
+ * its tail until the block closes, so what is held never depends on how the
+ * rows were cut into calls.  Closed blocks lie in pages of page_tokens rows of
+ * all kv heads.
+ * Sequence b (0-based in the call) has the pages table_dev[b][0..max_pages),
+ * of which only those that a call reads or writes need be valid: the others
+ * may hold anything (a page whose rows have left the window and are no sinks
+ * may go back to the pool), and the page of a block is first needed when the
+ * block closes.  Sequences may share pages that no call writes.  The capacity
+ * is max_pages * page_tokens positions; it and all pages are the caller's.
+ * A page id outside [0, pool_pages) that a call needs sets HY_GUARD_BAD_INDEX:
+ * nothing is written there, and its rows are left out of the attention. */
+typedef struct {
+  void* k_codes;        /* int8: page p, kv head h, row r of the page at + p * page_stride + (h * page_tokens + r) * hd */
+  void* v_codes;        /* (bytes; both 16-byte aligned) */
+  float* k_scales;      /* page p, head h, block j of the page at + p * scale_stride + h * (page_tokens / 16) + j */
+  float* v_scales;
+  int64_t page_stride;  /* bytes from page to page, a multiple of 16, >= nkv * page_tokens * hd */
+  int64_t scale_stride; /* floats from page to page, >= nkv * page_tokens / 16 */
+  int32_t page_tokens;  /* a multiple of 16, at most 65536 */
+  int32_t pool_pages;
+  void* tail;           /* bf16 [2][nkv][16][hd] (K, then V) of sequence b at + b * tail_stride, 16-byte aligned */
+  int64_t tail_stride;  /* bytes, a multiple of 16, >= 64 * nkv * hd */
+  const int32_t* table; /* device, [batch][max_pages] */
+  int32_t max_pages;
+} hy_kv_p8;
+
+/* Rows appended to the cache, with RoPE on the way: y_dev [n][ldy] are
+ * projection outputs q|k|v before RoPE (q is not read), rows
+ * [row_start_dev[b], row_start_dev[b + 1]) those of sequence b (0 <= b < batch
+ * <= 256; a sequence may have none; rows of y past row_start_dev[batch] are not
+ * read) at positions len_dev[b] on.  Blocks that become whole are closed.
+ * kv_new_dev (nullable) [n][2][nkv][hd] receives the values that the rows
+ * stand for after the call (k, then v).  len_dev is not changed.  A sequence
+ * with a negative length, more rows than its capacity has room for, or rows
+ * that are not within [0, n) in order is left as it was
+ * (HY_GUARD_BAD_POSITION); the others run.  rope_table_dev has at least
+ * capacity rows.  n = 0 does nothing.  The table and the tails must not alias
+ * between sequences that get rows. */
+int hy_op_kv_append_p8(const float* y_dev, int32_t ldy, int32_t n, int32_t batch, const int32_t* row_start_dev,
+                       const hy_kv_p8* kv, int32_t nq, int32_t nkv, int32_t hd, const int32_t* len_dev,
+                       const float* rope_table_dev, float* kv_new_dev, void* stream);
+
+/* Decode attention over the cache, one token for each of `batch` (1..256)
+ * sequences: y_dev [batch][ldy].  Sequence b rotates q and the new k at
+ * position T = len_dev[b], appends the new row as hy_op_kv_append_p8 does, and
+ * attends to the rows u <= T with u < sinks or u > T - window as held after
+ * that (window 0: every u <= T; the first `sinks` positions stay in view, at
+ * the positions they were rotated for).  o_dev [batch][ldo] FP32.
+ * kv_new_dev (nullable) [batch][2][nkv][hd].  A sequence whose T is negative or
+ * at or past its capacity is left as it was, its o and kv_new unwritten
+ * (HY_GUARD_BAD_POSITION); the others run.  Scores, softmax and sums are FP32;
+ * queries and probabilities enter the products with 22 bits, with an absolute
+ * error of 2^-34 of the head's largest |q| and 2^-39 of its largest
+ * probability.  The work is shared over the GPU by rows in view.
+ * workspace_dev: hy_op_attention_p8_workspace() bytes (0 for bad shapes or
+ * without a usable GPU), zeroed before its first use and then passed
+ * unmodified to later calls of the same batch, nq, nkv and hd; calls that can
+ * overlap on the GPU need a workspace each. */
+size_t hy_op_attention_p8_workspace(int32_t batch, int32_t nq, int32_t nkv, int32_t hd);
+int hy_op_attention_p8(const float* y_dev, int32_t ldy, int32_t batch, const hy_kv_p8* kv, int32_t nq, int32_t nkv,
+                       int32_t hd, int32_t window, int32_t sinks, const int32_t* len_dev, const float* rope_table_dev,
+                       float* o_dev, int32_t ldo, float* kv_new_dev, void* workspace_dev, void* stream);
+
+/* Prompt attention over the cache: the queries of the rows that
+ * hy_op_kv_append_p8 has just appended (the same y_dev, row_start_dev and
+ * len_dev, lengths before the append).  Row i of sequence b, at position t =
+ * len_dev[b] + i, attends to the rows u <= t with u < sinks or u > t - window, as
+ * held after the append (a row whose block has closed since then by its codes).
+ * o_dev [n][ldo] FP32; rows of o past row_start_dev[batch], and those of a
+ * sequence that the append refuses, stay as they are.  Precision as for
+ * hy_op_attention_p8.  workspace_dev: hy_op_attention_p8_prompt_workspace()
+ * bytes, 16-byte aligned, no zeroing needed, its contents meaningless between
+ * calls; calls that can overlap on the GPU need one each.  [Strata] "Act 1"
+ * (one launch per layer for all prompt tokens). */
+size_t hy_op_attention_p8_prompt_workspace(int32_t n, int32_t batch, int32_t nq, int32_t nkv, int32_t hd);
+int hy_op_attention_p8_prompt(const float* y_dev, int32_t ldy, int32_t n, int32_t batch, const int32_t* row_start_dev,
+                              const hy_kv_p8* kv, int32_t nq, int32_t nkv, int32_t hd, int32_t window, int32_t sinks,
+                              const int32_t* len_dev, const float* rope_table_dev, float* o_dev, int32_t ldo,
+                              void* workspace_dev, void* stream);
+
 /* hy_op_attention without a caller-provided workspace, for callers that
  * cannot allocate device memory: a host framework that owns the whole memory
  * budget through its own pool, a latency path where an allocation and the
