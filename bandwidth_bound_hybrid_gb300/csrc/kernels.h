@@ -247,6 +247,7 @@ cudaError_t append(const AppendParams& p, int hd, cudaStream_t st);
 namespace p8 {
 constexpr int kBlock = 16;      // rows of a block
 constexpr int kMaxB = 256;      // sequences of a call
+constexpr int kPromptCtas = 256; // CTAs of the prompt attention, at most
 struct Cache {
   int8_t* K;                    // page p, kv head h, row r: + p * page_stride + (h * page_tokens + r) * hd
   int8_t* V;

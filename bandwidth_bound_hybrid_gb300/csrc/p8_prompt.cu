@@ -1,128 +1,945 @@
-// Prompt attention over the paged 8-bit KV cache: a warp per query row and kv
-// head, FP32 throughout.
+// Prompt attention over the paged 8-bit KV cache on the tensor cores of sm_103a
+// (format: p8_dev.cuh).
+//
+// A tile is 128 query vectors of one sequence and kv head: 128 / G consecutive
+// rows with their G heads.  It goes over the blocks that any of its rows sees,
+// BN positions a step, with the running maximum and sum of a softmax:
+//   S = (q_hi + q_lo) cK^T,   w = 2^(s sK - m) sV 2^(14 - E),   O = (w_hi + w_lo) cV
+// q and w as two fp16 parts (22 bits; w down to 2^-39 of the step's largest V
+// scale), the codes exact in fp16, the blocks' scales FP32 factors of a score
+// and of the weight that meets a block of V (2^E above the step's largest).
+// A step's O is added to the outputs in registers, in FP32: the tensor cores
+// truncate what they add to an accumulator, which over a long context would be
+// 2^-24 a product, all one way.
+//
+// Roles of a CTA of 16 warps, one an SM:
+//   * 8 row warps: a thread has a row's scores of half a step (tcgen05.ld),
+//     the maximum is exchanged with the other half's thread; the weights go
+//     back into the scores' columns as the A operand of the second product
+//     (32 scores become 16 columns of w_hi and 16 of w_lo); then the step
+//     before is added, half the elements of a head a thread;
+//   * 4 warps widen the codes: 16 bytes of a row from the page (loads of the
+//     next half step on their way) to fp16 in shared memory, 128-byte swizzle,
+//     K as K-major B operand and V, laid out alike, as MN-major;
+//   * 1 thread issues tcgen05.mma: S of step k + 1 before O of step k, so that
+//     the row warps' softmax runs beside the tensor cores.
+// Two score and (hd <= 128) two output accumulators in TMEM: 512 columns.
+//
+// Work split: the steps of all tiles form one list, CTA c takes steps c n / C ..
+// of it.  A tile that several CTAs share leaves partials (outputs, maximum, sum)
+// in the workspace, joined by a second small kernel.
+#include <climits>
+
 #include "p8_dev.cuh"
+#include "tc05.cuh"
 
 namespace hy {
 namespace p8 {
 namespace {
 
+constexpr int kThreads = 512, kRowWarps = 8, kWidenWarps = 4;
+constexpr int kLeast = 2;  // steps of a CTA, if it can be
+
+template <int HD>
+struct Tile {
+  static constexpr int BM = 128, BN = HD == 256 ? 64 : 128;
+  static constexpr int NBLK = BN / kBlock;        // blocks of a step
+  static constexpr int kStages = HD == 256 ? 1 : 2;
+  static constexpr int NO = HD == 256 ? 1 : 2;    // output accumulators
+  static constexpr int kQ = BM * HD * 2;          // one part of the queries
+  static constexpr int kKV = BN * HD * 2;
+  static constexpr int kSmem = 2 * kQ + 2 * kStages * kKV;
+  static constexpr int NP = BN * HD / 16 / 128;   // 16-byte pieces of K or V a widening thread has
+};
+
+// What the row warps need of a step.
+struct Step {
+  float fk[8], fv[8];  // scales of K; of V times 2^(14 - E)
+  int u[8];            // first positions of the blocks; INT_MAX: not there
+  float ev;            // 2^(E - 14)
+  int edge;            // some row does not see all of it
+};
+
+struct alignas(16) Small {
+  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], ofull[2], oempty[2], mfull[4], qfull, done;
+  uint32_t tmem;
+  int open_nan;
+  Step step[4];
+  float qf[128];
+  float mx[2][2][128];
+  float ls[2][128];
+  // the work
+  int T[kMaxB], n[kMaxB], first[kMaxB];
+  long long at[kMaxB + 1];  // steps of one kv head before each sequence
+  long long begin, end;     // this CTA's steps
+  int b, g, i0;             // its first tile
+  long long tile;           // and that tile's first step
+};
+
+// A CTA's first piece, for the join: whether it is the tail of a tile that began in CTA `lo`, through CTA `hi`.
+struct Share {
+  int joins, lo, hi, b, g, i0;
+};
+
+struct Piece {
+  int b, g, i0;             // sequence, kv head, the tile's first row
+  long long tile;           // the tile's first step in the list
+  int T, n, rows, t0, t1;   // of the sequence: position, rows; of the tile: rows, first and last position
+  View view;
+  int steps, s0, s1;        // the tile's steps; this CTA's
+};
+
+// The blocks that some query of positions t0 .. t1 sees.
+__device__ __forceinline__ View view_range(int t0, int t1, int window, int sinks) {
+  View v = view_of(t0, window, sinks);
+  v.n += t1 / kBlock - t0 / kBlock;
+  return v;
+}
+template <int HD, int G>
+__device__ __forceinline__ int tile_steps(const Params& p, int T, int n, int i0) {
+  const int t0 = T + i0, t1 = T + min(n, i0 + Tile<HD>::BM / G) - 1;
+  return (view_range(t0, t1, p.window, p.sinks).n + Tile<HD>::NBLK - 1) / Tile<HD>::NBLK;
+}
+template <int HD, int G>
+__device__ __forceinline__ void set_piece(const Params& p, const Small& sm, Piece& w) {
+  w.T = sm.T[w.b];
+  w.n = sm.n[w.b];
+  w.rows = min(w.n - w.i0, Tile<HD>::BM / G);
+  w.t0 = w.T + w.i0;
+  w.t1 = w.t0 + w.rows - 1;
+  w.view = view_range(w.t0, w.t1, p.window, p.sinks);
+  w.steps = (w.view.n + Tile<HD>::NBLK - 1) / Tile<HD>::NBLK;
+  w.s0 = (int)(max(sm.begin, w.tile) - w.tile);
+  w.s1 = (int)(min(sm.end, w.tile + w.steps) - w.tile);
+}
+template <int HD, int G>
+__device__ __forceinline__ bool first_piece(const Params& p, const Small& sm, Piece& w) {
+  if (sm.begin >= sm.end) return false;
+  w.b = sm.b;
+  w.g = sm.g;
+  w.i0 = sm.i0;
+  w.tile = sm.tile;
+  set_piece<HD, G>(p, sm, w);
+  return true;
+}
+template <int HD, int G>
+__device__ __forceinline__ bool next_piece(const Params& p, const Small& sm, Piece& w) {
+  w.tile += w.steps;
+  if (w.tile >= sm.end) return false;
+  w.i0 += Tile<HD>::BM / G;
+  if (w.i0 >= w.n) {
+    w.i0 = 0;
+    do {
+      if (++w.b == p.nb) {
+        w.b = 0;
+        ++w.g;
+      }
+    } while (sm.n[w.b] == 0);  // (there is one with rows: the list has more steps)
+  }
+  set_piece<HD, G>(p, sm, w);
+  return true;
+}
+
+// Sequences, the list of steps and this CTA's span of it (the whole CTA).
+template <int HD, int G>
+__device__ __forceinline__ void plan_work(const Params& p, Small& sm, Share* share) {
+  constexpr int BQ = Tile<HD>::BM / G;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid < p.nb) {
+    const int T = p.len[tid], s = p.row_start[tid], e = p.row_start[tid + 1];
+    const bool ok = T >= 0 && s >= 0 && e >= s && e <= p.n &&
+                    (long long)T + (e - s) <= (long long)p.c.max_pages * p.c.page_tokens;
+    if (!ok && blockIdx.x == 0) set_guard(p.guard, kGuardBadPosition);
+    sm.T[tid] = T;
+    sm.first[tid] = s;
+    sm.n[tid] = ok ? e - s : 0;
+  }
+  __syncthreads();
+  for (int b = warp; b < p.nb; b += kThreads / 32) {
+    const int T = sm.T[b], n = sm.n[b];
+    long long s = 0;
+    for (int i0 = lane * BQ; i0 < n; i0 += 32 * BQ) s += tile_steps<HD, G>(p, T, n, i0);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) sm.at[b + 1] = s;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    long long base = 0;
+    for (int b0 = 0; b0 < p.nb; b0 += 32) {
+      long long incl = b0 + lane < p.nb ? sm.at[b0 + lane + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (b0 + lane < p.nb) sm.at[b0 + lane + 1] = base + incl;
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) sm.at[0] = 0;
+    __syncwarp();
+    const long long head = base, total = head * p.nkv;
+    const long long C = max(1ll, min((long long)gridDim.x, total / kLeast)), c = blockIdx.x;
+    const long long begin = c < C ? c * total / C : total, end = c < C ? (c + 1) * total / C : total;
+    Share mine = {0, 0, 0, 0, 0, 0};
+    if (begin < end) {
+      const int g = (int)(begin / head);
+      const long long r = begin - g * head;
+      int b = 0;  // the last b with at[b] <= r that has steps
+      for (int k = 0; k < p.nb; k += 32) {
+        const unsigned in = __ballot_sync(0xffffffffu, k + lane < p.nb && r < sm.at[min(k + lane, p.nb - 1) + 1]);
+        if (in) {
+          b = k + __ffs(in) - 1;
+          break;
+        }
+      }
+      long long at = sm.at[b];
+      const int T = sm.T[b], n = sm.n[b];
+      int i0 = 0, steps = 0;
+      for (int k = 0; k < n; k += 32 * BQ) {
+        const int i = k + lane * BQ;
+        const int s = i < n ? tile_steps<HD, G>(p, T, n, i) : 0;
+        int incl = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        const unsigned in = __ballot_sync(0xffffffffu, r < at + incl);
+        if (in) {
+          const int l = __ffs(in) - 1;
+          i0 = k + l * BQ;
+          steps = __shfl_sync(0xffffffffu, s, l);
+          at += __shfl_sync(0xffffffffu, incl - s, l);
+          break;
+        }
+        at += __shfl_sync(0xffffffffu, incl, 31);
+      }
+      const long long tile = g * head + at;
+      if (lane == 0) {
+        sm.b = b;
+        sm.g = g;
+        sm.i0 = i0;
+        sm.tile = tile;
+      }
+      // the last CTA c with c total / C <= s holds step s
+      const int lo = (int)(((tile + 1) * C - 1) / total), hi = (int)(((tile + steps) * C - 1) / total);
+      mine = {begin > tile && lo + 1 == c, lo, hi, b, g, i0};
+    }
+    if (lane == 0) {
+      sm.begin = begin;
+      sm.end = end;
+      share[blockIdx.x] = mine;
+    }
+  }
+  __syncthreads();
+}
+
+// ---------------------------------------------------------------- packed FP32
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// v truncated to fp16's 11 significant bits: v - trunc11(v) is exact
+__device__ __forceinline__ float trunc11(float v) { return __uint_as_float(__float_as_uint(v) & 0xffffe000u); }
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
-template <int HD, int G>
-__global__ void __launch_bounds__(128) k_rows(const Params p) {
-  extern __shared__ float smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = lane & 1, row = lane >> 1;
-  const long long unit = blockIdx.x * 4ll + warp;
-  const long long i = unit / p.nkv;
-  const int g = (int)(unit % p.nkv);
-  float* q = smem + warp * G * HD;
-  if (i >= p.n) return;
-  int b = 0;
-  while (b < p.nb && !(p.row_start[b] <= i && i < p.row_start[b + 1])) ++b;
-  if (b == p.nb) return;
-  const int rs = p.row_start[b], re = p.row_start[b + 1], T = p.len[b];
-  const long long cap = (long long)p.c.max_pages * p.c.page_tokens;
-  if (T < 0 || rs < 0 || re > p.n || (long long)T + (re - rs) > cap) {
-    if (lane == 0) set_guard(p.guard, kGuardBadPosition);
-    return;
-  }
-  const int t = T + (int)(i - rs), end = T + (re - rs);
-  const float* y = p.y + i * p.ld_y;
-  for (int k = lane; k < G * HD / 2; k += 32) {
-    const int j = k / (HD / 2), d = k % (HD / 2);
-    float x0 = y[(g * G + j) * HD + d], x1 = y[(g * G + j) * HD + d + HD / 2];
-    rotate(x0, x1, p.rope[(long long)t * (HD / 2) + d], &x0, &x1);
-    q[j * HD + d] = x0 * p.scale_log2e;
-    q[j * HD + d + HD / 2] = x1 * p.scale_log2e;
-  }
-  __syncwarp();
-  const View v = view_of(t, p.window, p.sinks);
-  float m[G], l[G], o[G][HD / 32];
-#pragma unroll
-  for (int j = 0; j < G; ++j) {
-    m[j] = -INFINITY;
-    l[j] = 0.f;
-#pragma unroll
-    for (int k = 0; k < HD / 32; ++k) o[j][k] = 0.f;
-  }
-  for (int n = 0; n < v.n; ++n) {
-    const int blk = block_at(v, n);
-    const bool open = blk == end / kBlock;
-    float s[G];
-#pragma unroll
-    for (int j = 0; j < G; ++j) s[j] = 0.f;
-    const uint16_t* tk = p.c.tail + b * p.c.tail_stride + (long long)g * kBlock * HD;
-    const uint16_t* tv = tk + (long long)p.nkv * kBlock * HD;
-    const int8_t *kc = nullptr, *vc = nullptr;
-    float ks = 1.f, vs = 1.f;
-    if (!open) {
-      const int pg = page_of(p.c, b, blk);
-      if (pg < 0) {
-        if (lane == 0) set_guard(p.guard, kGuardBadIndex);
-        continue;
-      }
-      kc = p.c.K + code_at(p.c, pg, g, blk % p.c.bpp, HD);
-      vc = p.c.V + code_at(p.c, pg, g, blk % p.c.bpp, HD);
-      ks = p.c.Ks[scale_at(p.c, pg, g, blk % p.c.bpp)];
-      vs = p.c.Vs[scale_at(p.c, pg, g, blk % p.c.bpp)];
-    }
-    const int u = blk * kBlock + row;
-    const bool seen = in_view(u, t, p.window, p.sinks);
-    if (seen)
-      for (int d = half * (HD / 2); d < (half + 1) * (HD / 2); ++d) {
-        const float x = open ? bf16_to_f32(tk[row * HD + d]) : (float)kc[row * HD + d];
-#pragma unroll
-        for (int j = 0; j < G; ++j) s[j] = fmaf(x, q[j * HD + d], s[j]);
-      }
-#pragma unroll
-    for (int j = 0; j < G; ++j) {
-      s[j] += __shfl_xor_sync(0xffffffffu, s[j], 1);
-      s[j] = seen ? s[j] * ks : -INFINITY;
-      const float mn = fmaxf(m[j], warp_max(s[j]));
-      const float corr = mn == -INFINITY ? 1.f : ex2(m[j] - mn);
-      m[j] = mn;
-      s[j] = seen ? ex2(s[j] - mn) : 0.f;
-      l[j] = l[j] * corr + 0.5f * warp_sum(s[j]);
-#pragma unroll
-      for (int k = 0; k < HD / 32; ++k) o[j][k] *= corr;
-    }
-    for (int r = 0; r < kBlock; ++r) {
-      if (!in_view(blk * kBlock + r, t, p.window, p.sinks)) continue;
-#pragma unroll
-      for (int k = 0; k < HD / 32; ++k) {
-        const int d = k * 32 + lane;
-        const float x = open ? bf16_to_f32(tv[r * HD + d]) : (float)vc[r * HD + d] * vs;
-#pragma unroll
-        for (int j = 0; j < G; ++j) o[j][k] = fmaf(__shfl_sync(0xffffffffu, s[j], 2 * r), x, o[j][k]);
-      }
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < G; ++j)
-#pragma unroll
-    for (int k = 0; k < HD / 32; ++k)
-      p.o[i * p.ld_o + (g * G + j) * HD + k * 32 + lane] = l[j] == 0.f ? 0.f : o[j][k] / l[j];
+// ---------------------------------------------------------------- tcgen05 forms
+// fp16 operands, FP32 accumulator; trans_b: B is MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool trans_b) {
+  return (1u << 4) | (trans_b ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// MN-major operand, 128-byte swizzle: rows of 64 elements, one per k; 8-row groups 1024 bytes apart, the next 64
+// elements `chunk` bytes on.
+__device__ __forceinline__ uint64_t sdesc_mn128(uint32_t saddr, uint32_t chunk) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFF);
+  d |= (uint64_t)((chunk >> 4) & 0x3FFF) << 16;
+  d |= (uint64_t)((1024 >> 4) & 0x3FFF) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+template <int R>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+// Registers of a thread by role: 8 x 176 + 4 x 120 + 4 x 40 = 2048, the launch's 16 x 128.
+constexpr int kRowRegs = 176, kWidenRegs = 120, kOtherRegs = 40;
+static_assert(kRowWarps * kRowRegs + kWidenWarps * kWidenRegs + 4 * kOtherRegs <= kThreads / 32 * 128, "register split");
+
+// A warp's wait; false, with the guard set, if it gave up.
+__device__ __forceinline__ bool wait_all(const Params& p, uint64_t* bar, uint32_t parity) {
+  const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
+  if (!ok && (threadIdx.x & 31) == 0) set_guard(p.guard, kGuardWaitTimeout);
+  return ok;
+}
+// A row warp's wait.  One that has given up goes on without waiting (its outputs are worthless, the guard says so),
+// so that it still meets the other row warps at their barriers.
+__device__ __forceinline__ void wait_row(const Params& p, uint64_t* bar, uint32_t parity, bool& ok) {
+  if (ok) ok = wait_all(p, bar, parity);
 }
 
+// ---------------------------------------------------------------- widening
+// The codes of a word's bytes as fp16 pairs, exact: c + 128 under the exponent of 1024, less 1152.
+__device__ __forceinline__ void widen(uint32_t w, uint32_t* h) {
+  const __half2 k1152 = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+  w ^= 0x80808080u;
+  const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), k1152);
+  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), k1152);
+  h[0] = *reinterpret_cast<const uint32_t*>(&x);
+  h[1] = *reinterpret_cast<const uint32_t*>(&y);
+}
+// 16 elements from 16 c of row r: two 16-byte chunks of a 128-byte row; the chunks of the upper half of a line's
+// pieces in the other order, so that 8 lanes store to 8 different bank groups.
+template <int BN>
+__device__ __forceinline__ void put16(uint8_t* tile, int r, int c, const uint32_t* h) {
+  uint8_t* row = tile + (c >> 2) * (BN * 128) + r * 128;
+  const int k = (c & 3) * 2, x = (c >> 2) & 1;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int s = i ^ x;
+    *reinterpret_cast<uint4*>(row + (((k + s) ^ (r & 7)) << 4)) =
+        s ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
+  }
+}
+
+template <int HD, int G>
+__device__ __forceinline__ void widen_role(const Params& p, Small& sm, uint8_t* kbuf, uint8_t* vbuf) {
+  using Ti = Tile<HD>;
+  constexpr int BN = Ti::BN, NBLK = Ti::NBLK, NP = Ti::NP, NC = HD / 16, NST = Ti::kStages;
+  const int wt = threadIdx.x - kRowWarps * 32, lane = threadIdx.x & 31;
+  Piece w;
+  int ks = 0;
+  for (bool more = first_piece<HD, G>(p, sm, w); more; more = next_piece<HD, G>(p, sm, w)) {
+    const int end = w.T + w.n, ob = end / kBlock;  // the open block, if end % 16
+    const uint16_t* tail = p.c.tail + w.b * p.c.tail_stride + (long long)w.g * kBlock * HD;
+    const long long tail_v = (long long)p.nkv * kBlock * HD;
+    // the open block's exponents: its values below 2^7
+    float osk = 0.f, osv = 0.f, upk = 0.f, upv = 0.f;
+    if (w.s1 == w.steps && end % kBlock != 0 && w.t1 / kBlock == ob) {
+      uint32_t a[2] = {0, 0};
+      bool nan = false;
+      for (int i = lane; i < (end % kBlock) * HD / 2; i += 32)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const uint32_t x = reinterpret_cast<const uint32_t*>(tail + v * tail_v)[i];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t m = (x >> (16 * h)) & 0x7fffu;
+            if (m < 0x7f80u)
+              a[v] = max(a[v], m);
+            else
+              nan |= v == 1;
+          }
+        }
+      a[0] = __reduce_max_sync(0xffffffffu, a[0]);
+      a[1] = __reduce_max_sync(0xffffffffu, a[1]);
+      const int ek = min(6 + 127 - (int)(a[0] >> 7), 100), ev = min(6 + 127 - (int)(a[1] >> 7), 100);
+      upk = pow2(ek);
+      upv = pow2(ev);
+      osk = pow2(-ek);
+      osv = pow2(-ev);
+      if (nan) sm.open_nan = 1;
+    }
+    // blocks of a step, a lane each: page (-1: none), block within it, scales, first position
+    struct Look {
+      int pg, off, u;
+      float ks, vs;
+    };
+    auto look_up = [&](int s) {
+      Look k = {-1, 0, INT_MAX, 0.f, 0.f};
+      const int i = s * NBLK + lane;
+      if (lane < NBLK && i < w.view.n) {
+        const int blk = block_at(w.view, i);
+        if (blk == ob) {  // (past the closed blocks)
+          k.pg = -2;
+          k.ks = osk;
+          k.vs = osv;
+          k.u = blk * kBlock;
+        } else {
+          const int at = blk / p.c.bpp;
+          k.off = blk - at * p.c.bpp;
+          k.pg = __ldg(p.c.table + (long long)w.b * p.c.max_pages + at);
+          if ((unsigned)k.pg >= (unsigned)p.c.pool_pages) {
+            if (wt < 32) set_guard(p.guard, kGuardBadIndex);
+            k.pg = -1;
+          } else {
+            const long long sc = scale_at(p.c, k.pg, w.g, k.off);
+            k.ks = __ldg(p.c.Ks + sc);
+            k.vs = __ldg(p.c.Vs + sc);
+            k.u = blk * kBlock;
+          }
+        }
+      }
+      return k;
+    };
+    // this thread's pieces of a step's K or V (zeros where there is no page)
+    auto load = [&](const Look& k, const int8_t* base, uint4* x) {
+#pragma unroll
+      for (int u = 0; u < NP; ++u) {
+        const int id = u * 128 + wt, r = id / NC;
+        const int pg = __shfl_sync(0xffffffffu, k.pg, r / kBlock), off = __shfl_sync(0xffffffffu, k.off, r / kBlock);
+        x[u] = make_uint4(0, 0, 0, 0);
+        if (pg >= 0)
+          x[u] = __ldg(reinterpret_cast<const uint4*>(base + code_at(p.c, pg, w.g, off, HD) +
+                                                      ((r % kBlock) * NC + id % NC) * 16));
+      }
+    };
+    auto store = [&](const Look& k, const uint4* x, uint8_t* tile, const uint16_t* rows, float up, bool is_v) {
+#pragma unroll
+      for (int u = 0; u < NP; ++u) {
+        const int id = u * 128 + wt, r = id / NC, c = id % NC;
+        const int pg = __shfl_sync(0xffffffffu, k.pg, r / kBlock);
+        uint32_t h[8];
+        if (pg != -2) {
+          widen(x[u].x, h);
+          widen(x[u].y, h + 2);
+          widen(x[u].z, h + 4);
+          widen(x[u].w, h + 6);
+        } else {  // rows of the tail that are there; V's NaN as 0 (its own rows' outputs get them at the end)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t q = 0;
+            if (r % kBlock < end % kBlock) q = reinterpret_cast<const uint32_t*>(rows + (r % kBlock) * HD + c * 16)[i];
+            if (is_v && (q & 0x7f80u) == 0x7f80u) q &= 0xffff0000u;
+            if (is_v && (q & 0x7f800000u) == 0x7f800000u) q &= 0xffffu;
+            h[i] = half2_bits(bf16_lo(q) * up, bf16_hi(q) * up);
+          }
+        }
+        put16<BN>(tile, r, c, h);
+      }
+    };
+    Look cur = look_up(w.s0), nxt = cur;
+    uint4 xk[NP], xv[NP];
+    load(cur, p.c.K, xk);
+    for (int s = w.s0; s < w.s1; ++s, ++ks) {
+      const int st = ks % NST;
+      const uint32_t ph = (ks / NST) & 1;
+      load(cur, p.c.V, xv);
+      if (s + 1 < w.s1) nxt = look_up(s + 1);
+      if (ks >= NST && !wait_all(p, &sm.kempty[st], ph ^ 1)) return;
+      // The step's scales and places, by one warp.  Those of step ks - 4 have been read: S of ks - NST is done, so O
+      // of ks - 4 at the latest had been issued before it, which waited for all row warps.
+      if (wt < 32) {
+        Step& m = sm.step[ks & 3];
+        const uint32_t vb = lane < NBLK && cur.u != INT_MAX && cur.vs == cur.vs ? __float_as_uint(cur.vs) : 0u;
+        const uint32_t top = __reduce_max_sync(0xffffffffu, vb);
+        const int E = top ? (int)(top >> 23) - 126 : 0;  // 2^E above the largest
+        bool full = true;
+        if (lane < NBLK) {
+          m.fk[lane] = cur.ks;
+          m.fv[lane] = cur.vs * pow2(14 - E);
+          m.u[lane] = cur.u;
+          full = cur.u != INT_MAX && cur.u + kBlock - 1 <= w.t0 &&
+                 (p.window <= 0 || cur.u > w.t1 - p.window || cur.u + kBlock <= p.sinks);
+        }
+        full = __all_sync(0xffffffffu, full);
+        if (lane == 0) {
+          m.ev = pow2(E - 14);
+          m.edge = !full;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.mfull[ks & 3]);
+      }
+      store(cur, xk, kbuf + st * Ti::kKV, tail, upk, false);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.kfull[st]);
+      if (s + 1 < w.s1) load(nxt, p.c.K, xk);
+      if (ks >= NST && !wait_all(p, &sm.vempty[st], ph ^ 1)) return;
+      store(cur, xv, vbuf + st * Ti::kKV, tail + tail_v, upv, true);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.vfull[st]);
+      cur = nxt;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- products
+template <int HD, int G>
+__device__ __forceinline__ void mma_role(const Params& p, Small& sm, uint32_t q, uint32_t kbuf, uint32_t vbuf) {
+  using Ti = Tile<HD>;
+  constexpr int BN = Ti::BN, NST = Ti::kStages, NO = Ti::NO;
+  const uint32_t tmem = sm.tmem, out = tmem + 2 * BN;
+  constexpr uint32_t id_s = idesc_f16(128, BN, false), id_o = idesc_f16(128, HD, true);
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = mbar_wait(bar, parity);
+    if (!ok) set_guard(p.guard, kGuardWaitTimeout);
+    return ok;
+  };
+  Piece w;
+  int ks = 0, np = 0;
+  bool ok = true;
+  for (bool more = first_piece<HD, G>(p, sm, w); more && ok; more = next_piece<HD, G>(p, sm, w), ++np) {
+    const int steps = w.s1 - w.s0;
+    ok = wait(&sm.qfull, np & 1);
+    auto scores = [&](int k) {
+      const int st = k % NST;
+      if (!wait(&sm.kfull[st], (k / NST) & 1)) return false;
+      tc::fence_after_sync();
+      const uint32_t d = tmem + (k & 1) * BN;
+      uint64_t a0 = tc::sdesc_k128(q), a1 = tc::sdesc_k128(q + Ti::kQ), b = tc::sdesc_k128(kbuf + st * Ti::kKV);
+      asm volatile("" : "+l"(a0), "+l"(a1), "+l"(b));  // (descriptors of the loop made here, not kept over the steps)
+#pragma unroll
+      for (int c = 0; c < HD / 16; ++c) {  // (addresses in 16-byte units; they stay below the field's 2^14)
+        const int at = ((c >> 2) * (128 * 128) + (c & 3) * 32) >> 4, bt = ((c >> 2) * (BN * 128) + (c & 3) * 32) >> 4;
+        tc::mma_bf16(d, a0 + at, b + bt, id_s, c > 0);
+        tc::mma_bf16(d, a1 + at, b + bt, id_s, true);
+      }
+      tc::mma_commit(&sm.kempty[st]);
+      tc::mma_commit(&sm.sfull[k & 1]);
+      return true;
+    };
+    if (ok) ok = scores(ks);
+    for (int s = 0; ok && s < steps; ++s, ++ks) {
+      if (s + 1 < steps && !(ok = scores(ks + 1))) break;
+      const int st = ks % NST, ob = ks % NO;
+      ok = wait(&sm.pfull[ks & 1], (ks >> 1) & 1) && wait(&sm.vfull[st], (ks / NST) & 1) &&
+           (ks < NO || wait(&sm.oempty[ob], ((ks / NO) - 1) & 1));
+      if (!ok) break;
+      tc::fence_after_sync();
+      const uint32_t d = out + ob * HD, a = tmem + (ks & 1) * BN;
+      uint64_t b = sdesc_mn128(vbuf + st * Ti::kKV, BN * 128);
+      asm volatile("" : "+l"(b));
+#pragma unroll
+      for (int c = 0; c < BN / 16; ++c) {
+        const uint32_t hi = a + (c >> 1) * 32 + (c & 1) * 8;
+        mma_ts(d, hi, b + c * (2048 >> 4), id_o, c > 0);
+        mma_ts(d, hi + 16, b + c * (2048 >> 4), id_o, true);
+      }
+      tc::mma_commit(&sm.vempty[st]);
+      tc::mma_commit(&sm.ofull[ob]);
+    }
+  }
+  // every issued MMA has completed before TMEM is released
+  tc::mma_commit(&sm.done);
+  wait(&sm.done, 0);
+}
+
+// ---------------------------------------------------------------- rows
+__device__ __forceinline__ uint32_t low_mask(int n) { return n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1; }
+
 template <int HD>
-void (*pick(int G))(Params) {
-  return G == 1 ? k_rows<HD, 1> : G == 2 ? k_rows<HD, 2> : G == 4 ? k_rows<HD, 4> : k_rows<HD, 8>;
+__host__ __device__ constexpr int part_floats_of() { return 128 * HD + 256; }  // outputs, maxima, sums
+
+template <int HD, int G>
+__device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q, float* part) {
+  using Ti = Tile<HD>;
+  constexpr int BN = Ti::BN, NO = Ti::NO, NV = BN / 2, NA = HD / 2;  // scores and outputs of a thread
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = warp & 3, half = warp >> 2, row = sub * 32 + lane;
+  const uint32_t lanes = (uint32_t)(sub * 32) << 16;
+  const uint32_t scores = sm.tmem + lanes + half * NV, outs = sm.tmem + lanes + 2 * BN + half * NA;
+  Piece w;
+  int ks = 0;
+  bool ok = true;
+  for (bool more = first_piece<HD, G>(p, sm, w); more; more = next_piece<HD, G>(p, sm, w)) {
+    // ------------------------------------------------ queries: warp `warp` rows 16 warp ..
+    // normalised by 2^e with 2^e max |q| in [2^9, 2^10): as two fp16 parts q keeps 22 bits of the row's largest
+    constexpr int PP = HD / 64;  // pairs of a lane
+    for (int m0 = warp * 16; m0 < warp * 16 + 16; m0 += 4) {
+      float x[4][PP][2];
+      float2 cs[4][PP];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // (rows past the tile's read its last one)
+        const int i = min((m0 + k) / G, w.rows - 1);
+        const float* y = p.y + (sm.first[w.b] + w.i0 + i) * p.ld_y + (long long)(w.g * G + (m0 + k) % G) * HD;
+        const float2* rope = p.rope + (long long)(w.t0 + i) * (HD / 2);
+#pragma unroll
+        for (int u = 0; u < PP; ++u) {
+          x[k][u][0] = y[u * 32 + lane];
+          x[k][u][1] = y[u * 32 + lane + HD / 2];
+          cs[k][u] = rope[u * 32 + lane];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t a = 0;
+#pragma unroll
+        for (int u = 0; u < PP; ++u) {
+          rotate(x[k][u][0], x[k][u][1], cs[k][u], &x[k][u][0], &x[k][u][1]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            x[k][u][h] *= p.scale_log2e;
+            a = max(a, __float_as_uint(x[k][u][h]) & 0x7fffffffu);
+          }
+        }
+        a = __reduce_max_sync(0xffffffffu, a);
+        const int e = min(max(9 + 127 - (int)(a >> 23), -103), 100), m = m0 + k;
+        const float up = pow2(e);
+        if (lane == 0) sm.qf[m] = pow2(-e);
+#pragma unroll
+        for (int u = 0; u < PP; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int d = u * 32 + lane + h * (HD / 2), c = d >> 3;
+            const float v = x[k][u][h] * up;
+            const __half hi = __float2half_rn(v), lo = __float2half_rn(v - __half2float(hi));
+            uint8_t* at = q + (c >> 3) * (128 * 128) + m * 128 + (((c ^ m) & 7) << 4) + (d & 7) * 2;
+            *reinterpret_cast<__half*>(at) = hi;
+            *reinterpret_cast<__half*>(at + Ti::kQ) = lo;
+          }
+      }
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.qfull);
+    // the queries' factors are another warp's: wait for the other row warps
+    named_barrier(9, kRowWarps * 32);
+    const float qf = sm.qf[row];
+    const int t = w.t0 + min(row / G, w.rows - 1);
+
+    uint64_t acc[NA / 2];
+#pragma unroll
+    for (int i = 0; i < NA / 2; ++i) acc[i] = 0;
+    float mx = -INFINITY, lsum = 0.f, corr = 1.f, ev = 0.f;
+    // the outputs of step k, under the reference that corr moved the running ones to
+    auto gather = [&](int k, float cf, float ef) {
+      const int ob = k % NO;
+      wait_row(p, &sm.ofull[ob], (k / NO) & 1, ok);
+      tc::fence_after_sync();
+      const bool moved = __any_sync(0xffffffffu, cf != 1.f);
+      const uint64_t c2 = pack2(cf, cf), e2 = pack2(ef, ef);
+#pragma unroll
+      for (int c = 0; c < NA; c += 32) {
+        float v[32];
+        tc::tmem_ld32(outs + ob * HD + c, v);
+        if (moved) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[c / 2 + i] = mul2(acc[c / 2 + i], c2);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[c / 2 + i] = fma2(pack2(v[2 * i], v[2 * i + 1]), e2, acc[c / 2 + i]);
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.oempty[ob]);
+    };
+    for (int s = w.s0; s < w.s1; ++s, ++ks) {
+      const int buf = ks & 1;
+      wait_row(p, &sm.mfull[ks & 3], (ks >> 2) & 1, ok);
+      wait_row(p, &sm.sfull[buf], (ks >> 1) & 1, ok);
+      tc::fence_after_sync();
+      const Step& m = sm.step[ks & 3];
+      float v[NV];
+#pragma unroll
+      for (int c = 0; c < NV; c += 32) tc::tmem_ld32(scores + buf * BN + c, v + c);
+      if (m.edge) {
+#pragma unroll
+        for (int j = 0; j < NV / 16; ++j) {
+          const int u = m.u[half * (NV / 16) + j];
+          uint32_t see = 0;
+          if (u != INT_MAX) {
+            see = low_mask(t - u + 1);
+            if (p.window > 0) see &= ~low_mask(t - p.window - u + 1) | low_mask(p.sinks - u);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (!(see >> i & 1)) v[j * 16 + i] = -INFINITY;
+        }
+      }
+      float top = -INFINITY, f[NV / 16];
+#pragma unroll
+      for (int j = 0; j < NV / 16; ++j) {
+        float b = v[j * 16];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) b = fmaxf(b, v[j * 16 + i]);
+        f[j] = m.fk[half * (NV / 16) + j] * qf;
+        // (a block of scale 0 has scores 0, and a row that it is out of view for none)
+        top = fmaxf(top, b == -INFINITY ? b : b * f[j]);
+      }
+      sm.mx[buf][half][row] = top;
+      named_barrier(1 + sub, 64);
+      top = fmaxf(top, sm.mx[buf][half ^ 1][row]);
+      const float mn = fmaxf(mx, top), ref = mn == -INFINITY ? 0.f : mn;
+      const float cf = mx == mn ? 1.f : ex2(mx - mn);
+      mx = mn;
+      // weights, their sum and their two parts
+      uint64_t sum2 = 0;
+      const uint64_t nref = pack2(-ref, -ref);
+#pragma unroll
+      for (int c = 0; c < NV; c += 32) {
+        uint32_t pr[32];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int j = (c + 2 * i) / 16;
+          const float fv = m.fv[half * (NV / 16) + j];
+          float a0, a1;
+          if (m.edge) {
+            a0 = v[c + 2 * i] == -INFINITY ? -INFINITY : fmaf(v[c + 2 * i], f[j], -ref);
+            a1 = v[c + 2 * i + 1] == -INFINITY ? -INFINITY : fmaf(v[c + 2 * i + 1], f[j], -ref);
+          } else {
+            unpack2(fma2(pack2(v[c + 2 * i], v[c + 2 * i + 1]), pack2(f[j], f[j]), nref), a0, a1);
+          }
+          const float p0 = ex2(a0), p1 = ex2(a1);
+          sum2 = add2(sum2, pack2(p0, p1));
+          float w0, w1, l0, l1;
+          unpack2(mul2(pack2(p0, p1), pack2(fv, fv)), w0, w1);
+          if (m.edge) {  // a NaN scale does not reach rows that do not see its block
+            if (v[c + 2 * i] == -INFINITY) w0 = 0.f;
+            if (v[c + 2 * i + 1] == -INFINITY) w1 = 0.f;
+          }
+          const float h0 = trunc11(w0), h1 = trunc11(w1);
+          l0 = w0 - h0;
+          l1 = w1 - h1;
+          pr[i] = half2_bits(h0, h1);
+          pr[16 + i] = half2_bits(l0, l1);
+        }
+        tmem_st32(scores + buf * BN + c, pr);
+      }
+      const float step_ev = m.ev;
+      wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.pfull[buf]);
+      float s0, s1;
+      unpack2(sum2, s0, s1);
+      lsum = fmaf(lsum, cf, s0 + s1);
+      if (s > w.s0) gather(ks - 1, corr, ev);
+      corr = cf;
+      ev = step_ev;
+    }
+    gather(ks - 1, corr, ev);
+
+    // ------------------------------------------------ outputs
+    sm.ls[half][row] = lsum;
+    named_barrier(1 + sub, 64);
+    const float l = lsum + sm.ls[half ^ 1][row];
+    float* o = nullptr;
+    float inv = 1.f;
+    const bool whole = w.s0 == 0 && w.s1 == w.steps, live = row < w.rows * G;
+    if (whole) {
+      inv = l == 0.f ? 0.f : 1.0f / l;
+      o = p.o + (sm.first[w.b] + w.i0 + row / G) * p.ld_o + (long long)(w.g * G + row % G) * HD + half * NA;
+    } else {
+      // a tile that begins here leaves the CTA's second partial, one that goes on its first
+      float* d = part + (2ll * blockIdx.x + (w.s0 == 0)) * part_floats_of<HD>();
+      o = d + row * HD + half * NA;
+      if (half == 0) {
+        d[128 * HD + row] = mx;
+        d[128 * HD + 128 + row] = l;
+      }
+    }
+    // an open row's NaN in V: in the outputs of the rows that see it
+    const int end = w.T + w.n, ob = end / kBlock;
+    uint32_t see = 0;
+    if (sm.open_nan && w.s1 == w.steps && w.t1 / kBlock == ob) {
+      see = low_mask(t - ob * kBlock + 1);
+      if (p.window > 0) see &= ~low_mask(t - p.window - ob * kBlock + 1) | low_mask(p.sinks - ob * kBlock);
+    }
+    const uint16_t* tv = p.c.tail + w.b * p.c.tail_stride + ((long long)p.nkv + w.g) * kBlock * HD + half * NA;
+    if (live) {
+      const bool vec = ((reinterpret_cast<uintptr_t>(o) & 15) == 0);
+#pragma unroll
+      for (int i = 0; i < NA / 4; ++i) {
+        float r[4];
+        unpack2(acc[2 * i], r[0], r[1]);
+        unpack2(acc[2 * i + 1], r[2], r[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r[k] *= inv;
+        if (see)
+          for (int m = 0; m < kBlock; ++m)
+            if (see >> m & 1)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if ((tv[m * HD + i * 4 + k] & 0x7f80u) == 0x7f80u) r[k] = __uint_as_float(0x7fc00000u);
+        if (vec) {
+          reinterpret_cast<float4*>(o)[i] = make_float4(r[0], r[1], r[2], r[3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[i * 4 + k] = r[k];
+        }
+      }
+    }
+  }
+}
+
+template <int HD, int G>
+__global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ Params p) {
+  using Ti = Tile<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Small& sm = *reinterpret_cast<Small*>(smem + Ti::kSmem);
+  Share* share = reinterpret_cast<Share*>(p.part);
+  float* part = p.part + 2048;
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.kfull[s], kWidenWarps);
+      mbar_init(&sm.vfull[s], kWidenWarps);
+      mbar_init(&sm.kempty[s], 1);
+      mbar_init(&sm.vempty[s], 1);
+      mbar_init(&sm.sfull[s], 1);
+      mbar_init(&sm.pfull[s], kRowWarps);
+      mbar_init(&sm.ofull[s], 1);
+      mbar_init(&sm.oempty[s], kRowWarps);
+    }
+    for (int s = 0; s < 4; ++s) mbar_init(&sm.mfull[s], 1);
+    mbar_init(&sm.qfull, kRowWarps);
+    mbar_init(&sm.done, 1);
+    sm.open_nan = 0;
+    fence_mbar_init();
+  }
+  plan_work<HD, G>(p, sm, share);
+  if (sm.begin >= sm.end) return;  // the whole CTA
+  if (warp == kRowWarps + kWidenWarps) tc::tmem_alloc(&sm.tmem, 512);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  uint8_t *q = smem, *kbuf = smem + 2 * Ti::kQ, *vbuf = kbuf + Ti::kStages * Ti::kKV;
+  if (warp < kRowWarps) {
+    regs_inc<kRowRegs>();
+    row_role<HD, G>(p, sm, q, part);
+  } else if (warp < kRowWarps + kWidenWarps) {
+    regs_dec<kWidenRegs>();
+    widen_role<HD, G>(p, sm, kbuf, vbuf);
+  } else {
+    regs_dec<kOtherRegs>();
+    if (warp == kRowWarps + kWidenWarps && (threadIdx.x & 31) == 0)
+      mma_role<HD, G>(p, sm, smem_addr(q), smem_addr(kbuf), smem_addr(vbuf));
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kRowWarps + kWidenWarps) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(sm.tmem, 512);
+  }
+}
+
+// The tile that CTA blockIdx.x + 1 found begun, if it is the second of its sharers: their partials joined, 16 rows a
+// block, a warp per row.
+template <int HD, int G>
+__global__ void __launch_bounds__(256) k_join(const __grid_constant__ Params p) {
+  const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Share s = reinterpret_cast<const Share*>(p.part)[c];
+  if (!s.joins) return;
+  const float* part = p.part + 2048;
+  const int first = p.row_start[s.b], n = p.row_start[s.b + 1] - first;
+  auto part_of = [&](int k) { return part + (2ll * k + (k == s.lo)) * part_floats_of<HD>(); };
+  for (int row = blockIdx.y * 16 + warp; row < blockIdx.y * 16 + 16; row += 8) {
+    const int i = s.i0 + row / G;
+    if (i >= n) return;
+    float R = -INFINITY, den = 0.f;
+    for (int k = s.lo + lane; k <= s.hi; k += 32) R = fmaxf(R, part_of(k)[128 * HD + row]);
+    R = warp_max(R);
+    float a[HD / 32];
+#pragma unroll
+    for (int d = 0; d < HD / 32; ++d) a[d] = 0.f;
+    for (int k = s.lo; k <= s.hi; ++k) {
+      const float* q = part_of(k);
+      const float r = q[128 * HD + row], f = R == -INFINITY ? (r == r ? 1.f : r) : ex2(r - R);
+      den = fmaf(f, q[128 * HD + 128 + row], den);
+#pragma unroll
+      for (int d = 0; d < HD / 32; ++d) a[d] = fmaf(f, q[row * HD + d * 32 + lane], a[d]);
+    }
+    const float inv = den == 0.f ? 0.f : 1.0f / den;
+    float* o = p.o + (first + i) * p.ld_o + (long long)(s.g * G + row % G) * HD;
+#pragma unroll
+    for (int d = 0; d < HD / 32; ++d) o[d * 32 + lane] = a[d] * inv;
+  }
+}
+
+struct Pick {
+  void (*k)(Params);
+  void (*join)(Params);
+  size_t smem, part;
+};
+template <int HD>
+Pick pick_g(int G) {
+  const size_t smem = Tile<HD>::kSmem + 1024 + sizeof(Small), part = part_floats_of<HD>();
+  switch (G) {
+    case 1: return {k_prompt<HD, 1>, k_join<HD, 1>, smem, part};
+    case 2: return {k_prompt<HD, 2>, k_join<HD, 2>, smem, part};
+    case 4: return {k_prompt<HD, 4>, k_join<HD, 4>, smem, part};
+    case 8: return {k_prompt<HD, 8>, k_join<HD, 8>, smem, part};
+  }
+  return {};
+}
+Pick pick(int hd, int G) {
+  return hd == 64 ? pick_g<64>(G) : hd == 128 ? pick_g<128>(G) : hd == 256 ? pick_g<256>(G) : Pick{};
 }
 
 }  // namespace
 
-size_t prompt_workspace(int, int, int, int, int, int) { return 256; }
-cudaError_t init_prompt() { return cudaSuccess; }
-cudaError_t prompt(const Params& p, int hd, int, cudaStream_t st) {
-  const int G = p.nq / p.nkv;
-  auto k = hd == 64 ? pick<64>(G) : hd == 128 ? pick<128>(G) : pick<256>(G);
-  const long long units = (long long)p.n * p.nkv;
-  k<<<(unsigned)((units + 3) / 4), 128, 4 * G * hd * 4, st>>>(p);
-  return cudaGetLastError();
+// shares of at most 256 CTAs, then two partials of each
+size_t prompt_workspace(int, int, int nq, int nkv, int hd, int nsm) {
+  const int C = nsm < kPromptCtas ? nsm : kPromptCtas;
+  return 8192 + 2 * (size_t)C * pick(hd, nq / nkv).part * 4;
+}
+
+cudaError_t init_prompt() {
+  for (int hd : {64, 128, 256})
+    for (int G : {1, 2, 4, 8}) {
+      const Pick k = pick(hd, G);
+      const cudaError_t e =
+          cudaFuncSetAttribute((const void*)k.k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
+      if (e != cudaSuccess) return e;
+    }
+  return cudaSuccess;
+}
+
+cudaError_t prompt(const Params& p, int hd, int nsm, cudaStream_t st) {
+  const Pick k = pick(hd, p.nq / p.nkv);
+  if (!k.k || p.nb < 1 || p.nb > kMaxB) return cudaErrorInvalidValue;
+  const int C = nsm < kPromptCtas ? nsm : kPromptCtas;
+  cudaError_t e = launch_k(k.k, dim3(C), dim3(kThreads), k.smem, st, false, p);
+  if (e != cudaSuccess || C < 2) return e;
+  return launch_k(k.join, dim3(C - 1, 8), dim3(256), 0, st, false, p);
 }
 
 }  // namespace p8
