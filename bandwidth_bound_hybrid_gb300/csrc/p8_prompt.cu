@@ -18,9 +18,10 @@
 //     back into the scores' columns as the A operand of the second product
 //     (32 scores become 16 columns of w_hi and 16 of w_lo); then the step
 //     before is added, half the elements of a head a thread;
-//   * 4 warps widen the codes: 16 bytes of a row from the page (loads of the
-//     next half step on their way) to fp16 in shared memory, 128-byte swizzle,
-//     K as K-major B operand and V, laid out alike, as MN-major;
+//   * 1 warp looks the pages and scales of a step up and copies its blocks'
+//     codes (each contiguous in its page) to a ring of shared memory in bulk;
+//   * 4 warps widen them to fp16 tiles in shared memory, 128-byte swizzle, K as
+//     K-major B operand and V, laid out alike, as MN-major;
 //   * 1 thread issues tcgen05.mma: S of step k + 1 before O of step k, so that
 //     the row warps' softmax runs beside the tensor cores.
 // Two score and (hd <= 128) two output accumulators in TMEM: 512 columns.
@@ -44,27 +45,35 @@ template <int HD>
 struct Tile {
   static constexpr int BM = 128, BN = HD == 256 ? 64 : 128;
   static constexpr int NBLK = BN / kBlock;        // blocks of a step
-  static constexpr int kStages = HD == 256 ? 1 : 2;
+  static constexpr int NSK = HD == 256 ? 1 : 2;   // widened tiles of K and of V
+  static constexpr int NSV = HD == 64 ? 2 : 1;
   static constexpr int NO = HD == 256 ? 1 : 2;    // output accumulators
   static constexpr int kQ = BM * HD * 2;          // one part of the queries
   static constexpr int kKV = BN * HD * 2;
-  static constexpr int kSmem = 2 * kQ + 2 * kStages * kKV;
-  static constexpr int NP = BN * HD / 16 / 128;   // 16-byte pieces of K or V a widening thread has
+  static constexpr int kSlot = 8192;              // codes of a ring slot
+  static constexpr int kSlots = HD == 256 ? 2 : 6;
+  static constexpr int NS = BN * HD / kSlot;      // slots of a step's K or V
+  static constexpr int SB = NBLK / NS;            // blocks of a slot
+  static constexpr int kSmem = 2 * kQ + (NSK + NSV) * kKV + kSlots * kSlot;
 };
 
-// What the row warps need of a step.
+// What the row and widening warps need of a step.
+constexpr int kSteps = 8;  // of them at a time
 struct Step {
   float fk[8], fv[8];  // scales of K; of V times 2^(14 - E)
   int u[8];            // first positions of the blocks; INT_MAX: not there
+  int kind[8];         // 0: codes in the ring, 1: nothing (zeros), 2: the open block
   float ev;            // 2^(E - 14)
   int edge;            // some row does not see all of it
+  float up[2];         // factors that bring the open block's K and V below 2^7
 };
 
 struct alignas(16) Small {
-  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], ofull[2], oempty[2], mfull[4], qfull, done;
+  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], ofull[2], oempty[2], mfull[kSteps], rfull[6], rempty[6], qfull,
+      done;
   uint32_t tmem;
   int open_nan;
-  Step step[4];
+  Step step[kSteps];
   float qf[128];
   float mx[2][2][128];
   float ls[2][128];
@@ -316,8 +325,8 @@ template <int R>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
-// Registers of a thread by role: 8 x 176 + 4 x 120 + 4 x 40 = 2048, the launch's 16 x 128.
-constexpr int kRowRegs = 176, kWidenRegs = 120, kOtherRegs = 40;
+// Registers of a thread by role: 8 x 184 + 4 x 80 + 4 x 64 = 2048, the launch's 16 x 128.
+constexpr int kRowRegs = 184, kWidenRegs = 80, kOtherRegs = 64;
 static_assert(kRowWarps * kRowRegs + kWidenWarps * kWidenRegs + 4 * kOtherRegs <= kThreads / 32 * 128, "register split");
 
 // A warp's wait; false, with the guard set, if it gave up.
@@ -357,155 +366,193 @@ __device__ __forceinline__ void put16(uint8_t* tile, int r, int c, const uint32_
   }
 }
 
+// Bulk copy to shared memory with the L2's usual policy (a tile's neighbours read the same blocks).
+__device__ __forceinline__ void copy_bulk(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_addr(dst)),
+               "l"(src), "r"(bytes), "r"(smem_addr(bar))
+               : "memory");
+}
+
+// Pages and scales of the steps, and the copies of their codes into the ring (one warp).
 template <int HD, int G>
-__device__ __forceinline__ void widen_role(const Params& p, Small& sm, uint8_t* kbuf, uint8_t* vbuf) {
+__device__ __forceinline__ void load_role(const Params& p, Small& sm, uint8_t* ring) {
   using Ti = Tile<HD>;
-  constexpr int BN = Ti::BN, NBLK = Ti::NBLK, NP = Ti::NP, NC = HD / 16, NST = Ti::kStages;
-  const int wt = threadIdx.x - kRowWarps * 32, lane = threadIdx.x & 31;
+  constexpr int NBLK = Ti::NBLK, SB = Ti::SB, kBytes = kBlock * HD;
+  const int lane = threadIdx.x & 31;
   Piece w;
-  int ks = 0;
-  for (bool more = first_piece<HD, G>(p, sm, w); more; more = next_piece<HD, G>(p, sm, w)) {
+  int ks = 0, slot = 0;
+  uint32_t use = 0;  // times the ring has been gone through
+  bool ok = true;
+  for (bool more = first_piece<HD, G>(p, sm, w); more && ok; more = next_piece<HD, G>(p, sm, w)) {
     const int end = w.T + w.n, ob = end / kBlock;  // the open block, if end % 16
-    const uint16_t* tail = p.c.tail + w.b * p.c.tail_stride + (long long)w.g * kBlock * HD;
-    const long long tail_v = (long long)p.nkv * kBlock * HD;
-    // the open block's exponents: its values below 2^7
-    float osk = 0.f, osv = 0.f, upk = 0.f, upv = 0.f;
+    float os[2] = {0.f, 0.f}, up[2] = {0.f, 0.f};
     if (w.s1 == w.steps && end % kBlock != 0 && w.t1 / kBlock == ob) {
-      uint32_t a[2] = {0, 0};
+      const uint16_t* tail = p.c.tail + w.b * p.c.tail_stride + (long long)w.g * kBlock * HD;
       bool nan = false;
-      for (int i = lane; i < (end % kBlock) * HD / 2; i += 32)
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const uint32_t x = reinterpret_cast<const uint32_t*>(tail + v * tail_v)[i];
+      for (int v = 0; v < 2; ++v) {
+        uint32_t a = 0;
+        for (int i = lane; i < (end % kBlock) * HD / 2; i += 32) {
+          const uint32_t x = reinterpret_cast<const uint32_t*>(tail + (long long)v * p.nkv * kBlock * HD)[i];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t m = (x >> (16 * h)) & 0x7fffu;
             if (m < 0x7f80u)
-              a[v] = max(a[v], m);
+              a = max(a, m);
             else
               nan |= v == 1;
           }
         }
-      a[0] = __reduce_max_sync(0xffffffffu, a[0]);
-      a[1] = __reduce_max_sync(0xffffffffu, a[1]);
-      const int ek = min(6 + 127 - (int)(a[0] >> 7), 100), ev = min(6 + 127 - (int)(a[1] >> 7), 100);
-      upk = pow2(ek);
-      upv = pow2(ev);
-      osk = pow2(-ek);
-      osv = pow2(-ev);
+        a = __reduce_max_sync(0xffffffffu, a);
+        const int e = min(6 + 127 - (int)(a >> 7), 100);
+        up[v] = pow2(e);
+        os[v] = pow2(-e);
+      }
       if (nan) sm.open_nan = 1;
     }
-    // blocks of a step, a lane each: page (-1: none), block within it, scales, first position
+    // blocks of a step, a lane each: where the codes are (-1: nowhere, -2: the tail), first position, scales
     struct Look {
-      int pg, off, u;
+      long long at;
+      int u;
       float ks, vs;
     };
     auto look_up = [&](int s) {
-      Look k = {-1, 0, INT_MAX, 0.f, 0.f};
+      Look k = {-1, INT_MAX, 0.f, 0.f};
       const int i = s * NBLK + lane;
       if (lane < NBLK && i < w.view.n) {
         const int blk = block_at(w.view, i);
         if (blk == ob) {  // (past the closed blocks)
-          k.pg = -2;
-          k.ks = osk;
-          k.vs = osv;
-          k.u = blk * kBlock;
+          k = {-2, blk * kBlock, os[0], os[1]};
         } else {
-          const int at = blk / p.c.bpp;
-          k.off = blk - at * p.c.bpp;
-          k.pg = __ldg(p.c.table + (long long)w.b * p.c.max_pages + at);
-          if ((unsigned)k.pg >= (unsigned)p.c.pool_pages) {
-            if (wt < 32) set_guard(p.guard, kGuardBadIndex);
-            k.pg = -1;
+          const int at = blk / p.c.bpp, off = blk - at * p.c.bpp;
+          const int pg = __ldg(p.c.table + (long long)w.b * p.c.max_pages + at);
+          if ((unsigned)pg >= (unsigned)p.c.pool_pages) {
+            set_guard(p.guard, kGuardBadIndex);
           } else {
-            const long long sc = scale_at(p.c, k.pg, w.g, k.off);
-            k.ks = __ldg(p.c.Ks + sc);
-            k.vs = __ldg(p.c.Vs + sc);
-            k.u = blk * kBlock;
+            const long long sc = scale_at(p.c, pg, w.g, off);
+            k = {code_at(p.c, pg, w.g, off, HD), blk * kBlock, __ldg(p.c.Ks + sc), __ldg(p.c.Vs + sc)};
           }
         }
       }
       return k;
     };
-    // this thread's pieces of a step's K or V (zeros where there is no page)
-    auto load = [&](const Look& k, const int8_t* base, uint4* x) {
-#pragma unroll
-      for (int u = 0; u < NP; ++u) {
-        const int id = u * 128 + wt, r = id / NC;
-        const int pg = __shfl_sync(0xffffffffu, k.pg, r / kBlock), off = __shfl_sync(0xffffffffu, k.off, r / kBlock);
-        x[u] = make_uint4(0, 0, 0, 0);
-        if (pg >= 0)
-          x[u] = __ldg(reinterpret_cast<const uint4*>(base + code_at(p.c, pg, w.g, off, HD) +
-                                                      ((r % kBlock) * NC + id % NC) * 16));
-      }
-    };
-    auto store = [&](const Look& k, const uint4* x, uint8_t* tile, const uint16_t* rows, float up, bool is_v) {
-#pragma unroll
-      for (int u = 0; u < NP; ++u) {
-        const int id = u * 128 + wt, r = id / NC, c = id % NC;
-        const int pg = __shfl_sync(0xffffffffu, k.pg, r / kBlock);
-        uint32_t h[8];
-        if (pg != -2) {
-          widen(x[u].x, h);
-          widen(x[u].y, h + 2);
-          widen(x[u].z, h + 4);
-          widen(x[u].w, h + 6);
-        } else {  // rows of the tail that are there; V's NaN as 0 (its own rows' outputs get them at the end)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint32_t q = 0;
-            if (r % kBlock < end % kBlock) q = reinterpret_cast<const uint32_t*>(rows + (r % kBlock) * HD + c * 16)[i];
-            if (is_v && (q & 0x7f80u) == 0x7f80u) q &= 0xffff0000u;
-            if (is_v && (q & 0x7f800000u) == 0x7f800000u) q &= 0xffffu;
-            h[i] = half2_bits(bf16_lo(q) * up, bf16_hi(q) * up);
+    Look cur = look_up(w.s0), nxt = cur;
+    for (int s = w.s0; s < w.s1 && ok; ++s, ++ks) {
+      nxt = look_up(s + 1);
+      for (int v = 0; v < 2; ++v)
+        for (int i = 0; i < Ti::NS; ++i) {
+          if (ok && use > 0) ok = wait_all(p, &sm.rempty[slot], (use & 1) ^ 1);
+          if (!ok) continue;
+          // The step's scales and kinds, once it has a slot: step ks - 8 has been read.  (The widening warps have left
+          // step ks - 4, so S of ks - 6 is done, and O of ks - 8 was issued before it, after the row warps.)
+          if (v == 0 && i == 0) {
+            Step& m = sm.step[ks % kSteps];
+            const uint32_t vb = cur.u != INT_MAX && cur.vs == cur.vs ? __float_as_uint(cur.vs) : 0u;
+            const uint32_t top = __reduce_max_sync(0xffffffffu, vb);
+            const int E = top ? (int)(top >> 23) - 126 : 0;  // 2^E above the largest
+            bool full = true;
+            if (lane < NBLK) {
+              m.fk[lane] = cur.ks;
+              m.fv[lane] = cur.vs * pow2(14 - E);
+              m.u[lane] = cur.u;
+              m.kind[lane] = cur.at >= 0 ? 0 : (int)-cur.at;
+              full = cur.u != INT_MAX && cur.u + kBlock - 1 <= w.t0 &&
+                     (p.window <= 0 || cur.u > w.t1 - p.window || cur.u + kBlock <= p.sinks);
+            }
+            full = __all_sync(0xffffffffu, full);
+            if (lane == 0) {
+              m.ev = pow2(E - 14);
+              m.edge = !full;
+              m.up[0] = up[0];
+              m.up[1] = up[1];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.mfull[ks % kSteps]);
+          }
+          const bool mine = lane / SB == i && lane < NBLK && cur.at >= 0;
+          const int n = __popc(__ballot_sync(0xffffffffu, mine));
+          if (lane == 0) mbar_arrive_expect_tx(&sm.rfull[slot], n * kBytes);
+          __syncwarp();
+          if (mine)
+            copy_bulk(ring + slot * Ti::kSlot + (lane % SB) * kBytes, (v ? p.c.V : p.c.K) + cur.at, kBytes,
+                      &sm.rfull[slot]);
+          if (++slot == Ti::kSlots) {
+            slot = 0;
+            ++use;
           }
         }
-        put16<BN>(tile, r, c, h);
-      }
-    };
-    Look cur = look_up(w.s0), nxt = cur;
-    uint4 xk[NP], xv[NP];
-    load(cur, p.c.K, xk);
-    for (int s = w.s0; s < w.s1; ++s, ++ks) {
-      const int st = ks % NST;
-      const uint32_t ph = (ks / NST) & 1;
-      load(cur, p.c.V, xv);
-      if (s + 1 < w.s1) nxt = look_up(s + 1);
-      if (ks >= NST && !wait_all(p, &sm.kempty[st], ph ^ 1)) return;
-      // The step's scales and places, by one warp.  Those of step ks - 4 have been read: S of ks - NST is done, so O
-      // of ks - 4 at the latest had been issued before it, which waited for all row warps.
-      if (wt < 32) {
-        Step& m = sm.step[ks & 3];
-        const uint32_t vb = lane < NBLK && cur.u != INT_MAX && cur.vs == cur.vs ? __float_as_uint(cur.vs) : 0u;
-        const uint32_t top = __reduce_max_sync(0xffffffffu, vb);
-        const int E = top ? (int)(top >> 23) - 126 : 0;  // 2^E above the largest
-        bool full = true;
-        if (lane < NBLK) {
-          m.fk[lane] = cur.ks;
-          m.fv[lane] = cur.vs * pow2(14 - E);
-          m.u[lane] = cur.u;
-          full = cur.u != INT_MAX && cur.u + kBlock - 1 <= w.t0 &&
-                 (p.window <= 0 || cur.u > w.t1 - p.window || cur.u + kBlock <= p.sinks);
-        }
-        full = __all_sync(0xffffffffu, full);
-        if (lane == 0) {
-          m.ev = pow2(E - 14);
-          m.edge = !full;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.mfull[ks & 3]);
-      }
-      store(cur, xk, kbuf + st * Ti::kKV, tail, upk, false);
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.kfull[st]);
-      if (s + 1 < w.s1) load(nxt, p.c.K, xk);
-      if (ks >= NST && !wait_all(p, &sm.vempty[st], ph ^ 1)) return;
-      store(cur, xv, vbuf + st * Ti::kKV, tail + tail_v, upv, true);
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.vfull[st]);
       cur = nxt;
+    }
+  }
+  // the CTA must not retire while its copies are in flight: the widening warps have waited for all of them, unless
+  // they gave up
+  for (int i = 0; i < Ti::kSlots; ++i) {
+    const uint32_t n = use + (i < slot);  // times that slot i was filled
+    if (n > 0) wait_all(p, &sm.rfull[i], (n - 1) & 1);
+  }
+}
+
+template <int HD, int G>
+__device__ __forceinline__ void widen_role(const Params& p, Small& sm, const uint8_t* ring, uint8_t* kbuf, uint8_t* vbuf) {
+  using Ti = Tile<HD>;
+  constexpr int BN = Ti::BN, NC = HD / 16, SB = Ti::SB;
+  const int wt = threadIdx.x - kRowWarps * 32, lane = threadIdx.x & 31;
+  Piece w;
+  int ks = 0, slot = 0;
+  uint32_t use = 0;
+  for (bool more = first_piece<HD, G>(p, sm, w); more; more = next_piece<HD, G>(p, sm, w)) {
+    const int open_rows = (w.T + w.n) % kBlock;
+    const uint16_t* tail = p.c.tail + w.b * p.c.tail_stride + (long long)w.g * kBlock * HD;
+    for (int s = w.s0; s < w.s1; ++s, ++ks) {
+      if (!wait_all(p, &sm.mfull[ks % kSteps], (ks / kSteps) & 1)) return;
+      const Step& m = sm.step[ks % kSteps];
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        constexpr int NSK = Ti::NSK, NSV = Ti::NSV;
+        const int n = v ? NSV : NSK, st = ks % n;
+        if (ks >= n && !wait_all(p, v ? &sm.vempty[st] : &sm.kempty[st], ((ks / n) & 1) ^ 1)) return;
+        uint8_t* tile = (v ? vbuf : kbuf) + st * Ti::kKV;
+        for (int i = 0; i < Ti::NS; ++i) {
+          if (!wait_all(p, &sm.rfull[slot], use & 1)) return;
+          const uint8_t* raw = ring + slot * Ti::kSlot;
+          uint4 x[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const uint4*>(raw + (u * 128 + wt) * 16);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int id = u * 128 + wt, r = i * (SB * kBlock) + id / NC, c = id % NC;
+            uint32_t h[8];
+            widen(x[u].x, h);
+            widen(x[u].y, h + 2);
+            widen(x[u].z, h + 4);
+            widen(x[u].w, h + 6);
+            const int kind = m.kind[r / kBlock];
+            if (kind != 0) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {  // rows of the tail that are there; V's NaN as 0 (see the outputs)
+                uint32_t q = 0;
+                if (kind == 2 && r % kBlock < open_rows)
+                  q = reinterpret_cast<const uint32_t*>(tail + (long long)v * p.nkv * kBlock * HD +
+                                                        (r % kBlock) * HD + c * 16)[k];
+                if (v && (q & 0x7f80u) == 0x7f80u) q &= 0xffff0000u;
+                if (v && (q & 0x7f800000u) == 0x7f800000u) q &= 0xffffu;
+                h[k] = half2_bits(bf16_lo(q) * m.up[v], bf16_hi(q) * m.up[v]);
+              }
+            }
+            put16<BN>(tile, r, c, h);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.rempty[slot]);
+          if (++slot == Ti::kSlots) {
+            slot = 0;
+            ++use;
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v ? &sm.vfull[st] : &sm.kfull[st]);
+      }
     }
   }
 }
@@ -514,7 +561,7 @@ __device__ __forceinline__ void widen_role(const Params& p, Small& sm, uint8_t* 
 template <int HD, int G>
 __device__ __forceinline__ void mma_role(const Params& p, Small& sm, uint32_t q, uint32_t kbuf, uint32_t vbuf) {
   using Ti = Tile<HD>;
-  constexpr int BN = Ti::BN, NST = Ti::kStages, NO = Ti::NO;
+  constexpr int BN = Ti::BN, NSK = Ti::NSK, NSV = Ti::NSV, NO = Ti::NO;
   const uint32_t tmem = sm.tmem, out = tmem + 2 * BN;
   constexpr uint32_t id_s = idesc_f16(128, BN, false), id_o = idesc_f16(128, HD, true);
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -529,8 +576,8 @@ __device__ __forceinline__ void mma_role(const Params& p, Small& sm, uint32_t q,
     const int steps = w.s1 - w.s0;
     ok = wait(&sm.qfull, np & 1);
     auto scores = [&](int k) {
-      const int st = k % NST;
-      if (!wait(&sm.kfull[st], (k / NST) & 1)) return false;
+      const int st = k % NSK;
+      if (!wait(&sm.kfull[st], (k / NSK) & 1)) return false;
       tc::fence_after_sync();
       const uint32_t d = tmem + (k & 1) * BN;
       uint64_t a0 = tc::sdesc_k128(q), a1 = tc::sdesc_k128(q + Ti::kQ), b = tc::sdesc_k128(kbuf + st * Ti::kKV);
@@ -548,8 +595,8 @@ __device__ __forceinline__ void mma_role(const Params& p, Small& sm, uint32_t q,
     if (ok) ok = scores(ks);
     for (int s = 0; ok && s < steps; ++s, ++ks) {
       if (s + 1 < steps && !(ok = scores(ks + 1))) break;
-      const int st = ks % NST, ob = ks % NO;
-      ok = wait(&sm.pfull[ks & 1], (ks >> 1) & 1) && wait(&sm.vfull[st], (ks / NST) & 1) &&
+      const int st = ks % NSV, ob = ks % NO;
+      ok = wait(&sm.pfull[ks & 1], (ks >> 1) & 1) && wait(&sm.vfull[st], (ks / NSV) & 1) &&
            (ks < NO || wait(&sm.oempty[ob], ((ks / NO) - 1) & 1));
       if (!ok) break;
       tc::fence_after_sync();
@@ -672,11 +719,17 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
     };
     for (int s = w.s0; s < w.s1; ++s, ++ks) {
       const int buf = ks & 1;
-      wait_row(p, &sm.mfull[ks & 3], (ks >> 2) & 1, ok);
+      wait_row(p, &sm.mfull[ks % kSteps], (ks / kSteps) & 1, ok);
       wait_row(p, &sm.sfull[buf], (ks >> 1) & 1, ok);
       tc::fence_after_sync();
-      const Step& m = sm.step[ks & 3];
-      float v[NV];
+      const Step& m = sm.step[ks % kSteps];
+      float v[NV], f[NV / 16], fv[NV / 16];
+#pragma unroll
+      for (int j = 0; j < NV / 16; ++j) {
+        f[j] = m.fk[half * (NV / 16) + j] * qf;
+        fv[j] = m.fv[half * (NV / 16) + j];
+      }
+      const float step_ev = m.ev;
 #pragma unroll
       for (int c = 0; c < NV; c += 32) tc::tmem_ld32(scores + buf * BN + c, v + c);
       if (m.edge) {
@@ -688,20 +741,26 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
             see = low_mask(t - u + 1);
             if (p.window > 0) see &= ~low_mask(t - p.window - u + 1) | low_mask(p.sinks - u);
           }
+          // A scale of 0 or NaN goes into the scores, so that it does not meet the -infinity of the positions out of
+          // view (a NaN block makes all of a row's outputs NaN, whether it is K's or V's).
+          const float z = f[j] * 0.f + fv[j] * 0.f;  // 0, or NaN
+          const bool odd = z != z || f[j] == 0.f;
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
+          for (int i = 0; i < 16; ++i) {
+            if (odd) v[j * 16 + i] = z;
             if (!(see >> i & 1)) v[j * 16 + i] = -INFINITY;
+          }
+          if (odd) f[j] = 1.f;
+          if (z != z) fv[j] = 0.f;
         }
       }
-      float top = -INFINITY, f[NV / 16];
+      float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < NV / 16; ++j) {
         float b = v[j * 16];
 #pragma unroll
         for (int i = 1; i < 16; ++i) b = fmaxf(b, v[j * 16 + i]);
-        f[j] = m.fk[half * (NV / 16) + j] * qf;
-        // (a block of scale 0 has scores 0, and a row that it is out of view for none)
-        top = fmaxf(top, b == -INFINITY ? b : b * f[j]);
+        top = fmaxf(top, b * f[j]);
       }
       sm.mx[buf][half][row] = top;
       named_barrier(1 + sub, 64);
@@ -718,31 +777,18 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int j = (c + 2 * i) / 16;
-          const float fv = m.fv[half * (NV / 16) + j];
-          float a0, a1;
-          if (m.edge) {
-            a0 = v[c + 2 * i] == -INFINITY ? -INFINITY : fmaf(v[c + 2 * i], f[j], -ref);
-            a1 = v[c + 2 * i + 1] == -INFINITY ? -INFINITY : fmaf(v[c + 2 * i + 1], f[j], -ref);
-          } else {
-            unpack2(fma2(pack2(v[c + 2 * i], v[c + 2 * i + 1]), pack2(f[j], f[j]), nref), a0, a1);
-          }
-          const float p0 = ex2(a0), p1 = ex2(a1);
+          float p0, p1, w0, w1;
+          unpack2(fma2(pack2(v[c + 2 * i], v[c + 2 * i + 1]), pack2(f[j], f[j]), nref), p0, p1);
+          p0 = ex2(p0);
+          p1 = ex2(p1);
           sum2 = add2(sum2, pack2(p0, p1));
-          float w0, w1, l0, l1;
-          unpack2(mul2(pack2(p0, p1), pack2(fv, fv)), w0, w1);
-          if (m.edge) {  // a NaN scale does not reach rows that do not see its block
-            if (v[c + 2 * i] == -INFINITY) w0 = 0.f;
-            if (v[c + 2 * i + 1] == -INFINITY) w1 = 0.f;
-          }
+          unpack2(mul2(pack2(p0, p1), pack2(fv[j], fv[j])), w0, w1);
           const float h0 = trunc11(w0), h1 = trunc11(w1);
-          l0 = w0 - h0;
-          l1 = w1 - h1;
           pr[i] = half2_bits(h0, h1);
-          pr[16 + i] = half2_bits(l0, l1);
+          pr[16 + i] = half2_bits(w0 - h0, w1 - h1);
         }
         tmem_st32(scores + buf * BN + c, pr);
       }
-      const float step_ev = m.ev;
       wait_st();
       tc::fence_before_sync();
       __syncwarp();
@@ -829,7 +875,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
       mbar_init(&sm.ofull[s], 1);
       mbar_init(&sm.oempty[s], kRowWarps);
     }
-    for (int s = 0; s < 4; ++s) mbar_init(&sm.mfull[s], 1);
+    for (int s = 0; s < kSteps; ++s) mbar_init(&sm.mfull[s], 1);
+    for (int s = 0; s < Ti::kSlots; ++s) {
+      mbar_init(&sm.rfull[s], 1);
+      mbar_init(&sm.rempty[s], kWidenWarps);
+    }
     mbar_init(&sm.qfull, kRowWarps);
     mbar_init(&sm.done, 1);
     sm.open_nan = 0;
@@ -841,17 +891,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  uint8_t *q = smem, *kbuf = smem + 2 * Ti::kQ, *vbuf = kbuf + Ti::kStages * Ti::kKV;
+  uint8_t *q = smem, *kbuf = smem + 2 * Ti::kQ, *vbuf = kbuf + Ti::NSK * Ti::kKV, *ring = vbuf + Ti::NSV * Ti::kKV;
   if (warp < kRowWarps) {
     regs_inc<kRowRegs>();
     row_role<HD, G>(p, sm, q, part);
   } else if (warp < kRowWarps + kWidenWarps) {
     regs_dec<kWidenRegs>();
-    widen_role<HD, G>(p, sm, kbuf, vbuf);
+    widen_role<HD, G>(p, sm, ring, kbuf, vbuf);
   } else {
     regs_dec<kOtherRegs>();
     if (warp == kRowWarps + kWidenWarps && (threadIdx.x & 31) == 0)
       mma_role<HD, G>(p, sm, smem_addr(q), smem_addr(kbuf), smem_addr(vbuf));
+    if (warp == kRowWarps + kWidenWarps + 1) load_role<HD, G>(p, sm, ring);
   }
   tc::fence_before_sync();
   __syncthreads();
