@@ -65,6 +65,7 @@ struct Step {
   int kind[8];         // 0: codes in the ring, 1: nothing (zeros), 2: the open block
   float ev;            // 2^(E - 14)
   int edge;            // some row does not see all of it
+  int odd;             // some block is not codes in the ring
   float up[2];         // factors that bring the open block's K and V below 2^7
 };
 
@@ -329,10 +330,26 @@ __device__ __forceinline__ void regs_dec() {
 constexpr int kRowRegs = 184, kWidenRegs = 80, kOtherRegs = 64;
 static_assert(kRowWarps * kRowRegs + kWidenWarps * kWidenRegs + 4 * kOtherRegs <= kThreads / 32 * 128, "register split");
 
+// Bounded wait for the phase of the given parity, in few instructions (the roles share the instruction cache): at
+// most 2^22 tries of up to 2 us.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
+  const uint32_t at = smem_addr(bar);
+#pragma unroll 1
+  for (int i = 0; i < 1 << 22; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(at), "r"(parity)
+        : "memory");
+    if (done) return true;
+  }
+  return false;
+}
 // A warp's wait; false, with the guard set, if it gave up.
 __device__ __forceinline__ bool wait_all(const Params& p, uint64_t* bar, uint32_t parity) {
-  const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
-  if (!ok && (threadIdx.x & 31) == 0) set_guard(p.guard, kGuardWaitTimeout);
+  const bool ok = __all_sync(0xffffffffu, wait_bar(bar, parity));
+  if (!ok) set_guard(p.guard, kGuardWaitTimeout);
   return ok;
 }
 // A row warp's wait.  One that has given up goes on without waiting (its outputs are worthless, the guard says so),
@@ -352,18 +369,13 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t* h) {
   h[0] = *reinterpret_cast<const uint32_t*>(&x);
   h[1] = *reinterpret_cast<const uint32_t*>(&y);
 }
-// 16 elements from 16 c of row r: two 16-byte chunks of a 128-byte row; the chunks of the upper half of a line's
-// pieces in the other order, so that 8 lanes store to 8 different bank groups.
+// 16 elements from 16 c of row r: two 16-byte chunks of a 128-byte row.
 template <int BN>
 __device__ __forceinline__ void put16(uint8_t* tile, int r, int c, const uint32_t* h) {
   uint8_t* row = tile + (c >> 2) * (BN * 128) + r * 128;
-  const int k = (c & 3) * 2, x = (c >> 2) & 1;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int s = i ^ x;
-    *reinterpret_cast<uint4*>(row + (((k + s) ^ (r & 7)) << 4)) =
-        s ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
-  }
+  const int k = (c & 3) * 2;
+  *reinterpret_cast<uint4*>(row + ((k ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+  *reinterpret_cast<uint4*>(row + (((k + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
 // Bulk copy to shared memory with the L2's usual policy (a tile's neighbours read the same blocks).
@@ -437,53 +449,68 @@ __device__ __forceinline__ void load_role(const Params& p, Small& sm, uint8_t* r
       }
       return k;
     };
-    Look cur = look_up(w.s0), nxt = cur;
-    for (int s = w.s0; s < w.s1 && ok; ++s, ++ks) {
-      nxt = look_up(s + 1);
-      for (int v = 0; v < 2; ++v)
-        for (int i = 0; i < Ti::NS; ++i) {
-          if (ok && use > 0) ok = wait_all(p, &sm.rempty[slot], (use & 1) ^ 1);
-          if (!ok) continue;
-          // The step's scales and kinds, once it has a slot: step ks - 8 has been read.  (The widening warps have left
-          // step ks - 4, so S of ks - 6 is done, and O of ks - 8 was issued before it, after the row warps.)
-          if (v == 0 && i == 0) {
-            Step& m = sm.step[ks % kSteps];
-            const uint32_t vb = cur.u != INT_MAX && cur.vs == cur.vs ? __float_as_uint(cur.vs) : 0u;
-            const uint32_t top = __reduce_max_sync(0xffffffffu, vb);
-            const int E = top ? (int)(top >> 23) - 126 : 0;  // 2^E above the largest
-            bool full = true;
-            if (lane < NBLK) {
-              m.fk[lane] = cur.ks;
-              m.fv[lane] = cur.vs * pow2(14 - E);
-              m.u[lane] = cur.u;
-              m.kind[lane] = cur.at >= 0 ? 0 : (int)-cur.at;
-              full = cur.u != INT_MAX && cur.u + kBlock - 1 <= w.t0 &&
-                     (p.window <= 0 || cur.u > w.t1 - p.window || cur.u + kBlock <= p.sinks);
-            }
-            full = __all_sync(0xffffffffu, full);
-            if (lane == 0) {
-              m.ev = pow2(E - 14);
-              m.edge = !full;
-              m.up[0] = up[0];
-              m.up[1] = up[1];
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.mfull[ks % kSteps]);
+    // K of step s, with its scales and kinds, or V
+    auto copy = [&](const Look& k, int v, int step) {
+#pragma unroll 1
+      for (int i = 0; i < Ti::NS; ++i) {
+        if (ok && use > 0) ok = wait_all(p, &sm.rempty[slot], (use & 1) ^ 1);
+        if (!ok) return;
+        // The step's scales and kinds, once it has a slot: step ks - 8 has been read.  (The widening warps have left K
+        // of step ks - 3, so S of ks - 5 is done, and O of ks - 7 was issued before it, after the row warps.)
+        if (v == 0 && i == 0) {
+          Step& m = sm.step[step % kSteps];
+          const uint32_t vb = k.u != INT_MAX && k.vs == k.vs ? __float_as_uint(k.vs) : 0u;
+          const uint32_t top = __reduce_max_sync(0xffffffffu, vb);
+          const int E = top ? (int)(top >> 23) - 126 : 0;  // 2^E above the largest
+          bool full = true, plain = true;
+          if (lane < NBLK) {
+            m.fk[lane] = k.ks;
+            m.fv[lane] = k.vs * pow2(14 - E);
+            m.u[lane] = k.u;
+            m.kind[lane] = k.at >= 0 ? 0 : (int)-k.at;
+            plain = k.at >= 0;
+            full = k.u != INT_MAX && k.u + kBlock - 1 <= w.t0 &&
+                   (p.window <= 0 || k.u > w.t1 - p.window || k.u + kBlock <= p.sinks);
           }
-          const bool mine = lane / SB == i && lane < NBLK && cur.at >= 0;
-          const int n = __popc(__ballot_sync(0xffffffffu, mine));
-          if (lane == 0) mbar_arrive_expect_tx(&sm.rfull[slot], n * kBytes);
+          full = __all_sync(0xffffffffu, full);
+          plain = __all_sync(0xffffffffu, plain);
+          if (lane == 0) {
+            m.ev = pow2(E - 14);
+            m.edge = !full;
+            m.odd = !plain;
+            m.up[0] = up[0];
+            m.up[1] = up[1];
+          }
           __syncwarp();
-          if (mine)
-            copy_bulk(ring + slot * Ti::kSlot + (lane % SB) * kBytes, (v ? p.c.V : p.c.K) + cur.at, kBytes,
-                      &sm.rfull[slot]);
-          if (++slot == Ti::kSlots) {
-            slot = 0;
-            ++use;
-          }
+          if (lane == 0) mbar_arrive(&sm.mfull[step % kSteps]);
         }
-      cur = nxt;
+        const bool mine = lane / SB == i && lane < NBLK && k.at >= 0;
+        const int n = __popc(__ballot_sync(0xffffffffu, mine));
+        if (lane == 0) mbar_arrive_expect_tx(&sm.rfull[slot], n * kBytes);
+        __syncwarp();
+        if (mine)
+          copy_bulk(ring + slot * Ti::kSlot + (lane % SB) * kBytes, (v ? p.c.V : p.c.K) + k.at, kBytes, &sm.rfull[slot]);
+        if (++slot == Ti::kSlots) {
+          slot = 0;
+          ++use;
+        }
+      }
+    };
+    // K a step ahead of V, as the tensor cores take them: K0, K1, V0, K2, V1, ...
+    const int steps = w.s1 - w.s0;
+    Look cur = {}, nxt = {}, after = look_up(w.s0);
+#pragma unroll 1
+    for (int i = 0; i < 2 * steps && ok; ++i) {
+      const int v = i > 0 && (i == 2 * steps - 1 || i % 2 == 0), step = v ? (i - 1) / 2 : (i + 1) / 2;
+      if (!v) {
+        cur = nxt;
+        nxt = after;
+        after = look_up(w.s0 + step + 1);
+      }
+      // (K of step s is nxt; then V of step s - 1 is cur, but for the last V)
+      copy(v && step + 1 < steps ? cur : nxt, v, ks + step);
     }
+    ks += steps;
   }
   // the CTA must not retire while its copies are in flight: the widening warps have waited for all of them, unless
   // they gave up
@@ -498,62 +525,79 @@ __device__ __forceinline__ void widen_role(const Params& p, Small& sm, const uin
   using Ti = Tile<HD>;
   constexpr int BN = Ti::BN, NC = HD / 16, SB = Ti::SB;
   const int wt = threadIdx.x - kRowWarps * 32, lane = threadIdx.x & 31;
+  // This thread's 16-byte pieces of a slot: piece c of row r0 + 2 u kPairs.  A pair of rows is taken by 2 NC threads
+  // so that 8 consecutive ones load from and store to eight bank groups (of two adjacent rows, one stores to the even
+  // chunks of the 128 bytes, the other to the odd ones).
+  const int j = wt % (2 * NC), c = j % NC, r0 = wt / (2 * NC) * 2 + ((j / NC) ^ ((c >> 2) & 1));
+  constexpr int kStep = 128 / NC;  // rows from one of a thread's pieces to the next
   Piece w;
   int ks = 0, slot = 0;
   uint32_t use = 0;
   for (bool more = first_piece<HD, G>(p, sm, w); more; more = next_piece<HD, G>(p, sm, w)) {
     const int open_rows = (w.T + w.n) % kBlock;
     const uint16_t* tail = p.c.tail + w.b * p.c.tail_stride + (long long)w.g * kBlock * HD;
-    for (int s = w.s0; s < w.s1; ++s, ++ks) {
-      if (!wait_all(p, &sm.mfull[ks % kSteps], (ks / kSteps) & 1)) return;
-      const Step& m = sm.step[ks % kSteps];
+    auto tile_of = [&](int v, int step) {
+      constexpr int NSK = Ti::NSK, NSV = Ti::NSV;
+      const int n = v ? NSV : NSK, st = step % n;
+      const Step& m = sm.step[step % kSteps];
+      if (v == 0 && !wait_all(p, &sm.mfull[step % kSteps], (step / kSteps) & 1)) return false;
+      if (step >= n && !wait_all(p, v ? &sm.vempty[st] : &sm.kempty[st], ((step / n) & 1) ^ 1)) return false;
+      uint8_t* tile = (v ? vbuf : kbuf) + st * Ti::kKV;
+#pragma unroll 1
+      for (int i = 0; i < Ti::NS; ++i) {
+        if (!wait_all(p, &sm.rfull[slot], use & 1)) return false;
+        const uint8_t* raw = ring + slot * Ti::kSlot + r0 * HD + c * 16;
+        uint4 x[4];
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        constexpr int NSK = Ti::NSK, NSV = Ti::NSV;
-        const int n = v ? NSV : NSK, st = ks % n;
-        if (ks >= n && !wait_all(p, v ? &sm.vempty[st] : &sm.kempty[st], ((ks / n) & 1) ^ 1)) return;
-        uint8_t* tile = (v ? vbuf : kbuf) + st * Ti::kKV;
-        for (int i = 0; i < Ti::NS; ++i) {
-          if (!wait_all(p, &sm.rfull[slot], use & 1)) return;
-          const uint8_t* raw = ring + slot * Ti::kSlot;
-          uint4 x[4];
+        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const uint4*>(raw + u * kStep * HD);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const uint4*>(raw + (u * 128 + wt) * 16);
-#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t h[8];
+          widen(x[u].x, h);
+          widen(x[u].y, h + 2);
+          widen(x[u].z, h + 4);
+          widen(x[u].w, h + 6);
+          put16<BN>(tile, i * (SB * kBlock) + r0 + u * kStep, c, h);
+        }
+        if (m.odd) {
+#pragma unroll 1
           for (int u = 0; u < 4; ++u) {
-            const int id = u * 128 + wt, r = i * (SB * kBlock) + id / NC, c = id % NC;
+            const int r = i * (SB * kBlock) + r0 + u * kStep, kind = m.kind[r / kBlock];
+            if (kind == 0) continue;
             uint32_t h[8];
-            widen(x[u].x, h);
-            widen(x[u].y, h + 2);
-            widen(x[u].z, h + 4);
-            widen(x[u].w, h + 6);
-            const int kind = m.kind[r / kBlock];
-            if (kind != 0) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {  // rows of the tail that are there; V's NaN as 0 (see the outputs)
-                uint32_t q = 0;
-                if (kind == 2 && r % kBlock < open_rows)
-                  q = reinterpret_cast<const uint32_t*>(tail + (long long)v * p.nkv * kBlock * HD +
-                                                        (r % kBlock) * HD + c * 16)[k];
-                if (v && (q & 0x7f80u) == 0x7f80u) q &= 0xffff0000u;
-                if (v && (q & 0x7f800000u) == 0x7f800000u) q &= 0xffffu;
-                h[k] = half2_bits(bf16_lo(q) * m.up[v], bf16_hi(q) * m.up[v]);
-              }
+            for (int k = 0; k < 8; ++k) {  // rows of the tail that are there; V's NaN as 0 (see the outputs)
+              uint32_t q = 0;
+              if (kind == 2 && r % kBlock < open_rows)
+                q = reinterpret_cast<const uint32_t*>(tail + (long long)v * p.nkv * kBlock * HD + (r % kBlock) * HD +
+                                                      c * 16)[k];
+              if (v && (q & 0x7f80u) == 0x7f80u) q &= 0xffff0000u;
+              if (v && (q & 0x7f800000u) == 0x7f800000u) q &= 0xffffu;
+              h[k] = half2_bits(bf16_lo(q) * m.up[v], bf16_hi(q) * m.up[v]);
             }
             put16<BN>(tile, r, c, h);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.rempty[slot]);
-          if (++slot == Ti::kSlots) {
-            slot = 0;
-            ++use;
-          }
         }
-        fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(v ? &sm.vfull[st] : &sm.kfull[st]);
+        if (lane == 0) mbar_arrive(&sm.rempty[slot]);
+        if (++slot == Ti::kSlots) {
+          slot = 0;
+          ++use;
+        }
       }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v ? &sm.vfull[st] : &sm.kfull[st]);
+      return true;
+    };
+    // K a step ahead of V: K0, K1, V0, K2, V1, ...
+    const int steps = w.s1 - w.s0;
+#pragma unroll 1
+    for (int i = 0; i < 2 * steps; ++i) {
+      const int v = i > 0 && (i == 2 * steps - 1 || i % 2 == 0), step = v ? (i - 1) / 2 : (i + 1) / 2;
+      if (!tile_of(v, ks + step)) return;
     }
+    ks += steps;
   }
 }
 
@@ -565,7 +609,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Small& sm, uint32_t q,
   const uint32_t tmem = sm.tmem, out = tmem + 2 * BN;
   constexpr uint32_t id_s = idesc_f16(128, BN, false), id_o = idesc_f16(128, HD, true);
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    const bool ok = mbar_wait(bar, parity);
+    const bool ok = wait_bar(bar, parity);
     if (!ok) set_guard(p.guard, kGuardWaitTimeout);
     return ok;
   };
@@ -581,12 +625,16 @@ __device__ __forceinline__ void mma_role(const Params& p, Small& sm, uint32_t q,
       tc::fence_after_sync();
       const uint32_t d = tmem + (k & 1) * BN;
       uint64_t a0 = tc::sdesc_k128(q), a1 = tc::sdesc_k128(q + Ti::kQ), b = tc::sdesc_k128(kbuf + st * Ti::kKV);
-      asm volatile("" : "+l"(a0), "+l"(a1), "+l"(b));  // (descriptors of the loop made here, not kept over the steps)
+#pragma unroll 1
+      for (int c = 0; c < HD / 64; ++c) {  // (addresses in 16-byte units; they stay below the field's 2^14)
 #pragma unroll
-      for (int c = 0; c < HD / 16; ++c) {  // (addresses in 16-byte units; they stay below the field's 2^14)
-        const int at = ((c >> 2) * (128 * 128) + (c & 3) * 32) >> 4, bt = ((c >> 2) * (BN * 128) + (c & 3) * 32) >> 4;
-        tc::mma_bf16(d, a0 + at, b + bt, id_s, c > 0);
-        tc::mma_bf16(d, a1 + at, b + bt, id_s, true);
+        for (int k = 0; k < 4; ++k) {
+          tc::mma_bf16(d, a0 + k * 2, b + k * 2, id_s, c + k > 0);
+          tc::mma_bf16(d, a1 + k * 2, b + k * 2, id_s, true);
+        }
+        a0 += 128 * 128 / 16;
+        a1 += 128 * 128 / 16;
+        b += BN * 128 / 16;
       }
       tc::mma_commit(&sm.kempty[st]);
       tc::mma_commit(&sm.sfull[k & 1]);
@@ -602,12 +650,13 @@ __device__ __forceinline__ void mma_role(const Params& p, Small& sm, uint32_t q,
       tc::fence_after_sync();
       const uint32_t d = out + ob * HD, a = tmem + (ks & 1) * BN;
       uint64_t b = sdesc_mn128(vbuf + st * Ti::kKV, BN * 128);
-      asm volatile("" : "+l"(b));
-#pragma unroll
-      for (int c = 0; c < BN / 16; ++c) {
-        const uint32_t hi = a + (c >> 1) * 32 + (c & 1) * 8;
-        mma_ts(d, hi, b + c * (2048 >> 4), id_o, c > 0);
-        mma_ts(d, hi + 16, b + c * (2048 >> 4), id_o, true);
+#pragma unroll 1
+      for (int c = 0; c < BN / 32; ++c) {
+        mma_ts(d, a + c * 32, b, id_o, c > 0);
+        mma_ts(d, a + c * 32 + 16, b, id_o, true);
+        mma_ts(d, a + c * 32 + 8, b + 2048 / 16, id_o, true);
+        mma_ts(d, a + c * 32 + 24, b + 2048 / 16, id_o, true);
+        b += 4096 / 16;
       }
       tc::mma_commit(&sm.vempty[st]);
       tc::mma_commit(&sm.ofull[ob]);
@@ -639,6 +688,7 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
     // ------------------------------------------------ queries: warp `warp` rows 16 warp ..
     // normalised by 2^e with 2^e max |q| in [2^9, 2^10): as two fp16 parts q keeps 22 bits of the row's largest
     constexpr int PP = HD / 64;  // pairs of a lane
+#pragma unroll 1
     for (int m0 = warp * 16; m0 < warp * 16 + 16; m0 += 4) {
       float x[4][PP][2];
       float2 cs[4][PP];
@@ -723,44 +773,60 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
       wait_row(p, &sm.sfull[buf], (ks >> 1) & 1, ok);
       tc::fence_after_sync();
       const Step& m = sm.step[ks % kSteps];
-      float v[NV], f[NV / 16], fv[NV / 16];
-#pragma unroll
-      for (int j = 0; j < NV / 16; ++j) {
-        f[j] = m.fk[half * (NV / 16) + j] * qf;
-        fv[j] = m.fv[half * (NV / 16) + j];
-      }
-      const float step_ev = m.ev;
-#pragma unroll
-      for (int c = 0; c < NV; c += 32) tc::tmem_ld32(scores + buf * BN + c, v + c);
-      if (m.edge) {
-#pragma unroll
-        for (int j = 0; j < NV / 16; ++j) {
-          const int u = m.u[half * (NV / 16) + j];
-          uint32_t see = 0;
-          if (u != INT_MAX) {
-            see = low_mask(t - u + 1);
-            if (p.window > 0) see &= ~low_mask(t - p.window - u + 1) | low_mask(p.sinks - u);
-          }
-          // A scale of 0 or NaN goes into the scores, so that it does not meet the -infinity of the positions out of
-          // view (a NaN block makes all of a row's outputs NaN, whether it is K's or V's).
-          const float z = f[j] * 0.f + fv[j] * 0.f;  // 0, or NaN
-          const bool odd = z != z || f[j] == 0.f;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (odd) v[j * 16 + i] = z;
-            if (!(see >> i & 1)) v[j * 16 + i] = -INFINITY;
-          }
-          if (odd) f[j] = 1.f;
-          if (z != z) fv[j] = 0.f;
+      const int j0 = half * (NV / 16);  // the thread's first block
+      const int edge = m.edge;
+      // A block's factors.  In a step that some row does not see all of, a scale of 0 or NaN goes into the scores, so
+      // that it does not meet the -infinity of the positions out of view (a NaN block makes all of a row's outputs NaN,
+      // whether it is K's or V's).
+      auto factors = [&](int j, float& f, float& fv) {
+        f = m.fk[j0 + j] * qf;
+        fv = m.fv[j0 + j];
+        const float z = f * 0.f + fv * 0.f;  // 0, or NaN
+        if (edge && z != z) fv = 0.f;
+        if (edge && !(z == z && f != 0.f)) {
+          f = 1.f;
+          return z;
         }
-      }
+        return 1.f;
+      };
+      // the maximum, 32 scores at a time (loops, not unrolled over the step: the roles share the instruction cache)
       float top = -INFINITY;
+#pragma unroll 1
+      for (int c = 0; c < NV; c += 32) {
+        float v[32];
+        tc::tmem_ld32(scores + buf * BN + c, v);
+        float f[2], fv[2];
+        const float z0 = factors(c / 16, f[0], fv[0]), z1 = factors(c / 16 + 1, f[1], fv[1]);
+        if (edge) {
+          uint32_t bits = 0;
 #pragma unroll
-      for (int j = 0; j < NV / 16; ++j) {
-        float b = v[j * 16];
+          for (int h = 0; h < 2; ++h) {
+            const int u = m.u[j0 + c / 16 + h];
+            uint32_t see = 0;
+            if (u != INT_MAX) {
+              see = low_mask(t - u + 1);
+              if (p.window > 0) see &= ~low_mask(t - p.window - u + 1) | low_mask(p.sinks - u);
+            }
+            bits |= see << (16 * h);
+          }
+          uint32_t w[32];
 #pragma unroll
-        for (int i = 1; i < 16; ++i) b = fmaxf(b, v[j * 16 + i]);
-        top = fmaxf(top, b * f[j]);
+          for (int i = 0; i < 32; ++i) {
+            const float z = i < 16 ? z0 : z1;
+            if (z != 1.f) v[i] = z;
+            if (!(bits >> i & 1)) v[i] = -INFINITY;
+            w[i] = __float_as_uint(v[i]);
+          }
+          tmem_st32(scores + buf * BN + c, w);
+          wait_st();
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float b = v[h * 16];
+#pragma unroll
+          for (int i = 1; i < 16; ++i) b = fmaxf(b, v[h * 16 + i]);
+          top = fmaxf(top, b * f[h]);
+        }
       }
       sm.mx[buf][half][row] = top;
       named_barrier(1 + sub, 64);
@@ -771,24 +837,30 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
       // weights, their sum and their two parts
       uint64_t sum2 = 0;
       const uint64_t nref = pack2(-ref, -ref);
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < NV; c += 32) {
+        float v[32];
+        tc::tmem_ld32(scores + buf * BN + c, v);
+        float f[2], fv[2];
+        factors(c / 16, f[0], fv[0]);
+        factors(c / 16 + 1, f[1], fv[1]);
         uint32_t pr[32];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int j = (c + 2 * i) / 16;
+          const int h = i / 8;
           float p0, p1, w0, w1;
-          unpack2(fma2(pack2(v[c + 2 * i], v[c + 2 * i + 1]), pack2(f[j], f[j]), nref), p0, p1);
+          unpack2(fma2(pack2(v[2 * i], v[2 * i + 1]), pack2(f[h], f[h]), nref), p0, p1);
           p0 = ex2(p0);
           p1 = ex2(p1);
           sum2 = add2(sum2, pack2(p0, p1));
-          unpack2(mul2(pack2(p0, p1), pack2(fv[j], fv[j])), w0, w1);
+          unpack2(mul2(pack2(p0, p1), pack2(fv[h], fv[h])), w0, w1);
           const float h0 = trunc11(w0), h1 = trunc11(w1);
           pr[i] = half2_bits(h0, h1);
           pr[16 + i] = half2_bits(w0 - h0, w1 - h1);
         }
         tmem_st32(scores + buf * BN + c, pr);
       }
+      const float step_ev = m.ev;
       wait_st();
       tc::fence_before_sync();
       __syncwarp();
@@ -838,12 +910,6 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
         unpack2(acc[2 * i + 1], r[2], r[3]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) r[k] *= inv;
-        if (see)
-          for (int m = 0; m < kBlock; ++m)
-            if (see >> m & 1)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if ((tv[m * HD + i * 4 + k] & 0x7f80u) == 0x7f80u) r[k] = __uint_as_float(0x7fc00000u);
         if (vec) {
           reinterpret_cast<float4*>(o)[i] = make_float4(r[0], r[1], r[2], r[3]);
         } else {
@@ -851,6 +917,11 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
           for (int k = 0; k < 4; ++k) o[i * 4 + k] = r[k];
         }
       }
+#pragma unroll 1
+      for (int m = 0; see >> m; ++m)
+#pragma unroll 1
+        for (int i = 0; i < NA; ++i)
+          if ((see >> m & 1) && (tv[m * HD + i] & 0x7f80u) == 0x7f80u) o[i] = __uint_as_float(0x7fc00000u);
     }
   }
 }
