@@ -18,8 +18,9 @@
 //     back into the scores' columns as the A operand of the second product
 //     (32 scores become 16 columns of w_hi and 16 of w_lo); then the step
 //     before is added, half the elements of a head a thread;
-//   * 1 warp looks the pages and scales of a step up and copies its blocks'
-//     codes (each contiguous in its page) to a ring of shared memory in bulk;
+//   * 1 warp copies the codes of a step's blocks (each contiguous in its page,
+//     adjacent ones together) to a ring of shared memory in bulk, another
+//     fetches their scales;
 //   * 4 warps widen them to fp16 tiles in shared memory, 128-byte swizzle, K as
 //     K-major B operand and V, laid out alike, as MN-major;
 //   * 1 thread issues tcgen05.mma: S of step k + 1 before O of step k, so that
@@ -52,6 +53,7 @@ struct Tile {
   static constexpr int kKV = BN * HD * 2;
   static constexpr int kSlot = 8192;              // codes of a ring slot
   static constexpr int kSlots = HD == 256 ? 2 : 6;
+  static constexpr int NP = kSlot / 16 / 128;     // 16-byte pieces of a slot that a widening thread has
   static constexpr int NS = BN * HD / kSlot;      // slots of a step's K or V
   static constexpr int SB = NBLK / NS;            // blocks of a slot
   static constexpr int kSmem = 2 * kQ + (NSK + NSV) * kKV + kSlots * kSlot;
@@ -65,14 +67,14 @@ struct Step {
   int kind[8];         // 0: codes in the ring, 1: nothing (zeros), 2: the open block
   float ev;            // 2^(E - 14)
   int edge;            // some row does not see all of it
-  int odd;             // some block is not codes in the ring
   float up[2];         // factors that bring the open block's K and V below 2^7
 };
 
 struct alignas(16) Small {
-  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], ofull[2], oempty[2], mfull[kSteps], rfull[6], rempty[6], qfull,
-      done;
+  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], ofull[2], oempty[2], mfull[kSteps], mempty[kSteps], rfull[6],
+      rempty[6], qfull, done;
   uint32_t tmem;
+  int odd[6];  // of a ring slot: some block's codes are not there
   int open_nan;
   Step step[kSteps];
   float qf[128];
@@ -346,9 +348,12 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
   }
   return false;
 }
-// A warp's wait; false, with the guard set, if it gave up.
+// A warp's wait, by one lane (32 lanes' tries of one barrier take 400 cycles); false, with the guard set, if it gave up.
 __device__ __forceinline__ bool wait_all(const Params& p, uint64_t* bar, uint32_t parity) {
-  const bool ok = __all_sync(0xffffffffu, wait_bar(bar, parity));
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = wait_bar(bar, parity);
+  ok = __all_sync(0xffffffffu, ok);
+  __syncwarp();
   if (!ok) set_guard(p.guard, kGuardWaitTimeout);
   return ok;
 }
@@ -386,17 +391,93 @@ __device__ __forceinline__ void copy_bulk(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// Pages and scales of the steps, and the copies of their codes into the ring (one warp).
+// Order in which the tensor cores take K and V of a piece's steps, K a step ahead: K0, K1, V0, K2, V1, ...
+__device__ __forceinline__ bool is_v(int i, int steps) { return i > 0 && (i == 2 * steps - 1 || i % 2 == 0); }
+
+// The copies of the codes into the ring (one warp; lane b the step's block b).  Adjacent blocks of a page are one copy.
 template <int HD, int G>
 __device__ __forceinline__ void load_role(const Params& p, Small& sm, uint8_t* ring) {
   using Ti = Tile<HD>;
   constexpr int NBLK = Ti::NBLK, SB = Ti::SB, kBytes = kBlock * HD;
   const int lane = threadIdx.x & 31;
   Piece w;
-  int ks = 0, slot = 0;
+  int slot = 0;
   uint32_t use = 0;  // times the ring has been gone through
   bool ok = true;
   for (bool more = first_piece<HD, G>(p, sm, w); more && ok; more = next_piece<HD, G>(p, sm, w)) {
+    const int ob = (w.T + w.n) / kBlock, steps = w.s1 - w.s0;
+    const int* table = p.c.table + (long long)w.b * p.c.max_pages;
+    // a block's page and place there are looked up a step before they become an address
+    int pg = -1, off = 0;
+    auto look_up = [&](int s) {
+      const int i = s * NBLK + lane;
+      pg = -1;
+      if (lane < NBLK && i < w.view.n) {
+        const int blk = block_at(w.view, i), at = blk / p.c.bpp;
+        off = blk - at * p.c.bpp;
+        if (blk != ob) pg = __ldg(table + at);  // (the open block is past the closed ones)
+      }
+    };
+    auto address = [&]() {
+      return (unsigned)pg < (unsigned)p.c.pool_pages ? code_at(p.c, pg, w.g, off, HD) : -1;
+    };
+    look_up(w.s0);
+    long long cur = -1, nxt = -1, next2 = address();
+    look_up(w.s0 + 1);
+#pragma unroll 1
+    for (int i = 0; i < 2 * steps && ok; ++i) {
+      const bool v = is_v(i, steps);
+      if (!v) {
+        cur = nxt;
+        nxt = next2;
+        next2 = address();
+        look_up(w.s0 + (i + 1) / 2 + 2);
+      }
+      // (K of step s is nxt; then V of step s - 1 is cur, but for the last V)
+      const long long at = v && i != 2 * steps - 1 ? cur : nxt;
+      const int8_t* base = v ? p.c.V : p.c.K;
+#pragma unroll 1
+      for (int j = 0; j < Ti::NS; ++j) {
+        const bool mine = lane / SB == j && at >= 0;
+        const unsigned all = __ballot_sync(0xffffffffu, mine);
+        const long long before = __shfl_up_sync(0xffffffffu, at, 1);
+        const bool starts = mine && (lane % SB == 0 || before < 0 || at != before + kBytes);
+        const unsigned heads = __ballot_sync(0xffffffffu, starts);
+        // blocks from a start to the next start or gap
+        const unsigned stop = (heads | ~all) & (lane < 31 ? ~0u << (lane + 1) : 0u);
+        const int n = __ffs(stop) - 1 - lane;
+        if (use > 0) ok = wait_all(p, &sm.rempty[slot], (use & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) {
+          sm.odd[slot] = __popc(all) != SB;
+          mbar_arrive_expect_tx(&sm.rfull[slot], __popc(all) * kBytes);
+        }
+        __syncwarp();
+        if (starts) copy_bulk(ring + slot * Ti::kSlot + (lane % SB) * kBytes, base + at, n * kBytes, &sm.rfull[slot]);
+        if (++slot == Ti::kSlots) {
+          slot = 0;
+          ++use;
+        }
+      }
+    }
+  }
+  // the CTA must not retire while its copies are in flight: the widening warps have waited for all of them, unless
+  // they gave up
+  for (int i = 0; i < Ti::kSlots; ++i) {
+    const uint32_t n = use + (i < slot);  // times that slot i was filled
+    if (n > 0) wait_all(p, &sm.rfull[i], (n - 1) & 1);
+  }
+}
+
+// The steps' scales and what is special about them (one warp; lane b the step's block b).
+template <int HD, int G>
+__device__ __forceinline__ void scale_role(const Params& p, Small& sm) {
+  using Ti = Tile<HD>;
+  constexpr int NBLK = Ti::NBLK;
+  const int lane = threadIdx.x & 31;
+  Piece w;
+  int ks = 0;
+  for (bool more = first_piece<HD, G>(p, sm, w); more; more = next_piece<HD, G>(p, sm, w)) {
     const int end = w.T + w.n, ob = end / kBlock;  // the open block, if end % 16
     float os[2] = {0.f, 0.f}, up[2] = {0.f, 0.f};
     if (w.s1 == w.steps && end % kBlock != 0 && w.t1 / kBlock == ob) {
@@ -405,6 +486,7 @@ __device__ __forceinline__ void load_role(const Params& p, Small& sm, uint8_t* r
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         uint32_t a = 0;
+#pragma unroll 1
         for (int i = lane; i < (end % kBlock) * HD / 2; i += 32) {
           const uint32_t x = reinterpret_cast<const uint32_t*>(tail + (long long)v * p.nkv * kBlock * HD)[i];
 #pragma unroll
@@ -423,100 +505,55 @@ __device__ __forceinline__ void load_role(const Params& p, Small& sm, uint8_t* r
       }
       if (nan) sm.open_nan = 1;
     }
-    // blocks of a step, a lane each: where the codes are (-1: nowhere, -2: the tail), first position, scales
-    struct Look {
-      long long at;
-      int u;
-      float ks, vs;
-    };
-    auto look_up = [&](int s) {
-      Look k = {-1, INT_MAX, 0.f, 0.f};
+    const int* table = p.c.table + (long long)w.b * p.c.max_pages;
+#pragma unroll 1
+    for (int s = w.s0; s < w.s1; ++s, ++ks) {
+      int u = INT_MAX, kind = 1;
+      float fk = 0.f, fv = 0.f;
       const int i = s * NBLK + lane;
       if (lane < NBLK && i < w.view.n) {
-        const int blk = block_at(w.view, i);
-        if (blk == ob) {  // (past the closed blocks)
-          k = {-2, blk * kBlock, os[0], os[1]};
+        const int blk = block_at(w.view, i), at = blk / p.c.bpp, off = blk - at * p.c.bpp;
+        if (blk == ob) {
+          u = blk * kBlock;
+          kind = 2;
+          fk = os[0];
+          fv = os[1];
         } else {
-          const int at = blk / p.c.bpp, off = blk - at * p.c.bpp;
-          const int pg = __ldg(p.c.table + (long long)w.b * p.c.max_pages + at);
-          if ((unsigned)pg >= (unsigned)p.c.pool_pages) {
-            set_guard(p.guard, kGuardBadIndex);
-          } else {
+          const int pg = __ldg(table + at);
+          if ((unsigned)pg < (unsigned)p.c.pool_pages) {
             const long long sc = scale_at(p.c, pg, w.g, off);
-            k = {code_at(p.c, pg, w.g, off, HD), blk * kBlock, __ldg(p.c.Ks + sc), __ldg(p.c.Vs + sc)};
+            fk = __ldg(p.c.Ks + sc);
+            fv = __ldg(p.c.Vs + sc);
+            u = blk * kBlock;
+            kind = 0;
+          } else {
+            set_guard(p.guard, kGuardBadIndex);
           }
         }
       }
-      return k;
-    };
-    // K of step s, with its scales and kinds, or V
-    auto copy = [&](const Look& k, int v, int step) {
-#pragma unroll 1
-      for (int i = 0; i < Ti::NS; ++i) {
-        if (ok && use > 0) ok = wait_all(p, &sm.rempty[slot], (use & 1) ^ 1);
-        if (!ok) return;
-        // The step's scales and kinds, once it has a slot: step ks - 8 has been read.  (The widening warps have left K
-        // of step ks - 3, so S of ks - 5 is done, and O of ks - 7 was issued before it, after the row warps.)
-        if (v == 0 && i == 0) {
-          Step& m = sm.step[step % kSteps];
-          const uint32_t vb = k.u != INT_MAX && k.vs == k.vs ? __float_as_uint(k.vs) : 0u;
-          const uint32_t top = __reduce_max_sync(0xffffffffu, vb);
-          const int E = top ? (int)(top >> 23) - 126 : 0;  // 2^E above the largest
-          bool full = true, plain = true;
-          if (lane < NBLK) {
-            m.fk[lane] = k.ks;
-            m.fv[lane] = k.vs * pow2(14 - E);
-            m.u[lane] = k.u;
-            m.kind[lane] = k.at >= 0 ? 0 : (int)-k.at;
-            plain = k.at >= 0;
-            full = k.u != INT_MAX && k.u + kBlock - 1 <= w.t0 &&
-                   (p.window <= 0 || k.u > w.t1 - p.window || k.u + kBlock <= p.sinks);
-          }
-          full = __all_sync(0xffffffffu, full);
-          plain = __all_sync(0xffffffffu, plain);
-          if (lane == 0) {
-            m.ev = pow2(E - 14);
-            m.edge = !full;
-            m.odd = !plain;
-            m.up[0] = up[0];
-            m.up[1] = up[1];
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.mfull[step % kSteps]);
-        }
-        const bool mine = lane / SB == i && lane < NBLK && k.at >= 0;
-        const int n = __popc(__ballot_sync(0xffffffffu, mine));
-        if (lane == 0) mbar_arrive_expect_tx(&sm.rfull[slot], n * kBytes);
-        __syncwarp();
-        if (mine)
-          copy_bulk(ring + slot * Ti::kSlot + (lane % SB) * kBytes, (v ? p.c.V : p.c.K) + k.at, kBytes, &sm.rfull[slot]);
-        if (++slot == Ti::kSlots) {
-          slot = 0;
-          ++use;
-        }
+      const uint32_t top = __reduce_max_sync(0xffffffffu, fv == fv ? __float_as_uint(fv) : 0u);
+      const int E = top ? (int)(top >> 23) - 126 : 0;  // 2^E above the largest
+      const bool full = lane >= NBLK || (u != INT_MAX && u + kBlock - 1 <= w.t0 &&
+                                         (p.window <= 0 || u > w.t1 - p.window || u + kBlock <= p.sinks));
+      const bool edge = !__all_sync(0xffffffffu, full);
+      const int sl = ks % kSteps;
+      if (ks >= kSteps && !wait_all(p, &sm.mempty[sl], ((ks / kSteps) & 1) ^ 1)) return;
+      Step& m = sm.step[sl];
+      if (lane < NBLK) {
+        m.fk[lane] = fk;
+        m.fv[lane] = fv * pow2(14 - E);
+        m.u[lane] = u;
+        m.kind[lane] = kind;
       }
-    };
-    // K a step ahead of V, as the tensor cores take them: K0, K1, V0, K2, V1, ...
-    const int steps = w.s1 - w.s0;
-    Look cur = {}, nxt = {}, after = look_up(w.s0);
-#pragma unroll 1
-    for (int i = 0; i < 2 * steps && ok; ++i) {
-      const int v = i > 0 && (i == 2 * steps - 1 || i % 2 == 0), step = v ? (i - 1) / 2 : (i + 1) / 2;
-      if (!v) {
-        cur = nxt;
-        nxt = after;
-        after = look_up(w.s0 + step + 1);
+      if (lane == 0) {
+        m.ev = pow2(E - 14);
+        m.edge = edge;
+        m.up[0] = up[0];
+        m.up[1] = up[1];
       }
-      // (K of step s is nxt; then V of step s - 1 is cur, but for the last V)
-      copy(v && step + 1 < steps ? cur : nxt, v, ks + step);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.mfull[sl]);
     }
-    ks += steps;
-  }
-  // the CTA must not retire while its copies are in flight: the widening warps have waited for all of them, unless
-  // they gave up
-  for (int i = 0; i < Ti::kSlots; ++i) {
-    const uint32_t n = use + (i < slot);  // times that slot i was filled
-    if (n > 0) wait_all(p, &sm.rfull[i], (n - 1) & 1);
   }
 }
 
@@ -539,19 +576,18 @@ __device__ __forceinline__ void widen_role(const Params& p, Small& sm, const uin
     auto tile_of = [&](int v, int step) {
       constexpr int NSK = Ti::NSK, NSV = Ti::NSV;
       const int n = v ? NSV : NSK, st = step % n;
-      const Step& m = sm.step[step % kSteps];
-      if (v == 0 && !wait_all(p, &sm.mfull[step % kSteps], (step / kSteps) & 1)) return false;
       if (step >= n && !wait_all(p, v ? &sm.vempty[st] : &sm.kempty[st], ((step / n) & 1) ^ 1)) return false;
       uint8_t* tile = (v ? vbuf : kbuf) + st * Ti::kKV;
 #pragma unroll 1
       for (int i = 0; i < Ti::NS; ++i) {
         if (!wait_all(p, &sm.rfull[slot], use & 1)) return false;
         const uint8_t* raw = ring + slot * Ti::kSlot + r0 * HD + c * 16;
-        uint4 x[4];
+        const int odd = sm.odd[slot];
+        uint4 x[Ti::NP];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const uint4*>(raw + u * kStep * HD);
+        for (int u = 0; u < Ti::NP; ++u) x[u] = *reinterpret_cast<const uint4*>(raw + u * kStep * HD);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < Ti::NP; ++u) {
           uint32_t h[8];
           widen(x[u].x, h);
           widen(x[u].y, h + 2);
@@ -559,9 +595,11 @@ __device__ __forceinline__ void widen_role(const Params& p, Small& sm, const uin
           widen(x[u].w, h + 6);
           put16<BN>(tile, i * (SB * kBlock) + r0 + u * kStep, c, h);
         }
-        if (m.odd) {
+        if (odd) {
+          if (!wait_all(p, &sm.mfull[step % kSteps], (step / kSteps) & 1)) return false;
+          const Step& m = sm.step[step % kSteps];
 #pragma unroll 1
-          for (int u = 0; u < 4; ++u) {
+          for (int u = 0; u < Ti::NP; ++u) {
             const int r = i * (SB * kBlock) + r0 + u * kStep, kind = m.kind[r / kBlock];
             if (kind == 0) continue;
             uint32_t h[8];
@@ -590,12 +628,11 @@ __device__ __forceinline__ void widen_role(const Params& p, Small& sm, const uin
       if (lane == 0) mbar_arrive(v ? &sm.vfull[st] : &sm.kfull[st]);
       return true;
     };
-    // K a step ahead of V: K0, K1, V0, K2, V1, ...
     const int steps = w.s1 - w.s0;
 #pragma unroll 1
     for (int i = 0; i < 2 * steps; ++i) {
-      const int v = i > 0 && (i == 2 * steps - 1 || i % 2 == 0), step = v ? (i - 1) / 2 : (i + 1) / 2;
-      if (!tile_of(v, ks + step)) return;
+      const int v = is_v(i, steps);
+      if (!tile_of(v, ks + (v ? (i - 1) / 2 : (i + 1) / 2))) return;
     }
     ks += steps;
   }
@@ -660,6 +697,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Small& sm, uint32_t q,
       }
       tc::mma_commit(&sm.vempty[st]);
       tc::mma_commit(&sm.ofull[ob]);
+      mbar_arrive(&sm.mempty[ks % kSteps]);  // the row warps have weighted the step, V is widened: its scales are read
     }
   }
   // every issued MMA has completed before TMEM is released
@@ -946,7 +984,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
       mbar_init(&sm.ofull[s], 1);
       mbar_init(&sm.oempty[s], kRowWarps);
     }
-    for (int s = 0; s < kSteps; ++s) mbar_init(&sm.mfull[s], 1);
+    for (int s = 0; s < kSteps; ++s) {
+      mbar_init(&sm.mfull[s], 1);
+      mbar_init(&sm.mempty[s], 1);
+    }
     for (int s = 0; s < Ti::kSlots; ++s) {
       mbar_init(&sm.rfull[s], 1);
       mbar_init(&sm.rempty[s], kWidenWarps);
@@ -974,6 +1015,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
     if (warp == kRowWarps + kWidenWarps && (threadIdx.x & 31) == 0)
       mma_role<HD, G>(p, sm, smem_addr(q), smem_addr(kbuf), smem_addr(vbuf));
     if (warp == kRowWarps + kWidenWarps + 1) load_role<HD, G>(p, sm, ring);
+    if (warp == kRowWarps + kWidenWarps + 2) scale_role<HD, G>(p, sm);
   }
   tc::fence_before_sync();
   __syncthreads();
