@@ -332,30 +332,32 @@ __device__ __forceinline__ void regs_dec() {
 constexpr int kRowRegs = 184, kWidenRegs = 80, kOtherRegs = 64;
 static_assert(kRowWarps * kRowRegs + kWidenWarps * kWidenRegs + 4 * kOtherRegs <= kThreads / 32 * 128, "register split");
 
-// Bounded wait for the phase of the given parity, in few instructions (the roles share the instruction cache): at
-// most 2^22 tries of up to 2 us.
+// Whether the phase of the given parity is over, after at most 2 us.
+__device__ __forceinline__ bool try_bar(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+constexpr int kTries = 1 << 22;  // bounds every wait: a few seconds
+// A thread's wait.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
-  const uint32_t at = smem_addr(bar);
 #pragma unroll 1
-  for (int i = 0; i < 1 << 22; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(at), "r"(parity)
-        : "memory");
-    if (done) return true;
-  }
+  for (int i = 0; i < kTries; ++i)
+    if (try_bar(bar, parity)) return true;
   return false;
 }
-// A warp's wait, by one lane (32 lanes' tries of one barrier take 400 cycles); false, with the guard set, if it gave up.
+// A warp's wait, all lanes' branches alike (a loop that lanes may leave one by one costs a ready wait 400 cycles
+// beside the other roles' warps); false, with the guard set, if it gave up.
 __device__ __forceinline__ bool wait_all(const Params& p, uint64_t* bar, uint32_t parity) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = wait_bar(bar, parity);
-  ok = __all_sync(0xffffffffu, ok);
-  __syncwarp();
-  if (!ok) set_guard(p.guard, kGuardWaitTimeout);
-  return ok;
+#pragma unroll 1
+  for (int i = 0; i < kTries; ++i)
+    if (__all_sync(0xffffffffu, try_bar(bar, parity))) return true;
+  set_guard(p.guard, kGuardWaitTimeout);
+  return false;
 }
 // A row warp's wait.  One that has given up goes on without waiting (its outputs are worthless, the guard says so),
 // so that it still meets the other row warps at their barriers.
@@ -675,6 +677,9 @@ __device__ __forceinline__ void mma_role(const Params& p, Small& sm, uint32_t q,
       }
       tc::mma_commit(&sm.kempty[st]);
       tc::mma_commit(&sm.sfull[k & 1]);
+      // the step's scales too: their warp's writes, passed on by an arrival of this thread's
+      if (!wait(&sm.mfull[k % kSteps], (k / kSteps) & 1)) return false;
+      mbar_arrive(&sm.sfull[k & 1]);
       return true;
     };
     if (ok) ok = scores(ks);
@@ -807,7 +812,6 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
     };
     for (int s = w.s0; s < w.s1; ++s, ++ks) {
       const int buf = ks & 1;
-      wait_row(p, &sm.mfull[ks % kSteps], (ks / kSteps) & 1, ok);
       wait_row(p, &sm.sfull[buf], (ks >> 1) & 1, ok);
       tc::fence_after_sync();
       const Step& m = sm.step[ks % kSteps];
@@ -979,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
       mbar_init(&sm.vfull[s], kWidenWarps);
       mbar_init(&sm.kempty[s], 1);
       mbar_init(&sm.vempty[s], 1);
-      mbar_init(&sm.sfull[s], 1);
+      mbar_init(&sm.sfull[s], 2);
       mbar_init(&sm.pfull[s], kRowWarps);
       mbar_init(&sm.ofull[s], 1);
       mbar_init(&sm.oempty[s], kRowWarps);
