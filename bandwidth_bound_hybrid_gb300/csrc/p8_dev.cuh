@@ -53,7 +53,7 @@ __device__ __forceinline__ int page_of(const Cache& c, int b, int j) {
   return (unsigned)pg < (unsigned)c.pool_pages ? pg : -1;
 }
 __device__ __forceinline__ long long code_at(const Cache& c, int pg, int g, int at, int hd) {
-  return pg * c.page_stride + ((long long)g * c.page_tokens + at * kBlock) * hd;
+  return pg * c.page_stride + (long long)(g * c.page_tokens + at * kBlock) * hd;
 }
 __device__ __forceinline__ long long scale_at(const Cache& c, int pg, int g, int at) {
   return pg * c.scale_stride + (long long)g * c.bpp + at;
@@ -66,9 +66,9 @@ struct View {
 };
 __device__ __forceinline__ View view_of(int t, int window, int sinks) {
   View v;
-  v.wb = window > 0 && t - window + 1 > 0 ? (t - window + 1) / kBlock : 0;
-  v.ns = min(v.wb, (int)(((long long)sinks + kBlock - 1) / kBlock));
-  v.n = v.ns + t / kBlock - v.wb + 1;
+  v.wb = window > 0 && t - window + 1 > 0 ? (unsigned)(t - window + 1) / kBlock : 0;
+  v.ns = min(v.wb, (int)(((unsigned)sinks + kBlock - 1) / kBlock));
+  v.n = v.ns + (int)((unsigned)t / kBlock) - v.wb + 1;
   return v;
 }
 __device__ __forceinline__ int block_at(const View& v, int i) { return i < v.ns ? i : i - v.ns + v.wb; }

@@ -318,6 +318,36 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// 64 consecutive FP32 columns of this warp's 32 TMEM lanes, one wait.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float* v) {
+  uint32_t r[64];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
+        "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
+        "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+        "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
+  if (N == 64)
+    tmem_ld64(taddr, v);
+  else
+    tc::tmem_ld32(taddr, v);
+}
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 template <int R>
@@ -730,51 +760,42 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
   for (bool more = first_piece<HD, G>(p, sm, w); more; more = next_piece<HD, G>(p, sm, w)) {
     // ------------------------------------------------ queries: warp `warp` rows 16 warp ..
     // normalised by 2^e with 2^e max |q| in [2^9, 2^10): as two fp16 parts q keeps 22 bits of the row's largest
-    constexpr int PP = HD / 64;  // pairs of a lane
+    // (8 lanes a row, 4 rows at a time: little code, since all of it misses the instruction cache at first)
+    constexpr int PP = HD / 16;  // rotate-half pairs of a lane
+    const int l8 = lane & 7;
 #pragma unroll 1
-    for (int m0 = warp * 16; m0 < warp * 16 + 16; m0 += 4) {
-      float x[4][PP][2];
-      float2 cs[4][PP];
+    for (int m = warp * 16 + (lane >> 3); m < warp * 16 + 16; m += 4) {
+      const int i = min(m / G, w.rows - 1);  // (rows past the tile's read its last one)
+      const float* y = p.y + (sm.first[w.b] + w.i0 + i) * p.ld_y + (long long)(w.g * G + m % G) * HD + l8;
+      const float2* rope = p.rope + (long long)(w.t0 + i) * (HD / 2) + l8;
+      float x[PP][2];
+      uint32_t a = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {  // (rows past the tile's read its last one)
-        const int i = min((m0 + k) / G, w.rows - 1);
-        const float* y = p.y + (sm.first[w.b] + w.i0 + i) * p.ld_y + (long long)(w.g * G + (m0 + k) % G) * HD;
-        const float2* rope = p.rope + (long long)(w.t0 + i) * (HD / 2);
+      for (int u = 0; u < PP; ++u) {
+        rotate(y[u * 8], y[u * 8 + HD / 2], rope[u * 8], &x[u][0], &x[u][1]);
 #pragma unroll
-        for (int u = 0; u < PP; ++u) {
-          x[k][u][0] = y[u * 32 + lane];
-          x[k][u][1] = y[u * 32 + lane + HD / 2];
-          cs[k][u] = rope[u * 32 + lane];
+        for (int h = 0; h < 2; ++h) {
+          x[u][h] *= p.scale_log2e;
+          a = max(a, __float_as_uint(x[u][h]) & 0x7fffffffu);
         }
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t a = 0;
+      for (int o = 1; o < 8; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+      const int e = min(max(9 + 127 - (int)(a >> 23), -103), 100);
+      const float up = pow2(e);
+      if (l8 == 0) sm.qf[m] = pow2(-e);
+      uint8_t* at = q + m * 128 + l8 * 2;
 #pragma unroll
-        for (int u = 0; u < PP; ++u) {
-          rotate(x[k][u][0], x[k][u][1], cs[k][u], &x[k][u][0], &x[k][u][1]);
+      for (int u = 0; u < PP; ++u)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            x[k][u][h] *= p.scale_log2e;
-            a = max(a, __float_as_uint(x[k][u][h]) & 0x7fffffffu);
-          }
+        for (int h = 0; h < 2; ++h) {  // element 8 c + l8
+          const int c = u + h * (HD / 16);
+          const float v = x[u][h] * up;
+          const __half hi = __float2half_rn(v), lo = __float2half_rn(v - __half2float(hi));
+          uint8_t* d = at + (c >> 3) * (128 * 128) + (((c ^ m) & 7) << 4);
+          *reinterpret_cast<__half*>(d) = hi;
+          *reinterpret_cast<__half*>(d + Ti::kQ) = lo;
         }
-        a = __reduce_max_sync(0xffffffffu, a);
-        const int e = min(max(9 + 127 - (int)(a >> 23), -103), 100), m = m0 + k;
-        const float up = pow2(e);
-        if (lane == 0) sm.qf[m] = pow2(-e);
-#pragma unroll
-        for (int u = 0; u < PP; ++u)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int d = u * 32 + lane + h * (HD / 2), c = d >> 3;
-            const float v = x[k][u][h] * up;
-            const __half hi = __float2half_rn(v), lo = __float2half_rn(v - __half2float(hi));
-            uint8_t* at = q + (c >> 3) * (128 * 128) + m * 128 + (((c ^ m) & 7) << 4) + (d & 7) * 2;
-            *reinterpret_cast<__half*>(at) = hi;
-            *reinterpret_cast<__half*>(at + Ti::kQ) = lo;
-          }
-      }
     }
     fence_async_smem();
     __syncwarp();
@@ -795,16 +816,17 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
       tc::fence_after_sync();
       const bool moved = __any_sync(0xffffffffu, cf != 1.f);
       const uint64_t c2 = pack2(cf, cf), e2 = pack2(ef, ef);
+      constexpr int NG = NA == 64 ? 64 : 32;  // outputs at a time
 #pragma unroll
-      for (int c = 0; c < NA; c += 32) {
-        float v[32];
-        tc::tmem_ld32(outs + ob * HD + c, v);
+      for (int c = 0; c < NA; c += NG) {
+        float v[NG];
+        tmem_ld<NG>(outs + ob * HD + c, v);
         if (moved) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[c / 2 + i] = mul2(acc[c / 2 + i], c2);
+          for (int i = 0; i < NG / 2; ++i) acc[c / 2 + i] = mul2(acc[c / 2 + i], c2);
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[c / 2 + i] = fma2(pack2(v[2 * i], v[2 * i + 1]), e2, acc[c / 2 + i]);
+        for (int i = 0; i < NG / 2; ++i) acc[c / 2 + i] = fma2(pack2(v[2 * i], v[2 * i + 1]), e2, acc[c / 2 + i]);
       }
       tc::fence_before_sync();
       __syncwarp();
@@ -831,44 +853,30 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
         }
         return 1.f;
       };
-      // the maximum, 32 scores at a time (loops, not unrolled over the step: the roles share the instruction cache)
+      // the maximum
       float top = -INFINITY;
-#pragma unroll 1
-      for (int c = 0; c < NV; c += 32) {
-        float v[32];
-        tc::tmem_ld32(scores + buf * BN + c, v);
-        float f[2], fv[2];
-        const float z0 = factors(c / 16, f[0], fv[0]), z1 = factors(c / 16 + 1, f[1], fv[1]);
+      float v[NV], f[NV / 16], fv[NV / 16];
+      tmem_ld<NV>(scores + buf * BN, v);
+#pragma unroll
+      for (int j = 0; j < NV / 16; ++j) {
+        const float z = factors(j, f[j], fv[j]);
         if (edge) {
-          uint32_t bits = 0;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int u = m.u[j0 + c / 16 + h];
-            uint32_t see = 0;
-            if (u != INT_MAX) {
-              see = low_mask(t - u + 1);
-              if (p.window > 0) see &= ~low_mask(t - p.window - u + 1) | low_mask(p.sinks - u);
-            }
-            bits |= see << (16 * h);
+          const int u = m.u[j0 + j];
+          uint32_t see = 0;
+          if (u != INT_MAX) {
+            see = low_mask(t - u + 1);
+            if (p.window > 0) see &= ~low_mask(t - p.window - u + 1) | low_mask(p.sinks - u);
           }
-          uint32_t w[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float z = i < 16 ? z0 : z1;
-            if (z != 1.f) v[i] = z;
-            if (!(bits >> i & 1)) v[i] = -INFINITY;
-            w[i] = __float_as_uint(v[i]);
+          for (int i = 0; i < 16; ++i) {
+            if (z != 1.f) v[j * 16 + i] = z;
+            if (!(see >> i & 1)) v[j * 16 + i] = -INFINITY;
           }
-          tmem_st32(scores + buf * BN + c, w);
-          wait_st();
         }
+        float b = v[j * 16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float b = v[h * 16];
-#pragma unroll
-          for (int i = 1; i < 16; ++i) b = fmaxf(b, v[h * 16 + i]);
-          top = fmaxf(top, b * f[h]);
-        }
+        for (int i = 1; i < 16; ++i) b = fmaxf(b, v[j * 16 + i]);
+        top = fmaxf(top, b * f[j]);
       }
       sm.mx[buf][half][row] = top;
       named_barrier(1 + sub, 64);
@@ -879,19 +887,14 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
       // weights, their sum and their two parts
       uint64_t sum2 = 0;
       const uint64_t nref = pack2(-ref, -ref);
-#pragma unroll 1
+#pragma unroll
       for (int c = 0; c < NV; c += 32) {
-        float v[32];
-        tc::tmem_ld32(scores + buf * BN + c, v);
-        float f[2], fv[2];
-        factors(c / 16, f[0], fv[0]);
-        factors(c / 16 + 1, f[1], fv[1]);
         uint32_t pr[32];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int h = i / 8;
+          const int h = (c + 2 * i) / 16;
           float p0, p1, w0, w1;
-          unpack2(fma2(pack2(v[2 * i], v[2 * i + 1]), pack2(f[h], f[h]), nref), p0, p1);
+          unpack2(fma2(pack2(v[c + 2 * i], v[c + 2 * i + 1]), pack2(f[h], f[h]), nref), p0, p1);
           p0 = ex2(p0);
           p1 = ex2(p1);
           sum2 = add2(sum2, pack2(p0, p1));
@@ -1002,6 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
     fence_mbar_init();
   }
   plan_work<HD, G>(p, sm, share);
+  pdl_launch_dependents();         // (the join waits for all of this kernel)
   if (sm.begin >= sm.end) return;  // the whole CTA
   if (warp == kRowWarps + kWidenWarps) tc::tmem_alloc(&sm.tmem, 512);
   tc::fence_before_sync();
@@ -1034,6 +1038,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
 template <int HD, int G>
 __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Params p) {
   const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
   const Share s = reinterpret_cast<const Share*>(p.part)[c];
   if (!s.joins) return;
   const float* part = p.part + 2048;
@@ -1107,7 +1112,7 @@ cudaError_t prompt(const Params& p, int hd, int nsm, cudaStream_t st) {
   const int C = nsm < kPromptCtas ? nsm : kPromptCtas;
   cudaError_t e = launch_k(k.k, dim3(C), dim3(kThreads), k.smem, st, false, p);
   if (e != cudaSuccess || C < 2) return e;
-  return launch_k(k.join, dim3(C - 1, 8), dim3(256), 0, st, false, p);
+  return launch_k(k.join, dim3(C - 1, 8), dim3(256), 0, st, true, p);
 }
 
 }  // namespace p8
