@@ -2606,6 +2606,12 @@ int hy_op_attention_p8_prompt(const float* y_dev, int32_t ldy, int32_t n, int32_
   if (!aligned(row_start_dev) || (n > 0 && !aligned(o_dev)) || !aligned16(workspace_dev) || window < 0 || sinks < 0 ||
       (long long)ldo < (long long)nq * hd)
     return fail(HY_ERR_ARG, "bad 8-bit paged prompt attention arguments (ldo >= nq hd, window and sinks not negative)");
+  // the list of steps: tiles of 128 query vectors, at least 4 blocks a step
+  long long blocks = (long long)p.c.max_pages * p.c.bpp;
+  const long long most = window / p8::kBlock + ((long long)sinks + p8::kBlock - 1) / p8::kBlock + 128 / p8::kBlock + 2;
+  if (window > 0 && most < blocks) blocks = most;
+  if (((long long)n / (128 / (nq / nkv)) + batch) * (blocks / 4 + 2) > 0x7fffffffll / nkv)
+    return fail(HY_ERR_UNSUPPORTED, "8-bit paged prompt attention: too many rows x positions in view in one call");
   if (n == 0) return HY_OK;
   int dev = 0, nsm = 0;
   if ((rc = op_guard(&p.guard)) != HY_OK || (rc = current_device(&dev, &nsm)) != HY_OK || (rc = ensure_p8(dev)) != HY_OK)

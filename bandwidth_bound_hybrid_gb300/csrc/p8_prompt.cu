@@ -59,6 +59,16 @@ struct Tile {
   static constexpr int kSmem = 2 * kQ + (NSK + NSV) * kKV + kSlots * kSlot;
 };
 
+struct Piece {
+  int b, g, i0;             // sequence (-1: no more pieces), kv head, the tile's first row
+  unsigned tile;            // the tile's first step in the list
+  int first;                // the tile's first row in y and o
+  int T, n, rows, t0, t1;   // of the sequence: position, rows; of the tile: rows, first and last position
+  View view;
+  int steps, s0, s1;        // the tile's steps; this CTA's
+};
+constexpr int kPieces = 4;  // of them at a time
+
 // What the row and widening warps need of a step.
 constexpr int kSteps = 8;  // of them at a time
 struct Step {
@@ -72,33 +82,26 @@ struct Step {
 
 struct alignas(16) Small {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], ofull[2], oempty[2], mfull[kSteps], mempty[kSteps], rfull[6],
-      rempty[6], qfull, done;
+      rempty[6], wfull[kPieces], wempty[kPieces], qfull, done;
   uint32_t tmem;
   int odd[6];  // of a ring slot: some block's codes are not there
   int open_nan;
   Step step[kSteps];
+  Piece piece[kPieces];
   float qf[128];
   float mx[2][2][128];
   float ls[2][128];
   // the work
   int T[kMaxB], n[kMaxB], first[kMaxB];
-  long long at[kMaxB + 1];  // steps of one kv head before each sequence
-  long long begin, end;     // this CTA's steps
+  unsigned at[kMaxB + 1];   // steps of one kv head before each sequence
+  unsigned begin, end;      // this CTA's steps
   int b, g, i0;             // its first tile
-  long long tile;           // and that tile's first step
+  unsigned tile;            // and that tile's first step
 };
 
 // A CTA's first piece, for the join: whether it is the tail of a tile that began in CTA `lo`, through CTA `hi`.
 struct Share {
   int joins, lo, hi, b, g, i0;
-};
-
-struct Piece {
-  int b, g, i0;             // sequence, kv head, the tile's first row
-  long long tile;           // the tile's first step in the list
-  int T, n, rows, t0, t1;   // of the sequence: position, rows; of the tile: rows, first and last position
-  View view;
-  int steps, s0, s1;        // the tile's steps; this CTA's
 };
 
 // The blocks that some query of positions t0 .. t1 sees.
@@ -107,51 +110,6 @@ __device__ __forceinline__ View view_range(int t0, int t1, int window, int sinks
   v.n += t1 / kBlock - t0 / kBlock;
   return v;
 }
-template <int HD, int G>
-__device__ __forceinline__ int tile_steps(const Params& p, int T, int n, int i0) {
-  const int t0 = T + i0, t1 = T + min(n, i0 + Tile<HD>::BM / G) - 1;
-  return (view_range(t0, t1, p.window, p.sinks).n + Tile<HD>::NBLK - 1) / Tile<HD>::NBLK;
-}
-template <int HD, int G>
-__device__ __forceinline__ void set_piece(const Params& p, const Small& sm, Piece& w) {
-  w.T = sm.T[w.b];
-  w.n = sm.n[w.b];
-  w.rows = min(w.n - w.i0, Tile<HD>::BM / G);
-  w.t0 = w.T + w.i0;
-  w.t1 = w.t0 + w.rows - 1;
-  w.view = view_range(w.t0, w.t1, p.window, p.sinks);
-  w.steps = (w.view.n + Tile<HD>::NBLK - 1) / Tile<HD>::NBLK;
-  w.s0 = (int)(max(sm.begin, w.tile) - w.tile);
-  w.s1 = (int)(min(sm.end, w.tile + w.steps) - w.tile);
-}
-template <int HD, int G>
-__device__ __forceinline__ bool first_piece(const Params& p, const Small& sm, Piece& w) {
-  if (sm.begin >= sm.end) return false;
-  w.b = sm.b;
-  w.g = sm.g;
-  w.i0 = sm.i0;
-  w.tile = sm.tile;
-  set_piece<HD, G>(p, sm, w);
-  return true;
-}
-template <int HD, int G>
-__device__ __forceinline__ bool next_piece(const Params& p, const Small& sm, Piece& w) {
-  w.tile += w.steps;
-  if (w.tile >= sm.end) return false;
-  w.i0 += Tile<HD>::BM / G;
-  if (w.i0 >= w.n) {
-    w.i0 = 0;
-    do {
-      if (++w.b == p.nb) {
-        w.b = 0;
-        ++w.g;
-      }
-    } while (sm.n[w.b] == 0);  // (there is one with rows: the list has more steps)
-  }
-  set_piece<HD, G>(p, sm, w);
-  return true;
-}
-
 // Sequences, the list of steps and this CTA's span of it (the whole CTA).
 template <int HD, int G>
 __device__ __forceinline__ void plan_work(const Params& p, Small& sm, Share* share) {
@@ -167,37 +125,49 @@ __device__ __forceinline__ void plan_work(const Params& p, Small& sm, Share* sha
     sm.n[tid] = ok ? e - s : 0;
   }
   __syncthreads();
+  // steps of the tile of sequence b's rows i0 .., 0 past its last
+  auto steps_at = [&](int b, int i0) {
+    const int n = sm.n[b], t0 = sm.T[b] + i0, t1 = t0 + min(n - i0, BQ) - 1;
+    if (i0 >= n) return 0u;
+    return (unsigned)(view_range(t0, t1, p.window, p.sinks).n + Tile<HD>::NBLK - 1) / Tile<HD>::NBLK;
+  };
+#pragma unroll 1
   for (int b = warp; b < p.nb; b += kThreads / 32) {
-    const int T = sm.T[b], n = sm.n[b];
-    long long s = 0;
-    for (int i0 = lane * BQ; i0 < n; i0 += 32 * BQ) s += tile_steps<HD, G>(p, T, n, i0);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    unsigned s = 0;
+#pragma unroll 1
+    for (int i0 = lane * BQ; i0 < sm.n[b]; i0 += 32 * BQ) s += steps_at(b, i0);
+    s = __reduce_add_sync(0xffffffffu, s);
     if (lane == 0) sm.at[b + 1] = s;
   }
   __syncthreads();
   if (warp == 0) {
-    long long base = 0;
-    for (int b0 = 0; b0 < p.nb; b0 += 32) {
-      long long incl = b0 + lane < p.nb ? sm.at[b0 + lane + 1] : 0;
+    auto scan = [&](unsigned v) {
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+        const unsigned u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
       }
-      if (b0 + lane < p.nb) sm.at[b0 + lane + 1] = base + incl;
-      base += __shfl_sync(0xffffffffu, incl, 31);
+      return v;
+    };
+    unsigned head = 0;  // steps of a head
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.nb; b0 += 32) {
+      const unsigned incl = scan(b0 + lane < p.nb ? sm.at[b0 + lane + 1] : 0);
+      if (b0 + lane < p.nb) sm.at[b0 + lane + 1] = head + incl;
+      head += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) sm.at[0] = 0;
     __syncwarp();
-    const long long head = base, total = head * p.nkv;
-    const long long C = max(1ll, min((long long)gridDim.x, total / kLeast)), c = blockIdx.x;
-    const long long begin = c < C ? c * total / C : total, end = c < C ? (c + 1) * total / C : total;
+    // CTA c of C takes steps c q + min(c, rem) ..
+    const unsigned total = head * p.nkv, c = blockIdx.x;
+    const unsigned C = max(1u, min(gridDim.x, total / kLeast)), q = total / C, rem = total - q * C;
+    const unsigned begin = c < C ? c * q + min(c, rem) : total, end = c < C ? begin + q + (c < rem) : total;
     Share mine = {0, 0, 0, 0, 0, 0};
     if (begin < end) {
       const int g = (int)(begin / head);
-      const long long r = begin - g * head;
-      int b = 0;  // the last b with at[b] <= r that has steps
+      const unsigned r = begin - g * head;
+      int b = 0;  // the first b with r < at[b + 1]
+#pragma unroll 1
       for (int k = 0; k < p.nb; k += 32) {
         const unsigned in = __ballot_sync(0xffffffffu, k + lane < p.nb && r < sm.at[min(k + lane, p.nb - 1) + 1]);
         if (in) {
@@ -205,18 +175,11 @@ __device__ __forceinline__ void plan_work(const Params& p, Small& sm, Share* sha
           break;
         }
       }
-      long long at = sm.at[b];
-      const int T = sm.T[b], n = sm.n[b];
-      int i0 = 0, steps = 0;
-      for (int k = 0; k < n; k += 32 * BQ) {
-        const int i = k + lane * BQ;
-        const int s = i < n ? tile_steps<HD, G>(p, T, n, i) : 0;
-        int incl = s;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += v;
-        }
+      unsigned at = sm.at[b], steps = 0;
+      int i0 = 0;
+#pragma unroll 1
+      for (int k = 0;; k += 32 * BQ) {  // (its steps end past r)
+        const unsigned s = steps_at(b, k + lane * BQ), incl = scan(s);
         const unsigned in = __ballot_sync(0xffffffffu, r < at + incl);
         if (in) {
           const int l = __ffs(in) - 1;
@@ -227,16 +190,16 @@ __device__ __forceinline__ void plan_work(const Params& p, Small& sm, Share* sha
         }
         at += __shfl_sync(0xffffffffu, incl, 31);
       }
-      const long long tile = g * head + at;
+      const unsigned tile = g * head + at, big = rem * (q + 1);
       if (lane == 0) {
         sm.b = b;
         sm.g = g;
         sm.i0 = i0;
         sm.tile = tile;
       }
-      // the last CTA c with c total / C <= s holds step s
-      const int lo = (int)(((tile + 1) * C - 1) / total), hi = (int)(((tile + steps) * C - 1) / total);
-      mine = {begin > tile && lo + 1 == c, lo, hi, b, g, i0};
+      auto cta_of = [&](unsigned s) { return (int)(s < big ? s / (q + 1) : rem + (s - big) / q); };
+      const int lo = cta_of(tile), hi = cta_of(tile + steps - 1);
+      mine = {begin > tile && lo + 1 == (int)c, lo, hi, b, g, i0};
     }
     if (lane == 0) {
       sm.begin = begin;
@@ -389,6 +352,60 @@ __device__ __forceinline__ bool wait_all(const Params& p, uint64_t* bar, uint32_
   set_guard(p.guard, kGuardWaitTimeout);
   return false;
 }
+// The pieces of this CTA's span, in order, by one warp for all roles (what a launch runs of its code it has to load, at
+// about 4 bytes a cycle: 60 KB take 8 us).
+template <int HD, int G>
+__device__ __forceinline__ void piece_role(const Params& p, Small& sm) {
+  Piece w = {sm.b, sm.g, sm.i0, sm.tile};
+#pragma unroll 1
+  for (int np = 0;; ++np) {
+    if (np > 0) {
+      w.tile += w.steps;
+      w.i0 += Tile<HD>::BM / G;
+      if (w.tile >= sm.end) {
+        w.b = -1;
+      } else if (w.i0 >= w.n) {
+        w.i0 = 0;
+        do {
+          if (++w.b == p.nb) {
+            w.b = 0;
+            ++w.g;
+          }
+        } while (sm.n[w.b] == 0);  // (there is one with rows: the list has more steps)
+      }
+    }
+    if (w.b >= 0) {
+      w.T = sm.T[w.b];
+      w.n = sm.n[w.b];
+      w.first = sm.first[w.b] + w.i0;
+      w.rows = min(w.n - w.i0, Tile<HD>::BM / G);
+      w.t0 = w.T + w.i0;
+      w.t1 = w.t0 + w.rows - 1;
+      w.view = view_range(w.t0, w.t1, p.window, p.sinks);
+      w.steps = (unsigned)(w.view.n + Tile<HD>::NBLK - 1) / Tile<HD>::NBLK;
+      w.s0 = (int)(max(sm.begin, w.tile) - w.tile);
+      w.s1 = (int)(min(sm.end, w.tile + w.steps) - w.tile);
+    }
+    const int k = np % kPieces;
+    if (np >= kPieces && !wait_all(p, &sm.wempty[k], ((np / kPieces) & 1) ^ 1)) return;
+    if ((threadIdx.x & 31) == 0) {
+      sm.piece[k] = w;
+      mbar_arrive(&sm.wfull[k]);
+    }
+    if (w.b < 0) return;
+  }
+}
+// Piece np for a warp; false after the last, or if the wait gave up.
+__device__ __forceinline__ bool next_piece(const Params& p, Small& sm, int np, Piece& w) {
+  const int k = np % kPieces;
+  if (!wait_all(p, &sm.wfull[k], (np / kPieces) & 1)) return false;
+  w = sm.piece[k];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.wempty[k]);
+  return w.b >= 0;
+}
+constexpr int kPieceReaders = kRowWarps + kWidenWarps + 3;
+
 // A row warp's wait.  One that has given up goes on without waiting (its outputs are worthless, the guard says so),
 // so that it still meets the other row warps at their barriers.
 __device__ __forceinline__ void wait_row(const Params& p, uint64_t* bar, uint32_t parity, bool& ok) {
@@ -436,7 +453,8 @@ __device__ __forceinline__ void load_role(const Params& p, Small& sm, uint8_t* r
   int slot = 0;
   uint32_t use = 0;  // times the ring has been gone through
   bool ok = true;
-  for (bool more = first_piece<HD, G>(p, sm, w); more && ok; more = next_piece<HD, G>(p, sm, w)) {
+#pragma unroll 1
+  for (int np = 0; ok && next_piece(p, sm, np, w); ++np) {
     const int ob = (w.T + w.n) / kBlock, steps = w.s1 - w.s0;
     const int* table = p.c.table + (long long)w.b * p.c.max_pages;
     // a block's page and place there are looked up a step before they become an address
@@ -509,7 +527,8 @@ __device__ __forceinline__ void scale_role(const Params& p, Small& sm) {
   const int lane = threadIdx.x & 31;
   Piece w;
   int ks = 0;
-  for (bool more = first_piece<HD, G>(p, sm, w); more; more = next_piece<HD, G>(p, sm, w)) {
+#pragma unroll 1
+  for (int np = 0; next_piece(p, sm, np, w); ++np) {
     const int end = w.T + w.n, ob = end / kBlock;  // the open block, if end % 16
     float os[2] = {0.f, 0.f}, up[2] = {0.f, 0.f};
     if (w.s1 == w.steps && end % kBlock != 0 && w.t1 / kBlock == ob) {
@@ -602,7 +621,8 @@ __device__ __forceinline__ void widen_role(const Params& p, Small& sm, const uin
   Piece w;
   int ks = 0, slot = 0;
   uint32_t use = 0;
-  for (bool more = first_piece<HD, G>(p, sm, w); more; more = next_piece<HD, G>(p, sm, w)) {
+#pragma unroll 1
+  for (int np = 0; next_piece(p, sm, np, w); ++np) {
     const int open_rows = (w.T + w.n) % kBlock;
     const uint16_t* tail = p.c.tail + w.b * p.c.tail_stride + (long long)w.g * kBlock * HD;
     auto tile_of = [&](int v, int step) {
@@ -683,10 +703,16 @@ __device__ __forceinline__ void mma_role(const Params& p, Small& sm, uint32_t q,
     return ok;
   };
   Piece w;
-  int ks = 0, np = 0;
+  int ks = 0;
   bool ok = true;
-  for (bool more = first_piece<HD, G>(p, sm, w); more && ok; more = next_piece<HD, G>(p, sm, w), ++np) {
+#pragma unroll 1
+  for (int np = 0; ok; ++np) {
+    if (!(ok = wait(&sm.wfull[np % kPieces], (np / kPieces) & 1))) break;
+    const Piece& w = sm.piece[np % kPieces];
+    const bool more = w.b >= 0;
     const int steps = w.s1 - w.s0;
+    mbar_arrive(&sm.wempty[np % kPieces]);
+    if (!more) break;
     ok = wait(&sm.qfull, np & 1);
     auto scores = [&](int k) {
       const int st = k % NSK;
@@ -757,7 +783,10 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
   Piece w;
   int ks = 0;
   bool ok = true;
-  for (bool more = first_piece<HD, G>(p, sm, w); more; more = next_piece<HD, G>(p, sm, w)) {
+#pragma unroll 1
+  for (int np = 0;; ++np) {
+    // (the row warps meet at barriers: all of them go on, or none)
+    if (named_barrier_or(9, kRowWarps * 32, !next_piece(p, sm, np, w))) break;
     // ------------------------------------------------ queries: warp `warp` rows 16 warp ..
     // normalised by 2^e with 2^e max |q| in [2^9, 2^10): as two fp16 parts q keeps 22 bits of the row's largest
     // (8 lanes a row, 4 rows at a time: little code, since all of it misses the instruction cache at first)
@@ -766,7 +795,7 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
 #pragma unroll 1
     for (int m = warp * 16 + (lane >> 3); m < warp * 16 + 16; m += 4) {
       const int i = min(m / G, w.rows - 1);  // (rows past the tile's read its last one)
-      const float* y = p.y + (sm.first[w.b] + w.i0 + i) * p.ld_y + (long long)(w.g * G + m % G) * HD + l8;
+      const float* y = p.y + (w.first + i) * p.ld_y + (long long)(w.g * G + m % G) * HD + l8;
       const float2* rope = p.rope + (long long)(w.t0 + i) * (HD / 2) + l8;
       float x[PP][2];
       uint32_t a = 0;
@@ -832,92 +861,117 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.oempty[ob]);
     };
-    for (int s = w.s0; s < w.s1; ++s, ++ks) {
-      const int buf = ks & 1;
-      wait_row(p, &sm.sfull[buf], (ks >> 1) & 1, ok);
-      tc::fence_after_sync();
-      const Step& m = sm.step[ks % kSteps];
-      const int j0 = half * (NV / 16);  // the thread's first block
-      const int edge = m.edge;
-      // A block's factors.  In a step that some row does not see all of, a scale of 0 or NaN goes into the scores, so
-      // that it does not meet the -infinity of the positions out of view (a NaN block makes all of a row's outputs NaN,
-      // whether it is K's or V's).
-      auto factors = [&](int j, float& f, float& fv) {
-        f = m.fk[j0 + j] * qf;
-        fv = m.fv[j0 + j];
-        const float z = f * 0.f + fv * 0.f;  // 0, or NaN
-        if (edge && z != z) fv = 0.f;
-        if (edge && !(z == z && f != 0.f)) {
-          f = 1.f;
-          return z;
-        }
-        return 1.f;
-      };
-      // the maximum
-      float top = -INFINITY;
-      float v[NV], f[NV / 16], fv[NV / 16];
-      tmem_ld<NV>(scores + buf * BN, v);
-#pragma unroll
-      for (int j = 0; j < NV / 16; ++j) {
-        const float z = factors(j, f[j], fv[j]);
-        if (edge) {
-          const int u = m.u[j0 + j];
-          uint32_t see = 0;
-          if (u != INT_MAX) {
-            see = low_mask(t - u + 1);
-            if (p.window > 0) see &= ~low_mask(t - p.window - u + 1) | low_mask(p.sinks - u);
+    // step s, then the outputs of the step before it
+#pragma unroll 1
+    for (int s = w.s0;; ++s, ++ks) {
+      float cf = 1.f, step_ev = 0.f;
+      if (s < w.s1) {
+        const int buf = ks & 1;
+        wait_row(p, &sm.sfull[buf], (ks >> 1) & 1, ok);
+        tc::fence_after_sync();
+        const Step& m = sm.step[ks % kSteps];
+        const int j0 = half * (NV / 16);  // the thread's first block
+        const int edge = m.edge;
+        // A block's factors.  In a step that some row does not see all of, a scale of 0 or NaN goes into the scores, so
+        // that it does not meet the -infinity of the positions out of view (a NaN block makes all of a row's outputs NaN,
+        // whether it is K's or V's).
+        auto factors = [&](int j, float& f, float& fv) {
+          f = m.fk[j0 + j] * qf;
+          fv = m.fv[j0 + j];
+          const float z = f * 0.f + fv * 0.f;  // 0, or NaN
+          if (edge && z != z) fv = 0.f;
+          if (edge && !(z == z && f != 0.f)) {
+            f = 1.f;
+            return z;
           }
+          return 1.f;
+        };
+        // the maximum, 32 scores at a time (loops, not unrolled over the step: the roles share the instruction cache);
+        // what is out of view goes back as -infinity
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < NV; c += 32) {
+          float v[32];
+          tc::tmem_ld32(scores + buf * BN + c, v);
+          float f[2], fv[2];
+          const float z0 = factors(c / 16, f[0], fv[0]), z1 = factors(c / 16 + 1, f[1], fv[1]);
+          if (edge) {
+            uint32_t bits = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int u = m.u[j0 + c / 16 + h];
+              uint32_t see = 0;
+              if (u != INT_MAX) {
+                see = low_mask(t - u + 1);
+                if (p.window > 0) see &= ~low_mask(t - p.window - u + 1) | low_mask(p.sinks - u);
+              }
+              bits |= see << (16 * h);
+            }
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float z = i < 16 ? z0 : z1;
+              if (z != 1.f) v[i] = z;
+              if (!(bits >> i & 1)) v[i] = -INFINITY;
+              w[i] = __float_as_uint(v[i]);
+            }
+            tmem_st32(scores + buf * BN + c, w);
+            wait_st();
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float b = v[h * 16];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) b = fmaxf(b, v[h * 16 + i]);
+            top = fmaxf(top, b * f[h]);
+          }
+        }
+        sm.mx[buf][half][row] = top;
+        named_barrier(1 + sub, 64);
+        top = fmaxf(top, sm.mx[buf][half ^ 1][row]);
+        const float mn = fmaxf(mx, top), ref = mn == -INFINITY ? 0.f : mn;
+        cf = mx == mn ? 1.f : ex2(mx - mn);
+        mx = mn;
+        // weights, their sum and their two parts
+        uint64_t sum2 = 0;
+        const uint64_t nref = pack2(-ref, -ref);
+#pragma unroll 1
+        for (int c = 0; c < NV; c += 32) {
+          float v[32];
+          tc::tmem_ld32(scores + buf * BN + c, v);
+          float f[2], fv[2];
+          factors(c / 16, f[0], fv[0]);
+          factors(c / 16 + 1, f[1], fv[1]);
+          uint32_t pr[32];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            if (z != 1.f) v[j * 16 + i] = z;
-            if (!(see >> i & 1)) v[j * 16 + i] = -INFINITY;
+            const int h = i / 8;
+            float p0, p1, w0, w1;
+            unpack2(fma2(pack2(v[2 * i], v[2 * i + 1]), pack2(f[h], f[h]), nref), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            sum2 = add2(sum2, pack2(p0, p1));
+            unpack2(mul2(pack2(p0, p1), pack2(fv[h], fv[h])), w0, w1);
+            const float h0 = trunc11(w0), h1 = trunc11(w1);
+            pr[i] = half2_bits(h0, h1);
+            pr[16 + i] = half2_bits(w0 - h0, w1 - h1);
           }
+          tmem_st32(scores + buf * BN + c, pr);
         }
-        float b = v[j * 16];
-#pragma unroll
-        for (int i = 1; i < 16; ++i) b = fmaxf(b, v[j * 16 + i]);
-        top = fmaxf(top, b * f[j]);
+        step_ev = m.ev;
+        wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.pfull[buf]);
+        float s0, s1;
+        unpack2(sum2, s0, s1);
+        lsum = fmaf(lsum, cf, s0 + s1);
       }
-      sm.mx[buf][half][row] = top;
-      named_barrier(1 + sub, 64);
-      top = fmaxf(top, sm.mx[buf][half ^ 1][row]);
-      const float mn = fmaxf(mx, top), ref = mn == -INFINITY ? 0.f : mn;
-      const float cf = mx == mn ? 1.f : ex2(mx - mn);
-      mx = mn;
-      // weights, their sum and their two parts
-      uint64_t sum2 = 0;
-      const uint64_t nref = pack2(-ref, -ref);
-#pragma unroll
-      for (int c = 0; c < NV; c += 32) {
-        uint32_t pr[32];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int h = (c + 2 * i) / 16;
-          float p0, p1, w0, w1;
-          unpack2(fma2(pack2(v[c + 2 * i], v[c + 2 * i + 1]), pack2(f[h], f[h]), nref), p0, p1);
-          p0 = ex2(p0);
-          p1 = ex2(p1);
-          sum2 = add2(sum2, pack2(p0, p1));
-          unpack2(mul2(pack2(p0, p1), pack2(fv[h], fv[h])), w0, w1);
-          const float h0 = trunc11(w0), h1 = trunc11(w1);
-          pr[i] = half2_bits(h0, h1);
-          pr[16 + i] = half2_bits(w0 - h0, w1 - h1);
-        }
-        tmem_st32(scores + buf * BN + c, pr);
-      }
-      const float step_ev = m.ev;
-      wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.pfull[buf]);
-      float s0, s1;
-      unpack2(sum2, s0, s1);
-      lsum = fmaf(lsum, cf, s0 + s1);
       if (s > w.s0) gather(ks - 1, corr, ev);
+      if (s == w.s1) break;
       corr = cf;
       ev = step_ev;
     }
-    gather(ks - 1, corr, ev);
 
     // ------------------------------------------------ outputs
     sm.ls[half][row] = lsum;
@@ -928,7 +982,7 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
     const bool whole = w.s0 == 0 && w.s1 == w.steps, live = row < w.rows * G;
     if (whole) {
       inv = l == 0.f ? 0.f : 1.0f / l;
-      o = p.o + (sm.first[w.b] + w.i0 + row / G) * p.ld_o + (long long)(w.g * G + row % G) * HD + half * NA;
+      o = p.o + (w.first + row / G) * p.ld_o + (long long)(w.g * G + row % G) * HD + half * NA;
     } else {
       // a tile that begins here leaves the CTA's second partial, one that goes on its first
       float* d = part + (2ll * blockIdx.x + (w.s0 == 0)) * part_floats_of<HD>();
@@ -999,6 +1053,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
       mbar_init(&sm.rfull[s], 1);
       mbar_init(&sm.rempty[s], kWidenWarps);
     }
+    for (int s = 0; s < kPieces; ++s) {
+      mbar_init(&sm.wfull[s], 1);
+      mbar_init(&sm.wempty[s], kPieceReaders);
+    }
     mbar_init(&sm.qfull, kRowWarps);
     mbar_init(&sm.done, 1);
     sm.open_nan = 0;
@@ -1024,6 +1082,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prompt(const __grid_constant__ 
       mma_role<HD, G>(p, sm, smem_addr(q), smem_addr(kbuf), smem_addr(vbuf));
     if (warp == kRowWarps + kWidenWarps + 1) load_role<HD, G>(p, sm, ring);
     if (warp == kRowWarps + kWidenWarps + 2) scale_role<HD, G>(p, sm);
+    if (warp == kRowWarps + kWidenWarps + 3) piece_role<HD, G>(p, sm);
   }
   tc::fence_before_sync();
   __syncthreads();
