@@ -40,7 +40,6 @@ namespace p8 {
 namespace {
 
 constexpr int kThreads = 512, kRowWarps = 8, kWidenWarps = 4;
-constexpr int kLeast = 2;  // steps of a CTA, if it can be
 
 template <int HD>
 struct Tile {
@@ -160,7 +159,7 @@ __device__ __forceinline__ void plan_work(const Params& p, Small& sm, Share* sha
     __syncwarp();
     // CTA c of C takes steps c q + min(c, rem) ..
     const unsigned total = head * p.nkv, c = blockIdx.x;
-    const unsigned C = max(1u, min(gridDim.x, total / kLeast)), q = total / C, rem = total - q * C;
+    const unsigned C = max(1u, min(gridDim.x, total)), q = total / C, rem = total - q * C;
     const unsigned begin = c < C ? c * q + min(c, rem) : total, end = c < C ? begin + q + (c < rem) : total;
     Share mine = {0, 0, 0, 0, 0, 0};
     if (begin < end) {
@@ -792,7 +791,7 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
     // (8 lanes a row, 4 rows at a time: little code, since all of it misses the instruction cache at first)
     constexpr int PP = HD / 16;  // rotate-half pairs of a lane
     const int l8 = lane & 7;
-#pragma unroll 1
+#pragma unroll 2
     for (int m = warp * 16 + (lane >> 3); m < warp * 16 + 16; m += 4) {
       const int i = min(m / G, w.rows - 1);  // (rows past the tile's read its last one)
       const float* y = p.y + (w.first + i) * p.ld_y + (long long)(w.g * G + m % G) * HD + l8;
@@ -801,7 +800,7 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
       uint32_t a = 0;
 #pragma unroll
       for (int u = 0; u < PP; ++u) {
-        rotate(y[u * 8], y[u * 8 + HD / 2], rope[u * 8], &x[u][0], &x[u][1]);
+        rotate(__ldg(y + u * 8), __ldg(y + u * 8 + HD / 2), __ldg(rope + u * 8), &x[u][0], &x[u][1]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           x[u][h] *= p.scale_log2e;
