@@ -367,13 +367,15 @@ __device__ __forceinline__ void plan_work(const Params& p, Small& sm) {
   items = p.nkv * __reduce_add_sync(0xffffffffu, items);
   least = p.nkv * __reduce_add_sync(0xffffffffu, least);
   most = __reduce_max_sync(0xffffffffu, most);
-  // m: a tile per warp if the CTAs suffice, else the least that fits
+  // m: a tile per warp if the CTAs suffice (or the few more with which one join does: 4096 rows of 4 x 128 12.7 us in
+  // ranges of 8 tiles, 33 sharers and two joins), else the least that fits
   unsigned m = 0;
   if (least <= (unsigned)grid) {
-    m = W;
-  } else if (items <= (unsigned)grid) {
+    m = W * max(1u, (most + W * kJoin - 1) / (W * kJoin));
+  } else if (items < (unsigned)grid) {
     const unsigned lo0 = max((total + grid - 1) / grid, (unsigned)W);
-    unsigned lo = lo0, hi = most;  // `hi` fits
+    // ranges of m tiles are fewer than total / m + items: `hi` fits
+    unsigned lo = lo0, hi = min(most, total / (grid - items) + 1);
     while (lo < hi) {
       const unsigned mid = (lo + hi) / 2;
       unsigned r = 0;
@@ -445,10 +447,7 @@ __device__ __forceinline__ void set_range(const Params& p, Small& sm, int t) {
     sm.g = it.g;
     sm.first = it.first;
     sm.end = it.end;
-    if (sm.m == W) {
-      sm.tile0 = k * W;
-      sm.ntile = min(W, n - k * W);
-    } else if (sm.m) {
+    if (sm.m) {
       const int len = (unsigned)n / (unsigned)parts, more = n - len * parts;
       sm.tile0 = k * len + min(k, more);
       sm.ntile = len + (k < more);
@@ -676,27 +675,29 @@ __device__ __forceinline__ void last_block(const Params& p, Small& sm, uint8_t* 
 
 // ---------------------------------------------------------------- joins
 // Partials first, first + step, ... (n <= 32 of them) of the item joined into
-// the outputs (final) or into the first of them.  Not inlined: its loads would
-// cost the tile loop registers.
+// the outputs (final) or into the first of them, by TG groups of threads, each
+// a TG-th of them.  Not inlined: its loads would cost the tile loop registers.
 template <int HD, int G>
 __device__ __noinline__ void join_parts(const Params& p, Small& sm, uint8_t* smem, int first, int step, int n,
                                         bool final) {
   using Sh = Shape<HD>;
   constexpr int NV = G * HD / 4, VT = (NV + Sh::kThreads - 1) / Sh::kThreads;  // vectors; of a thread
-  constexpr int NX = 8;                                                         // partials on their way at once
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int TG = VT == 1 ? Sh::kThreads / NV : 1, NX = 8;                   // NX partials on their way at once
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = VT == 1 ? tid / NV : 0, v0 = tid - grp * NV;
   const int c_lo = sm.c_lo, slot0 = sm.slot0;
   auto part_of = [&](int i) { return p.part + (2ll * (c_lo + i) + (i == 0 ? slot0 : 0)) * part_size(G, HD); };
   float* o = p.o + (long long)sm.b * p.ld_o + (long long)sm.g * G * HD;
   float* wt = reinterpret_cast<float*>(smem);  // [32][G] weights, joined reference and sum per head
+  float4* sums = reinterpret_cast<float4*>(smem + 2048);  // [TG][NV]
   float4 x[VT][NX];
   auto load = [&](int i0) {
 #pragma unroll
     for (int i = 0; i < NX; ++i)
 #pragma unroll
       for (int t = 0; t < VT; ++t)
-        if (i0 + i < n && tid + t * Sh::kThreads < NV)
-          x[t][i] = __ldcg(reinterpret_cast<const float4*>(part_of(first + (i0 + i) * step)) + tid + t * Sh::kThreads);
+        if (i0 + i * TG + grp < n && v0 + t * Sh::kThreads < NV)
+          x[t][i] = __ldcg(reinterpret_cast<const float4*>(part_of(first + (i0 + i * TG + grp) * step)) + v0 +
+                           t * Sh::kThreads);
   };
   load(0);
   for (int j = warp; j < G; j += Sh::W) {
@@ -720,19 +721,27 @@ __device__ __noinline__ void join_parts(const Params& p, Small& sm, uint8_t* sme
   float4 a[VT];
 #pragma unroll
   for (int t = 0; t < VT; ++t) a[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < n; i0 += NX) {
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += NX * TG) {
     if (i0 > 0) load(i0);
 #pragma unroll
     for (int i = 0; i < NX; ++i)
 #pragma unroll
       for (int t = 0; t < VT; ++t)
-        if (i0 + i < n && tid + t * Sh::kThreads < NV)
-          add_scaled(a[t], wt[(i0 + i) * G + (tid + t * Sh::kThreads) * 4 / HD], x[t][i]);
+        if (i0 + i * TG + grp < n && v0 + t * Sh::kThreads < NV)
+          add_scaled(a[t], wt[(i0 + i * TG + grp) * G + (v0 + t * Sh::kThreads) * 4 / HD], x[t][i]);
+  }
+  if (TG > 1) {
+    if (grp > 0) sums[tid] = a[0];
+    __syncthreads();
+#pragma unroll 1
+    for (int k = 1; k < TG; ++k)
+      if (grp == 0) add_scaled(a[0], 1.f, sums[k * NV + v0]);
   }
 #pragma unroll
   for (int t = 0; t < VT; ++t) {
-    const int v = tid + t * Sh::kThreads, j = v * 4 / HD;
-    if (v >= NV) break;
+    const int v = v0 + t * Sh::kThreads, j = v * 4 / HD;
+    if (v >= NV || grp > 0) break;
     if (final) {
       put_out(o + v * 4, a[t], inverse(wt[33 * G + j]));
     } else {
