@@ -37,9 +37,11 @@ namespace p8 {
 namespace {
 
 // ------------------------------------------------------------ append
-// A warp per block, kv head and K or V: its rows in registers as bf16 pairs
-// (4 + 4 adjacent values, the rotate-half partners, in a lane), from the tail
-// where they are old; one pass, the block's maximum by one reduction.
+// A warp (hd 256: two) per block, kv head and K or V: its rows in registers as
+// bf16 pairs (4 + 4 adjacent values, the rotate-half partners, in a lane), from
+// the tail where they are old; one pass, the block's maximum by one reduction.
+// Bound by its bytes.  Small CTAs in one wave: 4 x 2048 rows of 4 x 128 in 13.9
+// us (5.7 TB/s), 17.5 in CTAs of 8 warps with 80 registers, which make 1.1.
 // VEC: y, the table and kv_new are 16-byte aligned with rows of whole 16 bytes.
 template <bool VEC>
 __device__ __forceinline__ float4 load4(const float* p) {
@@ -57,44 +59,51 @@ __device__ __forceinline__ void store4(float* p, float a, float b, float c, floa
   }
 }
 
+constexpr int kAppendWarps = 4;  // of a CTA
 template <int HD, bool VEC>
-__global__ void __launch_bounds__(256) k_append(const __grid_constant__ Params p) {
-  constexpr int LV = HD / 8, RP = 32 / LV, NP = kBlock / RP;  // lanes of a row, rows of a pass, passes
-  __shared__ int at[kMaxB + 1], T0[kMaxB], first[kMaxB], rows[kMaxB], wsum[8];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  {
-    int blocks = 0;
-    if (tid < p.nb) {
-      const int T = p.len[tid], s = p.row_start[tid], e = p.row_start[tid + 1];
-      const bool ok = T >= 0 && s >= 0 && e >= s && e <= p.n &&
-                      (long long)T + (e - s) <= (long long)p.c.max_pages * p.c.page_tokens;
-      if (!ok && blockIdx.x == 0) set_guard(p.guard, kGuardBadPosition);
-      if (ok && e > s) {
-        const int j0 = T / kBlock, j1 = (T + (e - s)) / kBlock;  // the first block; the open one after the call
-        blocks = (T + (e - s) - 1) / kBlock - j0 + 1;
-        if (T % kBlock != 0 && j1 > j0 && (T + (e - s)) % kBlock != 0) --blocks;
+__global__ void __launch_bounds__(kAppendWarps * 32, 8) k_append(const __grid_constant__ Params p) {
+  constexpr int SP = HD == 256 ? 2 : 1;                             // warps of a unit, each a part of the rows
+  constexpr int LV = HD / 8, RP = 32 / LV, NP = kBlock / RP / SP;   // lanes of a row, rows of a pass, passes
+  __shared__ int at[kMaxB + 1], T0[kMaxB], first[kMaxB], rows[kMaxB];
+  __shared__ uint32_t top[2][kAppendWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    int base = 0;
+    for (int b0 = 0; b0 < p.nb; b0 += 32) {
+      const int b = b0 + lane;
+      int incl = 0;
+      if (b < p.nb) {
+        const int T = p.len[b], s = p.row_start[b], e = p.row_start[b + 1];
+        const bool ok = T >= 0 && s >= 0 && e >= s && e <= p.n &&
+                        (long long)T + (e - s) <= (long long)p.c.max_pages * p.c.page_tokens;
+        if (!ok && blockIdx.x == 0) set_guard(p.guard, kGuardBadPosition);
+        if (ok && e > s) {
+          const int j0 = T / kBlock, j1 = (T + (e - s)) / kBlock;  // the first block; the open one after the call
+          incl = (T + (e - s) - 1) / kBlock - j0 + 1;
+          if (T % kBlock != 0 && j1 > j0 && (T + (e - s)) % kBlock != 0) --incl;
+        }
+        T0[b] = T;
+        first[b] = s;
+        rows[b] = e - s;
       }
-      T0[tid] = T;
-      first[tid] = s;
-      rows[tid] = e - s;
-    }
-    int incl = blocks;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (b < p.nb) at[b + 1] = base + incl;
+      base += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) incl += wsum[w];
-    at[tid + 1] = incl;
-    if (tid == 0) at[0] = 0;
-    __syncthreads();
+    if (lane == 0) at[0] = 0;
   }
+  __syncthreads();
   const int heads = 2 * p.nkv;
   const long long total = (long long)at[p.nb] * heads;
   const int sub = lane / LV, e = (lane % LV) * 4;  // row of a pass; the lane's first element, of the first half
-  for (long long unit = blockIdx.x * 8ll + warp; unit < total; unit += gridDim.x * 8ll) {
+  const int row_off = warp % SP * (kBlock / SP);
+  int turn = 0;
+  for (long long unit = blockIdx.x * (long long)(kAppendWarps / SP) + warp / SP; unit < total;
+       unit += gridDim.x * (long long)(kAppendWarps / SP)) {
     const int bi = (int)(unit / heads), kg = (int)(unit % heads);
     int b = 0;
     for (int step = kMaxB / 2; step > 0; step >>= 1)  // the last b with at[b] <= bi that has blocks
@@ -115,7 +124,7 @@ __global__ void __launch_bounds__(256) k_append(const __grid_constant__ Params p
       uint32_t a = 0;
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
-        const int r = k * RP + sub, rc = min(max(r, lo), hi - 1);  // (a lane without a new row reads one all the same)
+        const int r = row_off + k * RP + sub, rc = min(max(r, lo), hi - 1);  // (a lane without a new row reads one all the same)
         const float* yr = y0 + (row0 + rc) * p.ld_y;
         const float4 x0 = load4<VEC>(yr), x1 = load4<VEC>(yr + HD / 2);
         float f0[4] = {x0.x, x0.y, x0.z, x0.w}, f1[4] = {x1.x, x1.y, x1.z, x1.w};
@@ -134,7 +143,7 @@ __global__ void __launch_bounds__(256) k_append(const __grid_constant__ Params p
       if (lo > 0 && closes) {
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
-          const int r = k * RP + sub;
+          const int r = row_off + k * RP + sub;
           if (r < lo) {
             const uint2 t0 = *reinterpret_cast<const uint2*>(tail + r * HD);
             const uint2 t1 = *reinterpret_cast<const uint2*>(tail + r * HD + HD / 2);
@@ -153,6 +162,12 @@ __global__ void __launch_bounds__(256) k_append(const __grid_constant__ Params p
 #pragma unroll
           for (int i = 0; i < 4; ++i) a = abs_max(a, v[k][i]);
         a = __reduce_max_sync(0xffffffffu, a);
+        if (SP > 1) {  // (the warps of a unit go the same way; two turns' places, so that one barrier a turn does)
+          if (lane == 0) top[turn][warp] = a;
+          named_barrier(1 + warp / SP, 32 * SP);
+          a = max(a, top[turn][warp ^ 1]);
+          turn ^= 1;
+        }
         s = block_scale(a, &inv);
         const int pg = page_of(p.c, b, j);
         if (pg < 0) {
@@ -164,7 +179,7 @@ __global__ void __launch_bounds__(256) k_append(const __grid_constant__ Params p
       }
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
-        const int r = k * RP + sub;
+        const int r = row_off + k * RP + sub;
         float val[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -682,7 +697,7 @@ __device__ __noinline__ void join_parts(const Params& p, Small& sm, uint8_t* sme
                                         bool final) {
   using Sh = Shape<HD>;
   constexpr int NV = G * HD / 4, VT = (NV + Sh::kThreads - 1) / Sh::kThreads;  // vectors; of a thread
-  constexpr int TG = VT == 1 ? Sh::kThreads / NV : 1, NX = 8;                   // NX partials on their way at once
+  constexpr int TG = VT == 1 ? Sh::kThreads / NV : 1, NX = HD == 256 ? 12 : 8;                   // NX partials on their way at once
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = VT == 1 ? tid / NV : 0, v0 = tid - grp * NV;
   const int c_lo = sm.c_lo, slot0 = sm.slot0;
   auto part_of = [&](int i) { return p.part + (2ll * (c_lo + i) + (i == 0 ? slot0 : 0)) * part_size(G, HD); };
@@ -1159,7 +1174,8 @@ cudaError_t append(const Params& p, int hd, cudaStream_t st) {
   if (p.n <= 0) return cudaSuccess;
   // rows cut into blocks: at most two more than whole ones for each sequence with rows
   const long long blocks = p.n / kBlock + 2ll * (p.nb < p.n ? p.nb : p.n);
-  long long grid = (blocks * 2 * p.nkv + 7) / 8;
+  const int units = hd == 256 ? kAppendWarps / 2 : kAppendWarps;  // of a CTA
+  long long grid = (blocks * 2 * p.nkv + units - 1) / units;
   if (grid > 1 << 20) grid = 1 << 20;
   auto ok = [](const void* q) { return ((uintptr_t)q & 15) == 0; };
   const bool vec = ok(p.y) && p.ld_y % 4 == 0 && ok(p.rope) && ok(p.kv_new);
@@ -1170,7 +1186,7 @@ cudaError_t append(const Params& p, int hd, cudaStream_t st) {
     case 256: k = vec ? k_append<256, true> : k_append<256, false>; break;
     default: return cudaErrorInvalidValue;
   }
-  k<<<(unsigned)grid, 256, 0, st>>>(p);
+  k<<<(unsigned)grid, kAppendWarps * 32, 0, st>>>(p);
   return cudaGetLastError();
 }
 
