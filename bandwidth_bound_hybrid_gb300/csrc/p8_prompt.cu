@@ -320,8 +320,8 @@ template <int R>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
-// Registers of a thread by role: 8 x 184 + 4 x 80 + 4 x 64 = 2048, the launch's 16 x 128.
-constexpr int kRowRegs = 184, kWidenRegs = 80, kOtherRegs = 64;
+// Registers of a thread by role: 8 x 192 + 4 x 64 + 4 x 64 = 2048, the launch's 16 x 128.
+constexpr int kRowRegs = 192, kWidenRegs = 64, kOtherRegs = 64;
 static_assert(kRowWarps * kRowRegs + kWidenWarps * kWidenRegs + 4 * kOtherRegs <= kThreads / 32 * 128, "register split");
 
 // Whether the phase of the given parity is over, after at most 2 us.
@@ -933,7 +933,7 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
         mx = mn;
         // weights, their sum and their two parts
         uint64_t sum2 = 0;
-        const uint64_t nref = pack2(-ref, -ref);
+        const uint64_t nref = pack2(-ref, -ref), minus1 = pack2(-1.f, -1.f);
 #pragma unroll 1
         for (int c = 0; c < NV; c += 32) {
           float v[32];
@@ -945,15 +945,17 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int h = i / 8;
-            float p0, p1, w0, w1;
+            float p0, p1, w0, w1, l0, l1;
             unpack2(fma2(pack2(v[2 * i], v[2 * i + 1]), pack2(f[h], f[h]), nref), p0, p1);
             p0 = ex2(p0);
             p1 = ex2(p1);
-            sum2 = add2(sum2, pack2(p0, p1));
-            unpack2(mul2(pack2(p0, p1), pack2(fv[h], fv[h])), w0, w1);
+            const uint64_t pp = pack2(p0, p1), f2 = pack2(fv[h], fv[h]);
+            sum2 = add2(sum2, pp);
+            unpack2(mul2(pp, f2), w0, w1);
             const float h0 = trunc11(w0), h1 = trunc11(w1);
+            unpack2(fma2(pack2(h0, h1), minus1, pack2(w0, w1)), l0, l1);  // w - h, exact
             pr[i] = half2_bits(h0, h1);
-            pr[16 + i] = half2_bits(w0 - h0, w1 - h1);
+            pr[16 + i] = half2_bits(l0, l1);
           }
           tmem_st32(scores + buf * BN + c, pr);
         }
