@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 8) k_append(const __grid_co
       uint32_t a = 0;
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
-        const int r = row_off + k * RP + sub, rc = min(max(r, lo), hi - 1);  // (a lane without a new row reads one all the same)
+        const int r = row_off + k * RP + sub;
+        const int rc = min(max(r, lo), hi - 1);  // (a lane without a new row reads one all the same)
         const float* yr = y0 + (row0 + rc) * p.ld_y;
         const float4 x0 = load4<VEC>(yr), x1 = load4<VEC>(yr + HD / 2);
         float f0[4] = {x0.x, x0.y, x0.z, x0.w}, f1[4] = {x1.x, x1.y, x1.z, x1.w};
@@ -697,7 +698,8 @@ __device__ __noinline__ void join_parts(const Params& p, Small& sm, uint8_t* sme
                                         bool final) {
   using Sh = Shape<HD>;
   constexpr int NV = G * HD / 4, VT = (NV + Sh::kThreads - 1) / Sh::kThreads;  // vectors; of a thread
-  constexpr int TG = VT == 1 ? Sh::kThreads / NV : 1, NX = HD == 256 ? 12 : 8;                   // NX partials on their way at once
+  constexpr int TG = VT == 1 ? Sh::kThreads / NV : 1;
+  constexpr int NX = HD == 256 ? 12 : 8;  // partials of a thread on their way at once
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = VT == 1 ? tid / NV : 0, v0 = tid - grp * NV;
   const int c_lo = sm.c_lo, slot0 = sm.slot0;
   auto part_of = [&](int i) { return p.part + (2ll * (c_lo + i) + (i == 0 ? slot0 : 0)) * part_size(G, HD); };

@@ -16,20 +16,32 @@
 //   * 8 row warps: a thread has a row's scores of half a step (tcgen05.ld),
 //     the maximum is exchanged with the other half's thread; the weights go
 //     back into the scores' columns as the A operand of the second product
-//     (32 scores become 16 columns of w_hi and 16 of w_lo); then the step
-//     before is added, half the elements of a head a thread;
+//     (16 scores become 8 columns of w_hi and 8 of w_lo); then the step before
+//     is added, half the elements of a head a thread;
 //   * 1 warp copies the codes of a step's blocks (each contiguous in its page,
 //     adjacent ones together) to a ring of shared memory in bulk, another
 //     fetches their scales;
 //   * 4 warps widen them to fp16 tiles in shared memory, 128-byte swizzle, K as
 //     K-major B operand and V, laid out alike, as MN-major;
 //   * 1 thread issues tcgen05.mma: S of step k + 1 before O of step k, so that
-//     the row warps' softmax runs beside the tensor cores.
+//     the row warps' softmax runs beside the tensor cores; 1 warp hands out the
+//     pieces (a CTA's steps of a tile).
 // Two score and (hd <= 128) two output accumulators in TMEM: 512 columns.
 //
-// Work split: the steps of all tiles form one list, CTA c takes steps c n / C ..
-// of it.  A tile that several CTAs share leaves partials (outputs, maximum, sum)
-// in the workspace, joined by a second small kernel.
+// Work split: the steps of all tiles form one list, of which CTA c takes an
+// equal span.  A tile that several CTAs share leaves partials (outputs, maximum,
+// sum) in the workspace, joined by a second small kernel.
+//
+// Bound by issue: 2048 rows of 4 x 128 with 16 heads at position 4096 take 197
+// us, 435 TFLOP/s of the two products (twice that is executed, 45% of the
+// measured bf16 rate).  A step of 128 x 128 takes 5400 cycles, of which the
+// products need 2048: a scheduler issues 3000 instructions for it (two row warps
+// 750 each, a widening warp 630, waits), at 55% of its cycles; the widening of
+// K and V (4800 cycles in one warp a scheduler) is the longest chain.
+// Measured and not kept: 8 widening warps (198 us, the row warps with 160
+// registers), tiles of 256 rows that share the widened codes (219), loads of the
+// codes in registers instead of the ring (407), a thread's 64 scores unrolled
+// (387: the roles' code then misses the instruction cache).
 #include <climits>
 
 #include "p8_dev.cuh"
@@ -80,8 +92,8 @@ struct Step {
 };
 
 struct alignas(16) Small {
-  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], ofull[2], oempty[2], mfull[kSteps], mempty[kSteps], rfull[6],
-      rempty[6], wfull[kPieces], wempty[kPieces], qfull, done;
+  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], ofull[2], oempty[2], mfull[kSteps],
+      mempty[kSteps], rfull[6], rempty[6], wfull[kPieces], wempty[kPieces], qfull, done;
   uint32_t tmem;
   int odd[6];  // of a ring slot: some block's codes are not there
   int open_nan;
@@ -263,7 +275,8 @@ __device__ __forceinline__ uint64_t sdesc_mn128(uint32_t saddr, uint32_t chunk) 
   d |= (uint64_t)2 << 61;
   return d;
 }
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       bool accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
@@ -280,35 +293,26 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-// 64 consecutive FP32 columns of this warp's 32 TMEM lanes, one wait.
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float* v) {
-  uint32_t r[64];
+// 16 columns: load with its wait, store.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
-      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
-      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
-        "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
-        "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
-        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
-        "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 #pragma unroll
-  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
-  if (N == 64)
-    tmem_ld64(taddr, v);
-  else
-    tc::tmem_ld32(taddr, v);
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -322,7 +326,8 @@ __device__ __forceinline__ void regs_dec() {
 }
 // Registers of a thread by role: 8 x 192 + 4 x 64 + 4 x 64 = 2048, the launch's 16 x 128.
 constexpr int kRowRegs = 192, kWidenRegs = 64, kOtherRegs = 64;
-static_assert(kRowWarps * kRowRegs + kWidenWarps * kWidenRegs + 4 * kOtherRegs <= kThreads / 32 * 128, "register split");
+static_assert(kRowWarps * kRowRegs + kWidenWarps * kWidenRegs + 4 * kOtherRegs <= kThreads / 32 * 128,
+              "register split");
 
 // Whether the phase of the given parity is over, after at most 2 us.
 __device__ __forceinline__ bool try_bar(uint64_t* bar, uint32_t parity) {
@@ -608,7 +613,8 @@ __device__ __forceinline__ void scale_role(const Params& p, Small& sm) {
 }
 
 template <int HD, int G>
-__device__ __forceinline__ void widen_role(const Params& p, Small& sm, const uint8_t* ring, uint8_t* kbuf, uint8_t* vbuf) {
+__device__ __forceinline__ void widen_role(const Params& p, Small& sm, const uint8_t* ring, uint8_t* kbuf,
+                                           uint8_t* vbuf) {
   using Ti = Tile<HD>;
   constexpr int BN = Ti::BN, NC = HD / 16, SB = Ti::SB;
   const int wt = threadIdx.x - kRowWarps * 32, lane = threadIdx.x & 31;
@@ -701,7 +707,6 @@ __device__ __forceinline__ void mma_role(const Params& p, Small& sm, uint32_t q,
     if (!ok) set_guard(p.guard, kGuardWaitTimeout);
     return ok;
   };
-  Piece w;
   int ks = 0;
   bool ok = true;
 #pragma unroll 1
@@ -750,8 +755,8 @@ __device__ __forceinline__ void mma_role(const Params& p, Small& sm, uint32_t q,
 #pragma unroll 1
       for (int c = 0; c < BN / 32; ++c) {
         mma_ts(d, a + c * 32, b, id_o, c > 0);
-        mma_ts(d, a + c * 32 + 16, b, id_o, true);
-        mma_ts(d, a + c * 32 + 8, b + 2048 / 16, id_o, true);
+        mma_ts(d, a + c * 32 + 8, b, id_o, true);
+        mma_ts(d, a + c * 32 + 16, b + 2048 / 16, id_o, true);
         mma_ts(d, a + c * 32 + 24, b + 2048 / 16, id_o, true);
         b += 4096 / 16;
       }
@@ -844,17 +849,16 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
       tc::fence_after_sync();
       const bool moved = __any_sync(0xffffffffu, cf != 1.f);
       const uint64_t c2 = pack2(cf, cf), e2 = pack2(ef, ef);
-      constexpr int NG = NA == 64 ? 64 : 32;  // outputs at a time
 #pragma unroll
-      for (int c = 0; c < NA; c += NG) {
-        float v[NG];
-        tmem_ld<NG>(outs + ob * HD + c, v);
+      for (int c = 0; c < NA; c += 32) {
+        float v[32];
+        tc::tmem_ld32(outs + ob * HD + c, v);
         if (moved) {
 #pragma unroll
-          for (int i = 0; i < NG / 2; ++i) acc[c / 2 + i] = mul2(acc[c / 2 + i], c2);
+          for (int i = 0; i < 16; ++i) acc[c / 2 + i] = mul2(acc[c / 2 + i], c2);
         }
 #pragma unroll
-        for (int i = 0; i < NG / 2; ++i) acc[c / 2 + i] = fma2(pack2(v[2 * i], v[2 * i + 1]), e2, acc[c / 2 + i]);
+        for (int i = 0; i < 16; ++i) acc[c / 2 + i] = fma2(pack2(v[2 * i], v[2 * i + 1]), e2, acc[c / 2 + i]);
       }
       tc::fence_before_sync();
       __syncwarp();
@@ -871,9 +875,9 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
         const Step& m = sm.step[ks % kSteps];
         const int j0 = half * (NV / 16);  // the thread's first block
         const int edge = m.edge;
-        // A block's factors.  In a step that some row does not see all of, a scale of 0 or NaN goes into the scores, so
-        // that it does not meet the -infinity of the positions out of view (a NaN block makes all of a row's outputs NaN,
-        // whether it is K's or V's).
+        // A block's factors.  In a step that some row does not see all of, a scale of 0 or NaN goes into the scores,
+        // so that it does not meet the -infinity of the positions out of view (a NaN block makes all of a row's
+        // outputs NaN, whether it is K's or V's).
         auto factors = [&](int j, float& f, float& fv) {
           f = m.fk[j0 + j] * qf;
           fv = m.fv[j0 + j];
@@ -935,29 +939,25 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
         uint64_t sum2 = 0;
         const uint64_t nref = pack2(-ref, -ref), minus1 = pack2(-1.f, -1.f);
 #pragma unroll 1
-        for (int c = 0; c < NV; c += 32) {
-          float v[32];
-          tc::tmem_ld32(scores + buf * BN + c, v);
-          float f[2], fv[2];
-          factors(c / 16, f[0], fv[0]);
-          factors(c / 16 + 1, f[1], fv[1]);
-          uint32_t pr[32];
+        for (int c = 0; c < NV; c += 16) {  // a block's 16 scores become 8 columns of high and 8 of low parts
+          float v[16], f, fv;
+          tmem_ld16(scores + buf * BN + c, v);
+          factors(c / 16, f, fv);
+          const uint64_t f2 = pack2(f, f), fv2 = pack2(fv, fv);
+          uint32_t pr[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int h = i / 8;
+          for (int i = 0; i < 8; ++i) {
             float p0, p1, w0, w1, l0, l1;
-            unpack2(fma2(pack2(v[2 * i], v[2 * i + 1]), pack2(f[h], f[h]), nref), p0, p1);
-            p0 = ex2(p0);
-            p1 = ex2(p1);
-            const uint64_t pp = pack2(p0, p1), f2 = pack2(fv[h], fv[h]);
+            unpack2(fma2(pack2(v[2 * i], v[2 * i + 1]), f2, nref), p0, p1);
+            const uint64_t pp = pack2(ex2(p0), ex2(p1));
             sum2 = add2(sum2, pp);
-            unpack2(mul2(pp, f2), w0, w1);
+            unpack2(mul2(pp, fv2), w0, w1);
             const float h0 = trunc11(w0), h1 = trunc11(w1);
             unpack2(fma2(pack2(h0, h1), minus1, pack2(w0, w1)), l0, l1);  // w - h, exact
             pr[i] = half2_bits(h0, h1);
-            pr[16 + i] = half2_bits(l0, l1);
+            pr[8 + i] = half2_bits(l0, l1);
           }
-          tmem_st32(scores + buf * BN + c, pr);
+          tmem_st16(scores + buf * BN + c, pr);
         }
         step_ev = m.ev;
         wait_st();
