@@ -339,7 +339,7 @@ __device__ __forceinline__ bool try_bar(uint64_t* bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
-constexpr int kTries = 1 << 22;  // bounds every wait: a few seconds
+constexpr int kTries = 1 << 20;  // bounds every wait: two seconds at most
 // A thread's wait.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1

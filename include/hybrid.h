@@ -535,7 +535,8 @@ int hy_op_kv_append_q4(const float* y_dev, int32_t ldy, int32_t n, void* Kq_dev,
  * block closes.  Sequences may share pages that no call writes.  The capacity
  * is max_pages * page_tokens positions; it and all pages are the caller's.
  * A page id outside [0, pool_pages) that a call needs sets HY_GUARD_BAD_INDEX:
- * nothing is written there, and its rows are left out of the attention. */
+ * nothing is written there, and its rows are left out of the attention (but for
+ * a block that the same decode call closes). */
 typedef struct {
   void* k_codes;        /* int8: page p, kv head h, row r of the page at + p * page_stride + (h * page_tokens + r) * hd */
   void* v_codes;        /* (bytes; both 16-byte aligned) */
@@ -598,7 +599,9 @@ int hy_op_attention_p8(const float* y_dev, int32_t ldy, int32_t batch, const hy_
  * hy_op_attention_p8.  workspace_dev: hy_op_attention_p8_prompt_workspace()
  * bytes, 16-byte aligned, no zeroing needed, its contents meaningless between
  * calls; calls that can overlap on the GPU need one each.  [Strata] "Act 1"
- * (one launch per layer for all prompt tokens). */
+ * (one launch per layer for all prompt tokens).
+ * HY_ERR_UNSUPPORTED, with nothing launched, where (n nq / (128 nkv) + batch) *
+ * (positions in view / 64 + 2) * nkv is above 2^31. */
 size_t hy_op_attention_p8_prompt_workspace(int32_t n, int32_t batch, int32_t nq, int32_t nkv, int32_t hd);
 int hy_op_attention_p8_prompt(const float* y_dev, int32_t ldy, int32_t n, int32_t batch, const int32_t* row_start_dev,
                               const hy_kv_p8* kv, int32_t nq, int32_t nkv, int32_t hd, int32_t window, int32_t sinks,

@@ -505,3 +505,164 @@ def test_prompt_and_steps_together(L):
             w.hist[b] = w.all_rows(b)
             w.lens[b] += 1
     assert guard(L) == 0
+
+
+# ------------------------------------------------------------------ every row once
+def equal_weights(nq, nkv, hd, lens, n=None, **kw):
+    """q = 0 and V of +-127: all rows in view weigh the same, V's codes and sums are exact, and the output is their mean."""
+    w = World(nq, nkv, hd, lens, n, **kw)
+    rng = w.rng
+    for b, T in enumerate(w.lens):
+        w.hist[b][1] = 127 * (2 * rng.integers(0, 2, w.hist[b][1].shape) - 1)
+    w.y[:, :nq * hd] = 0
+    v = w.y[:, (nq + nkv) * hd:(nq + 2 * nkv) * hd]
+    v[:] = 127 * (2 * rng.integers(0, 2, v.shape) - 1)
+    return w.fill()
+
+
+def check_means(w):
+    """sum / n with the reciprocal and the product rounded once each (2^-24 of the value each): below 2^-22."""
+    w.t.cuda.synchronize()
+    nq, nkv, hd = w.nq, w.nkv, w.hd
+    got = w.o.cpu().numpy()[:, :nq * hd].reshape(-1, nkv, nq // nkv, hd)
+    for b in range(w.B):
+        v = w.all_rows(b)[1].astype(np.float64)  # [nkv, T + n, hd]
+        csum = np.concatenate([np.zeros((nkv, 1, hd)), v.cumsum(1)], 1)
+        for i in range(w.n[b]):
+            t = w.lens[b] + i
+            lo = max(0, t - w.window + 1) if w.window else 0
+            s = min(w.sinks, lo) if w.window else 0
+            mean = (csum[:, t + 1] - csum[:, lo] + csum[:, s]) / (t + 1 - lo + s)
+            err = np.abs(got[w.start[b] + i] - mean[:, None])
+            assert (err <= 2.0 ** -22 * np.abs(mean[:, None])).all(), (b, i, err.max())
+
+
+@pytest.mark.parametrize("nq,nkv,hd", [(4, 2, 64), (16, 4, 128), (8, 1, 128), (16, 2, 256), (4, 2, 256), (8, 8, 128)])
+@pytest.mark.parametrize("lens,window,sinks", [([0], 0, 0), ([40000], 0, 0), ([9000, 17, 3333, 128, 2047], 0, 0),
+                                               ([9000, 17, 3333, 128, 2047, 700], 500, 20), ([20000] * 3, 12345, 100)])
+def test_decode_takes_every_row_once(L, nq, nkv, hd, lens, window, sinks):
+    w = equal_weights(nq, nkv, hd, lens, page=64, window=window, sinks=sinks)
+    ws = w.workspace(L)
+    assert w.decode(L, ws) == capi.HY_OK
+    check_means(w)
+
+
+@pytest.mark.parametrize("nq,nkv,hd", [(4, 2, 64), (16, 4, 128), (8, 1, 128), (16, 2, 256), (4, 2, 256), (8, 8, 128)])
+@pytest.mark.parametrize("lens,n,window,sinks", [([0], [300], 0, 0), ([5000], [3], 0, 0), ([1000, 17, 133, 128], [70, 200, 1, 33], 0, 0),
+                                                 ([3000, 17, 133, 128], [70, 200, 1, 33], 500, 20), ([2000], [700], 129, 17)])
+def test_prompt_takes_every_row_once(L, nq, nkv, hd, lens, n, window, sinks):
+    w = equal_weights(nq, nkv, hd, lens, n, page=64, window=window, sinks=sinks)
+    ws = w.workspace(L, prompt=True)
+    assert w.append(L) == capi.HY_OK
+    assert w.prompt(L, ws) == capi.HY_OK
+    check_means(w)
+
+
+# ------------------------------------------------------------------ as programs call them
+def test_same_bits_again(L):
+    """Nothing depends on the order in which CTAs arrive."""
+    t = pytest.importorskip("torch")
+    w = World(16, 4, 128, [5000, 300, 47], page=64).fill()
+    ws = w.workspace(L)
+    assert w.decode(L, ws) == capi.HY_OK
+    t.cuda.synchronize()
+    first = w.o.clone()
+    for _ in range(10):
+        assert w.decode(L, ws) == capi.HY_OK
+        t.cuda.synchronize()
+        assert t.equal(first, w.o)
+    w = World(16, 4, 128, [900, 300], [500, 40], page=64).fill()
+    ws = w.workspace(L, prompt=True)
+    assert w.append(L) == capi.HY_OK and w.prompt(L, ws) == capi.HY_OK
+    t.cuda.synchronize()
+    first = w.o.clone()
+    for _ in range(10):
+        assert w.prompt(L, ws) == capi.HY_OK
+        t.cuda.synchronize()
+        assert t.equal(first, w.o)
+
+
+@pytest.mark.parametrize("nq,nkv,hd", [(4, 2, 64), (16, 4, 128), (16, 2, 256)])
+def test_decode_without_values_unaligned(L, nq, nkv, hd):
+    """kv_new null; y and o at addresses of no alignment of their own."""
+    w = World(nq, nkv, hd, [33, 15, 500], page=32, pad_y=1, pad_o=1).fill()
+    t = w.t
+    y = t.empty(w.d["y"].numel() + 1, device="cuda")[1:].view_as(w.d["y"]).copy_(w.d["y"])
+    o = t.full((w.o.numel() + 1,), -77.0, device="cuda")[1:].view_as(w.o)
+    before = w.snapshot()
+    ws = w.workspace(L)
+    assert w.decode(L, ws, new=False, y=y.data_ptr(), o=o.data_ptr()) == capi.HY_OK
+    w.check_append(before, new=False)
+    w.o = o
+    w.check_attention()
+
+
+def test_prompt_captured_and_on_two_streams(L):
+    """Append and prompt attention in one graph each, replayed on two streams at once with new rows."""
+    t = pytest.importorskip("torch")
+    worlds = [World(8, 2, 128, [40, 0], [200, 33], page=32, seed=s).fill() for s in (1, 2)]
+    graphs = []
+    for w in worlds:
+        w.ws = w.workspace(L, prompt=True)
+        assert w.append(L) == capi.HY_OK and w.prompt(L, w.ws) == capi.HY_OK
+        t.cuda.synchronize()
+        g = t.cuda.CUDAGraph()
+        with t.cuda.graph(g):
+            assert w.append(L) == capi.HY_OK and w.prompt(L, w.ws) == capi.HY_OK
+        graphs.append(g)
+    streams = [t.cuda.Stream(), t.cuda.Stream()]
+    for _ in range(3):
+        for w in worlds:
+            w.y[:] = w.rng.standard_normal(w.y.shape).astype(np.float32)
+            w.d["y"].copy_(t.from_numpy(w.y))
+            # the tail's old rows again: the last replay's open block has taken their place
+            for b, T in enumerate(w.lens):
+                rest = w.hist[b][:, :, T // BLOCK * BLOCK:]
+                tl = w.d["tail"][b * w.ts:b * w.ts + 2 * w.nkv * BLOCK * w.hd].view(2, w.nkv, BLOCK, w.hd)
+                tl[:, :, :T % BLOCK] = t.from_numpy(rest.copy()).cuda().bfloat16()
+            w.o.fill_(-77.0)
+        t.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with t.cuda.stream(s):
+                g.replay()
+        t.cuda.synchronize()
+        for w in worlds:
+            w.check_attention(sample=8)
+
+
+def test_prompt_of_many_sequences(L):
+    """256 sequences of up to three rows, some with none."""
+    n = [i % 4 for i in range(256)]
+    w = World(4, 2, 64, [(37 * i) % 300 for i in range(256)], n, page=16).fill()
+    before = w.snapshot()
+    ws = w.workspace(L, prompt=True)
+    assert w.append(L) == capi.HY_OK
+    w.check_append(before)
+    assert w.prompt(L, ws) == capi.HY_OK
+    w.check_attention()
+    assert guard(L) == 0
+
+
+def test_prompt_pages_past_32_bits(L):
+    nq, nkv, hd, page = 4, 2, 64, 128
+    far = (1 << 32) // (nkv * page * hd + 48) + 5
+    w = World(nq, nkv, hd, [300, 100], [40, 200], page=page, far_page=far).fill()
+    assert int(w.table[0, 0]) * w.ps > 2 ** 32
+    before = w.snapshot()
+    ws = w.workspace(L, prompt=True)
+    assert w.append(L) == capi.HY_OK and w.prompt(L, ws) == capi.HY_OK
+    w.check_append(before)
+    w.check_attention(sample=8)
+
+
+def test_decode_closes_a_block_without_a_page(L):
+    """The block that closes has no page: nothing is written, its rows are attended to all the same."""
+    w = World(8, 2, 64, [47, 31], page=16).fill()
+    w.table[0, 2] = w.pool + 5
+    w.d["table"].copy_(w.t.from_numpy(w.table))
+    before = w.snapshot()
+    ws = w.workspace(L)
+    assert w.decode(L, ws) == capi.HY_OK
+    assert guard(L) == capi.HY_GUARD_BAD_INDEX
+    w.check_append(before, lost={(0, 2)})
+    w.check_attention()

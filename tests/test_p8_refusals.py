@@ -98,8 +98,9 @@ def test_other_pointers(L):
         assert call(L, op, n=-1) == ARG
     for op in ("append", "decode"):
         assert call(L, op, new=A + 1) == ARG
-    # a list of tiles past its counters
+    # lists of tiles and of steps past their counters
     assert call(L, "decode", cache(max_pages=1 << 24), batch=256) == UNSUPPORTED
+    assert call(L, "prompt", cache(max_pages=1 << 24), n=1 << 20) == UNSUPPORTED
 
 
 def test_no_rows_do_nothing(L):
