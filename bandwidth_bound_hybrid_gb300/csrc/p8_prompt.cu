@@ -534,37 +534,56 @@ __device__ __forceinline__ void scale_role(const Params& p, Small& sm) {
 #pragma unroll 1
   for (int np = 0; next_piece(p, sm, np, w); ++np) {
     const int end = w.T + w.n, ob = end / kBlock;  // the open block, if end % 16
+    // Factors that bring the open block's K and V below 2^7, and back (at its step, which this warp comes to steps
+    // before the others do).
     float os[2] = {0.f, 0.f}, up[2] = {0.f, 0.f};
-    if (w.s1 == w.steps && end % kBlock != 0 && w.t1 / kBlock == ob) {
-      const uint16_t* tail = p.c.tail + w.b * p.c.tail_stride + (long long)w.g * kBlock * HD;
+    auto open_block = [&]() {
+      const uint4* tk =
+          reinterpret_cast<const uint4*>(p.c.tail + w.b * p.c.tail_stride + (long long)w.g * kBlock * HD);
+      const uint4* tv = tk + (long long)p.nkv * kBlock * HD / 8;
+      uint32_t a[2] = {0, 0};
       bool nan = false;
+      auto take = [&](uint4 x, int v) {
+        const uint32_t q[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t m = (q[i / 2] >> (16 * (i & 1))) & 0x7fffu;
+          if (m < 0x7f80u)
+            a[v] = max(a[v], m);
+          else
+            nan |= v == 1;
+        }
+      };
+#pragma unroll 1
+      for (int i0 = lane; i0 < (end % kBlock) * HD / 8; i0 += 128) {
+        uint4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool in = i0 + 32 * i < (end % kBlock) * HD / 8;
+          x[i] = in ? tk[i0 + 32 * i] : make_uint4(0, 0, 0, 0);
+          y[i] = in ? tv[i0 + 32 * i] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          take(x[i], 0);
+          take(y[i], 1);
+        }
+      }
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
-        uint32_t a = 0;
-#pragma unroll 1
-        for (int i = lane; i < (end % kBlock) * HD / 2; i += 32) {
-          const uint32_t x = reinterpret_cast<const uint32_t*>(tail + (long long)v * p.nkv * kBlock * HD)[i];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t m = (x >> (16 * h)) & 0x7fffu;
-            if (m < 0x7f80u)
-              a = max(a, m);
-            else
-              nan |= v == 1;
-          }
-        }
-        a = __reduce_max_sync(0xffffffffu, a);
-        const int e = min(6 + 127 - (int)(a >> 7), 100);
+        const int e = min(6 + 127 - (int)(__reduce_max_sync(0xffffffffu, a[v]) >> 7), 100);
         up[v] = pow2(e);
         os[v] = pow2(-e);
       }
       if (nan) sm.open_nan = 1;
-    }
+    };
     const int* table = p.c.table + (long long)w.b * p.c.max_pages;
 #pragma unroll 1
     for (int s = w.s0; s < w.s1; ++s, ++ks) {
       int u = INT_MAX, kind = 1;
       float fk = 0.f, fv = 0.f;
+      // (the open block is the view's last, if the tile comes to it)
+      if (s == w.steps - 1 && end % kBlock != 0 && w.t1 / kBlock == ob) open_block();
       const int i = s * NBLK + lane;
       if (lane < NBLK && i < w.view.n) {
         const int blk = block_at(w.view, i), at = blk / p.c.bpp, off = blk - at * p.c.bpp;
@@ -655,17 +674,21 @@ __device__ __forceinline__ void widen_role(const Params& p, Small& sm, const uin
         if (odd) {
           if (!wait_all(p, &sm.mfull[step % kSteps], (step / kSteps) & 1)) return false;
           const Step& m = sm.step[step % kSteps];
+          const uint16_t* rows = tail + (long long)v * p.nkv * kBlock * HD + c * 16;
 #pragma unroll 1
           for (int u = 0; u < Ti::NP; ++u) {
             const int r = i * (SB * kBlock) + r0 + u * kStep, kind = m.kind[r / kBlock];
             if (kind == 0) continue;
+            uint4 y[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};  // rows of the tail that are there
+            if (kind == 2 && r % kBlock < open_rows) {
+              y[0] = reinterpret_cast<const uint4*>(rows + (r % kBlock) * HD)[0];
+              y[1] = reinterpret_cast<const uint4*>(rows + (r % kBlock) * HD)[1];
+            }
+            const uint32_t z[8] = {y[0].x, y[0].y, y[0].z, y[0].w, y[1].x, y[1].y, y[1].z, y[1].w};
             uint32_t h[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {  // rows of the tail that are there; V's NaN as 0 (see the outputs)
-              uint32_t q = 0;
-              if (kind == 2 && r % kBlock < open_rows)
-                q = reinterpret_cast<const uint32_t*>(tail + (long long)v * p.nkv * kBlock * HD + (r % kBlock) * HD +
-                                                      c * 16)[k];
+            for (int k = 0; k < 8; ++k) {  // V's NaN as 0 (see the outputs)
+              uint32_t q = z[k];
               if (v && (q & 0x7f80u) == 0x7f80u) q &= 0xffff0000u;
               if (v && (q & 0x7f800000u) == 0x7f800000u) q &= 0xffffu;
               h[k] = half2_bits(bf16_lo(q) * m.up[v], bf16_hi(q) * m.up[v]);
