@@ -30,6 +30,11 @@
 //   R = max_i r_i,  o = sum_i 2^(r_i - R) o_i / sum_i 2^(r_i - R) l_i
 // without any CTA waiting: the last of each 24 sharers to arrive joins the 24,
 // and the last of those joins the rest.
+//
+// Measured (4 kv heads x 128, 16 query heads): 8 sequences of 120k-131k rows in
+// 170 to 180 us, 5.7 to 6.05 TB/s of a measured copy's 6.8, with 63% of the issue
+// slots taken (widening: 5 operations for 4 codes); one of 4096 rows in 11.5 us,
+// a chain of latencies.
 #include "p8_dev.cuh"
 
 namespace hy {
