@@ -356,8 +356,7 @@ __device__ __forceinline__ bool wait_all(const Params& p, uint64_t* bar, uint32_
   set_guard(p.guard, kGuardWaitTimeout);
   return false;
 }
-// The pieces of this CTA's span, in order, by one warp for all roles (what a launch runs of its code it has to load, at
-// about 4 bytes a cycle: 60 KB take 8 us).
+// The pieces of this CTA's span, in order, by one warp for all roles.
 template <int HD, int G>
 __device__ __forceinline__ void piece_role(const Params& p, Small& sm) {
   Piece w = {sm.b, sm.g, sm.i0, sm.tile};
@@ -637,9 +636,9 @@ __device__ __forceinline__ void widen_role(const Params& p, Small& sm, const uin
   using Ti = Tile<HD>;
   constexpr int BN = Ti::BN, NC = HD / 16, SB = Ti::SB;
   const int wt = threadIdx.x - kRowWarps * 32, lane = threadIdx.x & 31;
-  // This thread's 16-byte pieces of a slot: piece c of row r0 + 2 u kPairs.  A pair of rows is taken by 2 NC threads
-  // so that 8 consecutive ones load from and store to eight bank groups (of two adjacent rows, one stores to the even
-  // chunks of the 128 bytes, the other to the odd ones).
+  // This thread's 16-byte pieces of a slot: piece c of rows r0, r0 + kStep, ...  A pair of rows is taken by 2 NC
+  // threads so that 8 consecutive ones load from and store to eight bank groups (of two adjacent rows, one stores to
+  // the even chunks of the 128 bytes, the other to the odd ones).
   const int j = wt % (2 * NC), c = j % NC, r0 = wt / (2 * NC) * 2 + ((j / NC) ^ ((c >> 2) & 1));
   constexpr int kStep = 128 / NC;  // rows from one of a thread's pieces to the next
   Piece w;
@@ -816,7 +815,7 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
     if (named_barrier_or(9, kRowWarps * 32, !next_piece(p, sm, np, w))) break;
     // ------------------------------------------------ queries: warp `warp` rows 16 warp ..
     // normalised by 2^e with 2^e max |q| in [2^9, 2^10): as two fp16 parts q keeps 22 bits of the row's largest
-    // (8 lanes a row, 4 rows at a time: little code, since all of it misses the instruction cache at first)
+    // (8 lanes a row, 4 rows at a time)
     constexpr int PP = HD / 16;  // rotate-half pairs of a lane
     const int l8 = lane & 7;
 #pragma unroll 2
