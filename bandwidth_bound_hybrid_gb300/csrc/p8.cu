@@ -995,6 +995,13 @@ __global__ void __launch_bounds__(Shape<HD>::kThreads, Shape<HD>::kCtas) k_attn(
             s[n][0] = (d[0][2 * n] + d[1][2 * n]) + (d[0][2 * n + 1] + d[1][2 * n + 1]);
           }
         }
+        // (scaled, then masked: a factor of 0, of a block of zeros, would make NaN of -infinity)
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          const float f = fk * qf[h];
+          s[0][h] *= f;
+          s[1][h] *= f;
+        }
         if (is_last || (p.window > 0 && u0 <= T - p.window && u0 + kBlock > p.sinks)) {
 #pragma unroll
           for (int n = 0; n < 2; ++n)
@@ -1007,9 +1014,6 @@ __global__ void __launch_bounds__(Shape<HD>::kThreads, Shape<HD>::kCtas) k_attn(
         float mn[NH];
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          const float f = fk * qf[h];
-          s[0][h] *= f;
-          s[1][h] *= f;
           float tm = fmaxf(s[0][h], s[1][h]);
           tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 4));
           tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 8));
