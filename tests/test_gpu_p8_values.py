@@ -1,4 +1,5 @@
-"""The paged 8-bit KV cache's attention over keys and values of unlike sizes: zero and tiny ones.
+"""The paged 8-bit KV cache's attention over keys and values of unlike sizes: zero, tiny and
+large ones.
 
 Against the plain form of tests/p8_util.py with its tolerances; every output is first checked to be finite, as a comparison
 with a bound does not fail for NaN."""
@@ -89,3 +90,30 @@ def test_zero_queries_over_zero_keys(L, nq, nkv, hd, qmul, kmul, vmul):
     """Queries and keys of zero or nearly: the mean of V in view (an idle slot, a first call on zeroed inputs)."""
     decode(L, World(nq, nkv, hd, [0, 5, 15, 16, 20, 100], page=16, qmul=qmul, kmul=kmul, vmul=vmul))
     prompt(L, World(nq, nkv, hd, [0, 5, 16, 100], [1, 7, 30, 12], page=16, qmul=qmul, kmul=kmul, vmul=vmul))
+
+
+def one_hot(nq, nkv, hd, T, n, size):
+    """Scores of up to 2^size, all far apart: no rotation, q and K along one axis, K's values a permutation of 0 .. 100
+    and their multiples."""
+    w = World(nq, nkv, hd, [T], n and [n], page=16)
+    w.rope[..., 0], w.rope[..., 1] = 1, 0
+    w.y[:, :(nq + nkv) * hd] = 0
+    a = 2.0 ** ((size - 7) // 2)
+    w.y[:, :nq * hd:hd] = a * np.where(np.arange(nq) % 2, -1, 1)
+    val = (np.arange(T + (n or 1)) * 37 % 101 * a).astype(np.float32)
+    w.hist[0][K] = 0
+    w.hist[0][K, :, :, 0] = val[:T]
+    w.y[:, nq * hd:(nq + nkv) * hd:hd] = val[T:, None]
+    return w
+
+
+@pytest.mark.parametrize("nq,nkv,hd", SHAPES)
+@pytest.mark.parametrize("size", [21, 27, 31, 41, 61, 101])
+def test_large_scores(L, nq, nkv, hd, size):
+    """One row has all of the weight (largest or smallest K, by the query's sign): no overflow on the way there.
+
+    The values of K are 1/100 of the largest apart and a block's codes move them by at most 1/254 of it, so two never meet.  The
+    largest score is at least 2^(size - 4), so scores differ by 2^(size - 4) (0.01 - 2/254) > 2^(size - 13), and FP32 errs by
+    at most 2 gamma(2 hd + 16) of the largest, 2^(size - 14) / 2^4."""
+    decode(L, one_hot(nq, nkv, hd, 99, None, size))
+    prompt(L, one_hot(nq, nkv, hd, 60, 40, size))
