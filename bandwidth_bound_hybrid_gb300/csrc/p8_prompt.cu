@@ -5,9 +5,13 @@
 // rows with their G heads.  It goes over the blocks that any of its rows sees,
 // BN positions a step, with the running maximum and sum of a softmax:
 //   S = (q_hi + q_lo) cK^T,   w = 2^(s sK - m) sV 2^(14 - E),   O = (w_hi + w_lo) cV
-// q and w as two fp16 parts (22 bits; w down to 2^-39 of the step's largest V
-// scale), the codes exact in fp16, the blocks' scales FP32 factors of a score
-// and of the weight that meets a block of V (2^E above the step's largest).
+// q and w as two fp16 parts (22 bits; w to 2^-39 of 2^E), the codes exact in
+// fp16, the blocks' scales FP32 factors of a score and of the weight that meets
+// a block of V.  2^E is above the step's largest V scale where the step's are
+// within 2^4 of each other.  Where they are not ("wide" steps), a block that a
+// row does not see, or hardly weighs, must not decide how finely the others
+// enter: there a row takes its own E, with 2^E up to 4 times the largest of its
+// products 2^(s sK - m) sV.
 // A step's O is added to the outputs in registers, in FP32: the tensor cores
 // truncate what they add to an accumulator, which over a long context would be
 // 2^-24 a product, all one way.
@@ -83,11 +87,12 @@ constexpr int kPieces = 4;  // of them at a time
 // What the row and widening warps need of a step.
 constexpr int kSteps = 8;  // of them at a time
 struct Step {
-  float fk[8], fv[8];  // scales of K; of V times 2^(14 - E)
+  float fk[8], fv[8];  // scales of K; of V times 2^(14 - E) (wide: as they are)
   int u[8];            // first positions of the blocks; INT_MAX: not there
   int kind[8];         // 0: codes in the ring, 1: nothing (zeros), 2: the open block
   float ev;            // 2^(E - 14)
   int edge;            // some row does not see all of it
+  int wide;            // V's scales are so far apart that each row takes its own E
   float up[2];         // factors that bring the open block's K and V below 2^7
 };
 
@@ -101,6 +106,7 @@ struct alignas(16) Small {
   Piece piece[kPieces];
   float qf[128];
   float mx[2][2][128];
+  float top[2][128];  // of a wide step: log2 of the largest product of weight and V scale
   float ls[2][128];
   // the work
   int T[kMaxB], n[kMaxB], first[kMaxB];
@@ -258,6 +264,8 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 // v truncated to fp16's 11 significant bits: v - trunc11(v) is exact
 __device__ __forceinline__ float trunc11(float v) { return __uint_as_float(__float_as_uint(v) & 0xffffe000u); }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// the least n with 2^n > v, for v from 2^-126; -126 below, 129 for NaN
+__device__ __forceinline__ float log2_above(float v) { return (float)((int)(__float_as_uint(v) >> 23 & 255) - 126); }
 
 // ---------------------------------------------------------------- tcgen05 forms
 // fp16 operands, FP32 accumulator; trans_b: B is MN-major.
@@ -605,7 +613,9 @@ __device__ __forceinline__ void scale_role(const Params& p, Small& sm) {
         }
       }
       const uint32_t top = __reduce_max_sync(0xffffffffu, fv == fv ? __float_as_uint(fv) : 0u);
-      const int E = top ? (int)(top >> 23) - 126 : 0;  // 2^E above the largest
+      const uint32_t low = __reduce_min_sync(0xffffffffu, fv > 0.f ? __float_as_uint(fv) : ~0u);
+      const bool wide = top && (top >> 23) - (low >> 23) > 3;
+      const int E = top && !wide ? (int)(top >> 23) - 126 : wide ? 14 : 0;  // 2^E above the largest
       const bool full = lane >= NBLK || (u != INT_MAX && u + kBlock - 1 <= w.t0 &&
                                          (p.window <= 0 || u > w.t1 - p.window || u + kBlock <= p.sinks));
       const bool edge = !__all_sync(0xffffffffu, full);
@@ -621,6 +631,7 @@ __device__ __forceinline__ void scale_role(const Params& p, Small& sm) {
       if (lane == 0) {
         m.ev = pow2(E - 14);
         m.edge = edge;
+        m.wide = wide;
         m.up[0] = up[0];
         m.up[1] = up[1];
       }
@@ -952,7 +963,7 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
           }
         }
         sm.mx[buf][half][row] = top;
-        named_barrier(1 + sub, 64);
+        const bool wide = named_barrier_or(1 + sub, 64, m.wide != 0);  // (the same for both halves, whatever m holds)
         top = fmaxf(top, sm.mx[buf][half ^ 1][row]);
         const float mn = fmaxf(mx, top), ref = mn == -INFINITY ? 0.f : mn;
         cf = mx == mn ? 1.f : ex2(mx - mn);
@@ -963,12 +974,34 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
         // From about 2^25 on a score's rounding in the maximum is worth factors of 2, and an unrounded product less the
         // maximum gives weights above 1 that no longer fit fp16: there each product is rounded as the maximum was.  (A loop
         // of its own: a choice within the other one costs 2048 rows of 4 x 128 3%.)
-        if (__any_sync(0xffffffffu, fabsf(ref) >= 1048576.f)) {
+        step_ev = m.ev;
+        if (wide || __any_sync(0xffffffffu, fabsf(ref) >= 1048576.f)) {
+          float up = 1.f;  // 2^(14 - E) of a row in a wide step
+          if (wide) {
+            float g = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < NV; c += 16) {
+              float v[16], f, fv;
+              tmem_ld16(scores + buf * BN + c, v);
+              factors(c / 16, f, fv);
+#pragma unroll
+              for (int i = 1; i < 16; ++i) v[0] = fmaxf(v[0], v[i]);
+              g = fmaxf(g, __fsub_rn(__fmul_rn(v[0], f), ref) + log2_above(fv));
+            }
+            sm.top[half][row] = g;
+            named_barrier(1 + sub, 64);
+            const int e = (int)ceilf(fmaxf(fmaxf(g, sm.top[half ^ 1][row]), -110.f));
+            up = pow2(14 - e);
+            step_ev = pow2(e - 14);
+          }
 #pragma unroll 1
           for (int c = 0; c < NV; c += 16) {
             float v[16], f, fv;
             tmem_ld16(scores + buf * BN + c, v);
             factors(c / 16, f, fv);
+            // (bounded for blocks out of view, whose weights are 0; in view what it bounds has weights below 2^-86)
+            fv *= up;
+            if (fv > 0x1p100f) fv = 0x1p100f;
             uint32_t pr[16];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -1008,7 +1041,6 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
             tmem_st16(scores + buf * BN + c, pr);
           }
         }
-        step_ev = m.ev;
         wait_st();
         tc::fence_before_sync();
         __syncwarp();
