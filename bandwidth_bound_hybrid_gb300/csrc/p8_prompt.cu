@@ -11,7 +11,8 @@
 // within 2^4 of each other.  Where they are not ("wide" steps), a block that a
 // row does not see, or hardly weighs, must not decide how finely the others
 // enter: there a row takes its own E, with 2^E up to 4 times the largest of its
-// products 2^(s sK - m) sV.
+// products 2^(s sK - m) sV.  The open block's rows are fp16 under a power of two,
+// one for all of them or, where they are far apart, one each.
 // A step's O is added to the outputs in registers, in FP32: the tensor cores
 // truncate what they add to an accumulator, which over a long context would be
 // 2^-24 a product, all one way.
@@ -93,7 +94,12 @@ struct Step {
   float ev;            // 2^(E - 14)
   int edge;            // some row does not see all of it
   int wide;            // V's scales are so far apart that each row takes its own E
-  float up[2];         // factors that bring the open block's K and V below 2^7
+  // What brings the open block's rows below 2^15 (K) and, as codes are, 2^7 (V).  Rows of about one size share one
+  // power of two, and its inverses are in fk and fv.  Rows far apart, which must not take bits from one another, have one
+  // each: then `open` is the block (else -1, and rk and rv are not read), the step is wide, a row's scale is fk rk for K
+  // and rv for V (0: no row, or one of zeros).
+  float uk[kBlock], uv[kBlock], rk[kBlock], rv[kBlock];
+  int open;
 };
 
 struct alignas(16) Small {
@@ -541,64 +547,77 @@ __device__ __forceinline__ void scale_role(const Params& p, Small& sm) {
 #pragma unroll 1
   for (int np = 0; next_piece(p, sm, np, w); ++np) {
     const int end = w.T + w.n, ob = end / kBlock;  // the open block, if end % 16
-    // Factors that bring the open block's K and V below 2^7, and back (at its step, which this warp comes to steps
-    // before the others do).
-    float os[2] = {0.f, 0.f}, up[2] = {0.f, 0.f};
-    auto open_block = [&]() {
-      const uint4* tk =
-          reinterpret_cast<const uint4*>(p.c.tail + w.b * p.c.tail_stride + (long long)w.g * kBlock * HD);
+    // The powers of two of the open block's rows (at its step, which this warp comes to steps before the others do).
+    // Returns whether the rows are far apart; top and low take their V scales, fk and fv are those of the block.
+    auto open_block = [&](Step& m, uint32_t& top, uint32_t& low, float& fk, float& fv) {
+      const int row = lane / 2, rows = end % kBlock;  // half a row a lane
+      const uint4* tk = reinterpret_cast<const uint4*>(p.c.tail + w.b * p.c.tail_stride +
+                                                       ((long long)w.g * kBlock + row) * HD + lane % 2 * (HD / 2));
       const uint4* tv = tk + (long long)p.nkv * kBlock * HD / 8;
-      uint32_t a[2] = {0, 0};
-      bool nan = false;
-      auto take = [&](uint4 x, int v) {
-        const uint32_t q[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t m = (q[i / 2] >> (16 * (i & 1))) & 0x7fffu;
-          if (m < 0x7f80u)
-            a[v] = max(a[v], m);
-          else
-            nan |= v == 1;
-        }
+      // the largest finite |x| of pairs, low and high halves; others are noted
+      uint32_t a = 0, b = 0, none = 0, nan = 0;
+      auto take = [](uint32_t& most, uint32_t x, uint32_t& bad) {
+        const uint32_t m = x & 0x7fff7fffu, is = __vcmpgtu2(m, 0x7f7f7f7fu);
+        bad |= is;
+        most = __vmaxu2(most, m & ~is);
       };
 #pragma unroll 1
-      for (int i0 = lane; i0 < (end % kBlock) * HD / 8; i0 += 128) {
-        uint4 x[4], y[4];
+      for (int i0 = 0; i0 < HD / 16 && row < rows; i0 += 2) {
+        uint4 x[2], y[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool in = i0 + 32 * i < (end % kBlock) * HD / 8;
-          x[i] = in ? tk[i0 + 32 * i] : make_uint4(0, 0, 0, 0);
-          y[i] = in ? tv[i0 + 32 * i] : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 2; ++i) {
+          x[i] = tk[i0 + i];
+          y[i] = tv[i0 + i];
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          take(x[i], 0);
-          take(y[i], 1);
+        for (int i = 0; i < 2; ++i) {
+          take(a, x[i].x, none);
+          take(a, x[i].y, none);
+          take(a, x[i].z, none);
+          take(a, x[i].w, none);
+          take(b, y[i].x, nan);
+          take(b, y[i].y, nan);
+          take(b, y[i].z, nan);
+          take(b, y[i].w, nan);
         }
       }
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const int e = min(6 + 127 - (int)(__reduce_max_sync(0xffffffffu, a[v]) >> 7), 100);
-        up[v] = pow2(e);
-        os[v] = pow2(-e);
-      }
+      __syncwarp();
       if (nan) sm.open_nan = 1;
+      a = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));  // K's in the low half, V's in the high one
+      a = __vmaxu2(a, __shfl_xor_sync(0xffffffffu, a, 1));
+      b = a >> 16;
+      a &= 0xffffu;
+      // extremes over the rows that are not 0
+      const uint32_t hk = __reduce_max_sync(0xffffffffu, a), lk = __reduce_min_sync(0xffffffffu, a ? a : ~0u);
+      const uint32_t hv = __reduce_max_sync(0xffffffffu, b), lv = __reduce_min_sync(0xffffffffu, b ? b : ~0u);
+      auto factor = [](uint32_t m, int bits) { return min(bits - 1 + 127 - (int)(m >> 7), 100); };  // |bf16 m| to below 2^bits
+      const bool apart = (hk && (hk >> 7) - (lk >> 7) > 8) || (hv && (hv >> 7) - (lv >> 7) > 3);
+      const int ek = factor(hk, 15), rk = apart ? factor(a, 15) : ek, rv = factor(apart ? b : hv, 7);
+      if (lane % 2 == 0) {
+        m.uk[row] = pow2(rk);
+        m.uv[row] = pow2(rv);
+        m.rk[row] = ek - rk < -126 ? 0.f : pow2(ek - rk);
+        m.rv[row] = b ? pow2(-rv) : 0.f;
+      }
+      fk = pow2(-ek);
+      fv = hv && !apart ? pow2(-rv) : 0.f;
+      if (hv) {
+        top = max(top, __float_as_uint(pow2(-factor(hv, 7))));
+        low = min(low, __float_as_uint(pow2(-factor(apart ? lv : hv, 7))));
+      }
+      return apart;
     };
     const int* table = p.c.table + (long long)w.b * p.c.max_pages;
 #pragma unroll 1
     for (int s = w.s0; s < w.s1; ++s, ++ks) {
       int u = INT_MAX, kind = 1;
       float fk = 0.f, fv = 0.f;
-      // (the open block is the view's last, if the tile comes to it)
-      if (s == w.steps - 1 && end % kBlock != 0 && w.t1 / kBlock == ob) open_block();
       const int i = s * NBLK + lane;
       if (lane < NBLK && i < w.view.n) {
         const int blk = block_at(w.view, i), at = blk / p.c.bpp, off = blk - at * p.c.bpp;
         if (blk == ob) {
           u = blk * kBlock;
           kind = 2;
-          fk = os[0];
-          fv = os[1];
         } else {
           const int pg = __ldg(table + at);
           if ((unsigned)pg < (unsigned)p.c.pool_pages) {
@@ -612,16 +631,27 @@ __device__ __forceinline__ void scale_role(const Params& p, Small& sm) {
           }
         }
       }
-      const uint32_t top = __reduce_max_sync(0xffffffffu, fv == fv ? __float_as_uint(fv) : 0u);
-      const uint32_t low = __reduce_min_sync(0xffffffffu, fv > 0.f ? __float_as_uint(fv) : ~0u);
-      const bool wide = top && (top >> 23) - (low >> 23) > 3;
-      const int E = top && !wide ? (int)(top >> 23) - 126 : wide ? 14 : 0;  // 2^E above the largest
       const bool full = lane >= NBLK || (u != INT_MAX && u + kBlock - 1 <= w.t0 &&
                                          (p.window <= 0 || u > w.t1 - p.window || u + kBlock <= p.sinks));
       const bool edge = !__all_sync(0xffffffffu, full);
       const int sl = ks % kSteps;
       if (ks >= kSteps && !wait_all(p, &sm.mempty[sl], ((ks / kSteps) & 1) ^ 1)) return;
       Step& m = sm.step[sl];
+      uint32_t top = fv == fv ? __float_as_uint(fv) : 0u, low = fv > 0.f ? __float_as_uint(fv) : ~0u;
+      // (the open block is the view's last, if the tile comes to it)
+      bool apart = false;
+      if (s == w.steps - 1 && end % kBlock != 0 && w.t1 / kBlock == ob) {
+        float ok, ov = 0.f;
+        apart = open_block(m, top, low, ok, ov);
+        if (kind == 2) {
+          fk = ok;
+          fv = ov;
+        }
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      low = __reduce_min_sync(0xffffffffu, low);
+      const bool wide = apart || (top && (top >> 23) - (low >> 23) > 3);
+      const int E = top && !wide ? (int)(top >> 23) - 126 : wide ? 14 : 0;  // 2^E above the largest
       if (lane < NBLK) {
         m.fk[lane] = fk;
         m.fv[lane] = fv * pow2(14 - E);
@@ -632,8 +662,7 @@ __device__ __forceinline__ void scale_role(const Params& p, Small& sm) {
         m.ev = pow2(E - 14);
         m.edge = edge;
         m.wide = wide;
-        m.up[0] = up[0];
-        m.up[1] = up[1];
+        m.open = apart ? w.view.n - 1 - s * NBLK : -1;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.mfull[sl]);
@@ -695,13 +724,14 @@ __device__ __forceinline__ void widen_role(const Params& p, Small& sm, const uin
               y[1] = reinterpret_cast<const uint4*>(rows + (r % kBlock) * HD)[1];
             }
             const uint32_t z[8] = {y[0].x, y[0].y, y[0].z, y[0].w, y[1].x, y[1].y, y[1].z, y[1].w};
+            const float up = kind == 2 ? (v ? m.uv : m.uk)[r % kBlock] : 0.f;  // (not written without an open block)
             uint32_t h[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {  // V's NaN as 0 (see the outputs)
               uint32_t q = z[k];
               if (v && (q & 0x7f80u) == 0x7f80u) q &= 0xffff0000u;
               if (v && (q & 0x7f800000u) == 0x7f800000u) q &= 0xffffu;
-              h[k] = half2_bits(bf16_lo(q) * m.up[v], bf16_hi(q) * m.up[v]);
+              h[k] = half2_bits(bf16_lo(q) * up, bf16_hi(q) * up);
             }
             put16<BN>(tile, r, c, h);
           }
@@ -925,6 +955,15 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
         // the maximum, 32 scores at a time (loops, not unrolled over the step: the roles share the instruction cache);
         // what is out of view goes back as -infinity
         float top = -INFINITY;
+        if ((unsigned)(m.open - j0) < NV / 16) {  // rows with scales of their own
+          float v[16];
+          uint32_t w[16];
+          tmem_ld16(scores + buf * BN + (m.open - j0) * 16, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i] * m.rk[i]);
+          tmem_st16(scores + buf * BN + (m.open - j0) * 16, w);
+          wait_st();
+        }
 #pragma unroll 1
         for (int c = 0; c < NV; c += 32) {
           float v[32];
@@ -976,7 +1015,8 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
         // of its own: a choice within the other one costs 2048 rows of 4 x 128 3%.)
         step_ev = m.ev;
         if (wide || __any_sync(0xffffffffu, fabsf(ref) >= 1048576.f)) {
-          float up = 1.f;  // 2^(14 - E) of a row in a wide step
+          const int open = m.open - j0;  // the block whose rows have scales of their own, if it is among the thread's
+          float up = 1.f;                // 2^(14 - E) of a row in a wide step
           if (wide) {
             float g = -INFINITY;
 #pragma unroll 1
@@ -985,8 +1025,8 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
               tmem_ld16(scores + buf * BN + c, v);
               factors(c / 16, f, fv);
 #pragma unroll
-              for (int i = 1; i < 16; ++i) v[0] = fmaxf(v[0], v[i]);
-              g = fmaxf(g, __fsub_rn(__fmul_rn(v[0], f), ref) + log2_above(fv));
+              for (int i = 0; i < 16; ++i)
+                g = fmaxf(g, __fsub_rn(__fmul_rn(v[i], f), ref) + log2_above(c / 16 == open ? m.rv[i] : fv));
             }
             sm.top[half][row] = g;
             named_barrier(1 + sub, 64);
@@ -1000,8 +1040,8 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
             tmem_ld16(scores + buf * BN + c, v);
             factors(c / 16, f, fv);
             // (bounded for blocks out of view, whose weights are 0; in view what it bounds has weights below 2^-86)
-            fv *= up;
-            if (fv > 0x1p100f) fv = 0x1p100f;
+            auto bounded = [](float x) { return x > 0x1p100f ? 0x1p100f : x; };  // NaN stays
+            fv = bounded(fv * up);
             uint32_t pr[16];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -1009,7 +1049,7 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 x[k] = ex2(__fsub_rn(__fmul_rn(v[2 * i + k], f), ref));
-                w[k] = x[k] * fv;
+                w[k] = x[k] * (c / 16 == open ? bounded(m.rv[2 * i + k] * up) : fv);
                 h[k] = trunc11(w[k]);
               }
               sum2 = add2(sum2, pack2(x[0], x[1]));

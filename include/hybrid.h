@@ -599,8 +599,10 @@ int hy_op_attention_p8(const float* y_dev, int32_t ldy, int32_t batch, const hy_
  * hy_op_attention_p8, but that a probability p enters with the scale s of its
  * block of V: their product has 22 bits, with an absolute error of 2^-34 of the
  * larger of s times the row's largest p and the largest product p s among the
- * blocks of which the row sees some position.  Blocks that a row does not see
- * take nothing from it.  workspace_dev: hy_op_attention_p8_prompt_workspace()
+ * blocks of which the row sees some position; an open block's row counts as a
+ * block, and its K and V enter with an absolute error of 2^-30 (K) and 2^-27 (V)
+ * of the row's largest.  What a row does not see takes nothing from it.
+ * workspace_dev: hy_op_attention_p8_prompt_workspace()
  * bytes, 16-byte aligned, no zeroing needed, its contents meaningless between
  * calls; calls that can overlap on the GPU need one each.  [Strata] "Act 1"
  * (one launch per layer for all prompt tokens).

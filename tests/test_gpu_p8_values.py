@@ -247,3 +247,30 @@ def test_prompt_wide_steps_twice_and_nan(L):
     t = np.arange(400)
     sees = (t >= 128) & (t - 150 < 143)
     assert np.isnan(got[sees]).all() and np.isfinite(got[~sees]).all()
+
+
+@pytest.mark.parametrize("nq,nkv,hd", SHAPES)
+@pytest.mark.parametrize("which", [K, V])
+@pytest.mark.parametrize("mul", [2.0 ** -60, *FAR])
+def test_prompt_open_rows_out_of_view(L, nq, nkv, hd, which, mul):
+    """Rows of the open block, which are bf16 each for itself: later ones, or ones that the window has left, are of no matter."""
+    w = World(nq, nkv, hd, [0, 37, 100], [200, 9, 13], page=16)
+    for b, at in ((0, 198), (1, 45), (2, 112)):
+        scale_rows(w, b, which, at, at + 1, mul)
+    run_apart(L, w, sample=300)
+    w = World(nq, nkv, hd, [180, 5], [27, 10], page=16, window=5, sinks=1)
+    for b, at in ((0, 193), (1, 2), (1, 9)):
+        scale_rows(w, b, which, at, at + 1, mul)
+    run_apart(L, w, sample=300)
+
+
+@pytest.mark.parametrize("nq,nkv,hd", SHAPES)
+@pytest.mark.parametrize("span", [2, 20, 90])
+def test_prompt_open_rows_far_apart(L, nq, nkv, hd, span):
+    """V of every open row of a size of its own, beside closed blocks of one size; rows of zeros among them."""
+    w = World(nq, nkv, hd, [0, 37, 160], [95, 9, 15], page=16)
+    for b in range(3):
+        end = w.lens[b] + w.n[b]
+        for t in range(end // BLOCK * BLOCK, end):
+            scale_rows(w, b, V, t, t + 1, 0.0 if w.rng.random() < 0.1 else 2.0 ** int(w.rng.integers(-span, span + 1)))
+    run_apart(L, w)
