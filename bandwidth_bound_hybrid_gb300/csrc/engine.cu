@@ -2571,8 +2571,8 @@ int hy_op_attention_p8(const float* y_dev, int32_t ldy, int32_t batch, const hy_
   if (!aligned(o_dev) || !null_or_aligned(kv_new_dev) || !aligned16(workspace_dev) || window < 0 || sinks < 0 ||
       (long long)ldo < (long long)nq * hd)
     return fail(HY_ERR_ARG, "bad 8-bit paged attention arguments (ldo >= nq hd, window and sinks not negative)");
-  if ((long long)batch * nkv * p.c.max_pages * p.c.bpp > (1 << 30))  // the list of tiles
-    return fail(HY_ERR_UNSUPPORTED, "8-bit paged cache: batch x nkv x capacity above 2^34 rows");
+  if ((long long)batch * nkv * p8::most_blocks(p.c, window, sinks) > p8::kMaxTiles)
+    return fail(HY_ERR_UNSUPPORTED, "8-bit paged cache: batch x nkv x blocks in view above 2^30");
   int dev = 0, nsm = 0;
   if ((rc = op_guard(&p.guard)) != HY_OK || (rc = current_device(&dev, &nsm)) != HY_OK || (rc = ensure_p8(dev)) != HY_OK)
     return rc;

@@ -277,6 +277,14 @@ struct Params {
   unsigned* counter;            // zero between launches
   unsigned* guard;
 };
+constexpr long long kMaxTiles = 1 << 30;  // of a decode call: most_blocks for each sequence and kv head
+// The most blocks that a decode step of a sequence can have in view.
+inline long long most_blocks(const Cache& c, int window, int sinks) {
+  const long long all = (long long)c.max_pages * c.bpp;
+  if (window <= 0) return all;
+  const long long most = window / kBlock + 2ll + ((long long)sinks + kBlock - 1) / kBlock;
+  return most < all ? most : all;
+}
 size_t part_floats(int nq, int nkv, int hd, int nsm);
 size_t counters(int nb, int nkv);
 cudaError_t init();

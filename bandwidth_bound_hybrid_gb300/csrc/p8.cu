@@ -332,8 +332,8 @@ __device__ __forceinline__ uint32_t place(int r, int c) {
 // length a head, a CTA each; or (m = 0) the tiles themselves, in spans: CTA c
 // begins at tile c q + min(c, rem) (q = total / CTAs, rem = total % CTAs),
 // moved to the border of an item that is within `near` tiles (near <= q / 4, so
-// that the order of the CTAs stays).  The launch refuses caches of more than
-// 2^30 tiles.  These run in warp 0, all lanes alike unless said.
+// that the order of the CTAs stays).  A call with more than 2^30 tiles is
+// refused.  These run in warp 0, all lanes alike unless said.
 struct Item {
   int b, g, first, end;  // sequence, kv head, its units in the list
 };
@@ -1167,14 +1167,9 @@ cudaError_t attention(const Params& p, int hd, int nsm, cudaStream_t st) {
   if (p.nb < 1 || p.nb > kMaxB || p.nkv <= 0 || p.nq % p.nkv) return cudaErrorInvalidValue;
   const Pick k = pick(hd, p.nq / p.nkv);
   if (!k.k) return cudaErrorInvalidValue;
-  // the most blocks the sequences can have in view
-  long long per = (long long)p.c.max_pages * p.c.bpp;
-  if (p.window > 0) {
-    const long long most = p.window / kBlock + 2ll + ((long long)p.sinks + kBlock - 1) / kBlock;
-    if (most < per) per = most;
-  }
+  const long long per = most_blocks(p.c, p.window, p.sinks);
   const long long tiles = p.nkv * per * p.nb, chunks = p.nkv * ((per + k.warps - 1) / k.warps) * p.nb;
-  if (tiles > (1 << 30)) return cudaErrorInvalidValue;
+  if (tiles > kMaxTiles) return cudaErrorInvalidValue;
   long long grid = (long long)nsm * k.per_sm;
   if (grid > (kCounters - 1) * kJoin) grid = (kCounters - 1) * kJoin;  // what the joins can count
   if (grid > chunks) grid = chunks;

@@ -580,6 +580,9 @@ int hy_op_kv_append_p8(const float* y_dev, int32_t ldy, int32_t n, int32_t batch
  * queries and probabilities enter the products with 22 bits, with an absolute
  * error of 2^-34 of the head's largest |q| and 2^-39 of its largest
  * probability.  The work is shared over the GPU by rows in view.
+ * HY_ERR_UNSUPPORTED, with nothing launched, where batch * nkv * blocks is above
+ * 2^30, blocks being those of the capacity or, with a window, at most window / 16
+ * + 2 and the sinks' (rounded up).
  * workspace_dev: hy_op_attention_p8_workspace() bytes (0 for bad shapes or
  * without a usable GPU), zeroed before its first use and then passed
  * unmodified to later calls of the same batch, nq, nkv and hd; calls that can
