@@ -1011,8 +1011,9 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
         uint64_t sum2 = 0;
         const uint64_t nref = pack2(-ref, -ref), minus1 = pack2(-1.f, -1.f);
         // From about 2^25 on a score's rounding in the maximum is worth factors of 2, and an unrounded product less the
-        // maximum gives weights above 1 that no longer fit fp16: there each product is rounded as the maximum was.  (A loop
-        // of its own: a choice within the other one costs 2048 rows of 4 x 128 3%.)
+        // maximum gives weights above 1 that no longer fit fp16: there, and in wide steps, each product is rounded as the
+        // maximum was.  (A loop of its own: a choice within the other one costs 2048 rows of 4 x 128 3%; all steps wide
+        // take them 242 us instead of 199.)
         step_ev = m.ev;
         if (wide || __any_sync(0xffffffffu, fabsf(ref) >= 1048576.f)) {
           const int open = m.open - j0;  // the block whose rows have scales of their own, if it is among the thread's
@@ -1024,9 +1025,15 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
               float v[16], f, fv;
               tmem_ld16(scores + buf * BN + c, v);
               factors(c / 16, f, fv);
+              if (c / 16 == open) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                g = fmaxf(g, __fsub_rn(__fmul_rn(v[i], f), ref) + log2_above(c / 16 == open ? m.rv[i] : fv));
+                for (int i = 0; i < 16; ++i) g = fmaxf(g, __fsub_rn(__fmul_rn(v[i], f), ref) + log2_above(m.rv[i]));
+              } else {
+                float b = v[0];
+#pragma unroll
+                for (int i = 1; i < 16; ++i) b = fmaxf(b, v[i]);
+                g = fmaxf(g, __fsub_rn(__fmul_rn(b, f), ref) + log2_above(fv));
+              }
             }
             sm.top[half][row] = g;
             named_barrier(1 + sub, 64);
@@ -1042,19 +1049,23 @@ __device__ __forceinline__ void row_role(const Params& p, Small& sm, uint8_t* q,
             // (bounded for blocks out of view, whose weights are 0; in view what it bounds has weights below 2^-86)
             auto bounded = [](float x) { return x > 0x1p100f ? 0x1p100f : x; };  // NaN stays
             fv = bounded(fv * up);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = ex2(__fsub_rn(__fmul_rn(v[i], f), ref));  // (a packed pair is contracted)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum2 = add2(sum2, pack2(v[2 * i], v[2 * i + 1]));
+            if (c / 16 == open) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] *= bounded(m.rv[i] * up);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) unpack2(mul2(pack2(v[2 * i], v[2 * i + 1]), pack2(fv, fv)), v[2 * i], v[2 * i + 1]);
+            }
             uint32_t pr[16];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              float x[2], w[2], h[2];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                x[k] = ex2(__fsub_rn(__fmul_rn(v[2 * i + k], f), ref));
-                w[k] = x[k] * (c / 16 == open ? bounded(m.rv[2 * i + k] * up) : fv);
-                h[k] = trunc11(w[k]);
-              }
-              sum2 = add2(sum2, pack2(x[0], x[1]));
-              pr[i] = half2_bits(h[0], h[1]);
-              pr[8 + i] = half2_bits(w[0] - h[0], w[1] - h[1]);
+              const float h0 = trunc11(v[2 * i]), h1 = trunc11(v[2 * i + 1]);
+              pr[i] = half2_bits(h0, h1);
+              pr[8 + i] = half2_bits(v[2 * i] - h0, v[2 * i + 1] - h1);
             }
             tmem_st16(scores + buf * BN + c, pr);
           }
