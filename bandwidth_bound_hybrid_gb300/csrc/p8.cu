@@ -248,7 +248,7 @@ struct alignas(16) Small {
   int m;                           // most tiles of a range; 0: spans
   int q, rem, near;
   int unit, unit_end;              // this CTA's units
-  int b, g, first, end, tile0, ntile, next;  // the item and this CTA's range of it
+  int b, g, tile0, ntile, next;    // the item and this CTA's range of it
   int c_lo, np, slot0;             // the CTAs that share the item
 };
 
@@ -466,8 +466,6 @@ __device__ __forceinline__ void set_range(const Params& p, Small& sm, int t) {
   if ((threadIdx.x & 31) == 0) {
     sm.b = it.b;
     sm.g = it.g;
-    sm.first = it.first;
-    sm.end = it.end;
     if (sm.m) {
       const int len = (unsigned)n / (unsigned)parts, more = n - len * parts;
       sm.tile0 = k * len + min(k, more);
