@@ -34,7 +34,9 @@
 // Measured (4 kv heads x 128, 16 query heads): 8 sequences of 120k-131k rows in
 // 170 to 180 us, 5.7 to 6.05 TB/s of a measured copy's 6.8, with 63% of the issue
 // slots taken (widening: 5 operations for 4 codes); one of 4096 rows in 11.5 us,
-// a chain of latencies.
+// a chain of latencies.  Registers spill: at head dim 256 (255 of them) 172 to
+// 200 bytes, 424 with 8 heads a kv head; at 128 (128, for two CTAs an SM) 136 to
+// 164; at 64 16 to 24.
 #include "p8_dev.cuh"
 
 namespace hy {

@@ -37,16 +37,18 @@
 // equal span.  A tile that several CTAs share leaves partials (outputs, maximum,
 // sum) in the workspace, joined by a second small kernel.
 //
-// Bound by issue: 2048 rows of 4 x 128 with 16 heads at position 4096 take 197
-// us, 435 TFLOP/s of the two products (twice that is executed, 45% of the
-// measured bf16 rate).  A step of 128 x 128 takes 5400 cycles, of which the
-// products need 2048: a scheduler issues 3000 instructions for it (two row warps
-// 750 each, a widening warp 630, waits), at 55% of its cycles; the widening of
-// K and V (4800 cycles in one warp a scheduler) is the longest chain.
-// Measured and not kept: 8 widening warps (198 us, the row warps with 160
-// registers), tiles of 256 rows that share the widened codes (219), loads of the
-// codes in registers instead of the ring (407), a thread's 64 scores unrolled
-// (387: the roles' code then misses the instruction cache).
+// Bound by a chain, the widening of K and V: 2048 rows of 4 x 128 with 16 heads at
+// position 4096 take 200 us, 429 TFLOP/s of the two products (twice that is
+// executed, 44% of the measured bf16 rate); of 2 x 256 397 us (432), of 4 x 64
+// 150 (286: half the products, but as many scores).  A step of 128 x 128 takes
+// 5450 cycles, of which the products need 2048 and the widening 4800 in one warp
+// a scheduler; a scheduler issues 3050 instructions for it (two row warps 750
+// each, a widening warp 630, waits), in 54% of its cycles.  One row over 30k
+// positions takes 45.6 us: a step costs what 128 query vectors cost.
+// Measured and not kept, against 197 us then: 8 widening warps (198, the row warps
+// with 160 registers), tiles of 256 rows that share the widened codes (219), loads
+// of the codes in registers instead of the ring (407), a thread's 64 scores
+// unrolled (387: the roles' code then misses the instruction cache).
 #include <climits>
 
 #include "p8_dev.cuh"

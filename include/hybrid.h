@@ -525,9 +525,11 @@ int hy_op_kv_append_q4(const float* y_dev, int32_t ldy, int32_t n, void* Kq_dev,
  * |x| over the block's 16 hd values, s = a / 127, c = round-half-even(x * (127
  * / a)) clamped to [-127, 127]; a < 2^-100: s = 0 and c = 0; a NaN in the block:
  * s = NaN and c = 0.  The rows of a sequence's last, open block stay bf16 in
- * its tail until the block closes, so what is held never depends on how the
- * rows were cut into calls.  Closed blocks lie in pages of page_tokens rows of
- * all kv heads.
+ * its tail until the block closes, so what is held after a call never depends
+ * on how the rows were cut into calls.  (What a row is attended to with does: a
+ * block that closes within a prompt call serves all of the call's rows by its
+ * codes, a decode step by the bf16 rows before it closes.)  Closed blocks lie in
+ * pages of page_tokens rows of all kv heads.
  * Sequence b (0-based in the call) has the pages table_dev[b][0..max_pages),
  * of which only those that a call reads or writes need be valid: the others
  * may hold anything (a page whose rows have left the window and are no sinks
@@ -576,10 +578,14 @@ int hy_op_kv_append_p8(const float* y_dev, int32_t ldy, int32_t n, int32_t batch
  * the positions they were rotated for).  o_dev [batch][ldo] FP32.
  * kv_new_dev (nullable) [batch][2][nkv][hd].  A sequence whose T is negative or
  * at or past its capacity is left as it was, its o and kv_new unwritten
- * (HY_GUARD_BAD_POSITION); the others run.  Scores, softmax and sums are FP32;
+ * (HY_GUARD_BAD_POSITION); the others run.  Scores, softmax and sums are FP32
+ * (a block's products are summed in the tensor cores, which truncate);
  * queries and probabilities enter the products with 22 bits, with an absolute
  * error of 2^-34 of the head's largest |q| and 2^-39 of its largest
- * probability.  The work is shared over the GPU by rows in view.
+ * probability; the open block's K and V in view enter with an absolute error of
+ * 2^-39 of the largest |K| and |V| among them.  V is summed with weights of up
+ * to 1 and divided at the end: the sums overflow where positions in view times
+ * |V| pass 2^127.  The work is shared over the GPU by rows in view.
  * HY_ERR_UNSUPPORTED, with nothing launched, where batch * nkv * blocks is above
  * 2^30, blocks being those of the capacity or, with a window, at most window / 16
  * + 2 and the sinks' (rounded up).
@@ -596,19 +602,23 @@ int hy_op_attention_p8(const float* y_dev, int32_t ldy, int32_t batch, const hy_
  * hy_op_kv_append_p8 has just appended (the same y_dev, row_start_dev and
  * len_dev, lengths before the append).  Row i of sequence b, at position t =
  * len_dev[b] + i, attends to the rows u <= t with u < sinks or u > t - window, as
- * held after the append (a row whose block has closed since then by its codes).
+ * held after the append.  So a row sees its own block, once later rows of the
+ * call have closed it, by codes whose scale those rows took part in: outputs
+ * depend on how a prompt is cut into calls by the format's rounding (1/254 of a
+ * block's largest |x|), where the cache does not.
  * o_dev [n][ldo] FP32; rows of o past row_start_dev[batch], and those of a
- * sequence that the append refuses, stay as they are.  Precision as for
- * hy_op_attention_p8, but that a probability p enters with the scale s of its
- * block of V: their product has 22 bits, with an absolute error of 2^-34 of the
- * larger of s times the row's largest p and the largest product p s among the
- * blocks of which the row sees some position; an open block's row counts as a
- * block, and its K and V enter with an absolute error of 2^-30 (K) and 2^-27 (V)
- * of the row's largest.  What a row does not see takes nothing from it.
- * workspace_dev: hy_op_attention_p8_prompt_workspace()
- * bytes, 16-byte aligned, no zeroing needed, its contents meaningless between
- * calls; calls that can overlap on the GPU need one each.  [Strata] "Act 1"
- * (one launch per layer for all prompt tokens).
+ * sequence that the append refuses, stay as they are.
+ * Precision as for hy_op_attention_p8, but for V: a probability p enters with
+ * the scale s of its block of V.  Their product has 22 bits, with an absolute
+ * error of 2^-34 of the larger of s times the row's largest p and the largest
+ * product p s among the blocks of which the row sees some position, at any
+ * sizes of what it does not see.  A row of the open block counts as a block
+ * (s = its largest |V| / 127); its K and V enter with an absolute error of 2^-30
+ * (K) and 2^-27 (V) of the row's largest.
+ * workspace_dev: hy_op_attention_p8_prompt_workspace() bytes, 16-byte aligned,
+ * no zeroing needed, its contents meaningless between calls; calls that can
+ * overlap on the GPU need one each.  [Strata] "Act 1" (one launch per layer for
+ * all prompt tokens).
  * HY_ERR_UNSUPPORTED, with nothing launched, where (n nq / (128 nkv) + batch) *
  * (positions in view / 64 + 2) * nkv is above 2^31. */
 size_t hy_op_attention_p8_prompt_workspace(int32_t n, int32_t batch, int32_t nq, int32_t nkv, int32_t hd);
